@@ -372,6 +372,117 @@ ql_status qlinear_gemm_noalloc(const ql_desc *desc, const ql_packed_const *w,
                                const void *x, int64_t M, void *y,
                                ql_stream_t stream);
 
+/* ---- Gated feed-forward block, 8-bit checkpoints and input gradients -------
+ *
+ * A gated block multiplies by two layers of one format and K and combines
+ * them: h = act(g) * u, g = x . Wg^T, u = x . Wu^T.  Both are one packed
+ * layer here, rows 0 .. F-1 the gate, rows F .. 2F-1 the up projection
+ * (N = 2F): the stack that qlinear_concat_n makes.  The weights are frozen
+ * codes, so the backward pass has input gradients only. */
+
+typedef enum {
+  QL_ACT_SILU = 0,      /* a / (1 + e^-a)                                        */
+  QL_ACT_GELU_TANH = 1, /* a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2       */
+  QL_ACT_GELU = 2       /* a (1 + erf(a / sqrt(2))) / 2                          */
+} ql_act;
+
+/* A matrix of `rows` x `cols` activations held in 8 bits (device pointers,
+ * caller-owned, 16-byte aligned): with cp = cols rounded up to 16,
+ *   codes i8 [rows][cp]     (columns cols .. cp-1 hold 0)
+ *   exps  u8 [rows][cp/16]  one exponent E for each 16 values along a row
+ *   value = code * 2^(E - 127), exact in bfloat16.
+ * E is the smallest (at least 1) for which the group's largest magnitude v has
+ * rint(v * 2^(127 - E)) <= 127, and code = rint(value * 2^(127 - E)),
+ * nearest-even.  A group with an infinity, a NaN or a magnitude of at least
+ * 2^128 * 255/256 has E = 255, codes 0 and is restored as NaN. */
+typedef struct {
+  void *codes;
+  void *exps;
+} ql_saved8;
+
+typedef struct {
+  const void *codes;
+  const void *exps;
+} ql_saved8_const;
+
+/* Byte sizes of the two buffers (host-only, no CUDA call).
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows or cols < 1), QL_ERR_RANGE
+ * (rows * cp above 2^38). */
+ql_status qlinear_saved8_bytes(int64_t rows, int64_t cols, size_t *codes_bytes, size_t *exps_bytes);
+
+/* x bf16 [rows][cols] -> its 8-bit form (one kernel; bit-exact by the
+ * definition above).  Errors: QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_RANGE,
+ * QL_ERR_ALIGN, QL_ERR_CUDA. */
+ql_status qlinear_save8(const void *x, int64_t rows, int64_t cols, const ql_saved8 *out, ql_stream_t stream);
+
+/* The 8-bit form -> out bf16 [rows][cols] (one kernel; exact).  A gated block's
+ * checkpoint is restored with rows = 2M, cols = F: g and u of each token in
+ * turn.  Errors: as qlinear_save8. */
+ql_status qlinear_restore8(const ql_saved8_const *in, int64_t rows, int64_t cols, void *out, ql_stream_t stream);
+
+/* Bytes of caller-provided device workspace qlinear_gated needs, with or
+ * without a checkpoint (host-only, no CUDA call): that of qlinear_gemm for the
+ * layer, or of qlinear_gemv where the call runs on it and that is more.
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (also: N odd or K % 64 != 0),
+ * QL_ERR_RANGE, QL_ERR_UNSUPPORTED. */
+ql_status qlinear_gated_workspace_bytes(const ql_desc *desc, int64_t M, size_t *bytes);
+
+/* h[M][F] (bf16) = act(g) * u, x bf16 [M][K], any M >= 1, K % 64 == 0, N = 2F.
+ * g and u are the accumulators of qlinear_gemv / qlinear_gemm; activation and
+ * product are taken in fp32 from them, with one rounding to bf16.  Decode
+ * (M <= 8; affine with group 32 or 64 and K % 256 == 0: M <= 32) runs on the
+ * GEMV kernels, each CTA streaming the gate and up rows of the same features;
+ * everything else, and every call with a checkpoint, on the tcgen05 GEMM, whose
+ * tiles are 64 gate rows and the same features' 64 up rows.
+ * x is finite: an infinity or a NaN in a token spoils that token's h in the
+ * GEMM form and gives an unspecified h for it in the decode forms (whose x is
+ * fixed point, as qlinear_gemv's); other tokens are not affected.
+ * `saved` (may be NULL): where the 8-bit form of (g, u) goes for
+ * qlinear_gated_backward, rows 2m and 2m+1 of a [2M][F] matrix being g and u of
+ * token m (qlinear_saved8_bytes(2M, F)); rounded from the fp32 accumulators.
+ * `workspace`: at least qlinear_gated_workspace_bytes(), 256-byte aligned,
+ * overwritten; calls sharing one must not overlap on the GPU.  h must not
+ * overlap x.
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (also: workspace too small), QL_ERR_ALIGN,
+ * QL_ERR_RANGE, QL_ERR_UNSUPPORTED (format, activation or device),
+ * QL_ERR_CUDA. */
+ql_status qlinear_gated(const ql_desc *desc, const ql_packed_const *w, const void *x, int64_t M, int32_t act,
+                        void *h, const ql_saved8 *saved, void *workspace, size_t workspace_bytes,
+                        ql_stream_t stream);
+
+/* Bytes of caller-provided device workspace qlinear_gemm_dx and
+ * qlinear_gated_backward need (host-only, no CUDA call): with Np = N rounded up
+ * to 64 and r = 32 (affine: the group), the sum of 2*M*Np (dy in fp16), 4*M,
+ * Np, 4*(K/r)*Np (scaled metadata), each rounded up to 256, and 148 * 1024 * T
+ * (partial sums), T = 32 tokens up to M = 32, else 256.
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_RANGE, QL_ERR_UNSUPPORTED. */
+ql_status qlinear_gemm_dx_workspace_bytes(const ql_desc *desc, int64_t M, size_t *bytes);
+
+/* Input gradient of the layer: dx[M][K] (bf16) = dy[M][N] (bf16) . W, any
+ * M >= 1 and every N and K of the format.  On the tcgen05 tensor cores, the
+ * dequantisation fused: each dy row is scaled to fp16 against the power-of-two
+ * scales that the weight rows get (as qlinear_gemm's operands, rounded once
+ * each), fp32 accumulation, one rounding to bf16.  Results do not depend on
+ * timing (split sums are added in a fixed order).
+ * `workspace`: at least qlinear_gemm_dx_workspace_bytes(), 256-byte aligned,
+ * overwritten; calls sharing one must not overlap on the GPU.  dx must not
+ * overlap dy.
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (also: workspace too small), QL_ERR_ALIGN,
+ * QL_ERR_RANGE, QL_ERR_UNSUPPORTED (format or device), QL_ERR_CUDA. */
+ql_status qlinear_gemm_dx(const ql_desc *desc, const ql_packed_const *w, const void *dy, int64_t M, void *dx,
+                          void *workspace, size_t workspace_bytes, ql_stream_t stream);
+
+/* Backward pass of qlinear_gated from its checkpoint: with g and u the restored
+ * values and dh bf16 [M][F] the gradient of h,
+ *   dg = dh * u * act'(g),  du = dh * act(g),  dx[M][K] (bf16) = dg . Wg + du . Wu.
+ * dg and du are taken in fp32 and enter the product as scaled fp16, as dy in
+ * qlinear_gemm_dx.  `dgu` (may be NULL): bf16 [M][2F], (dg | du) per token, for
+ * adapters beside the frozen projections.  Workspace: that of qlinear_gemm_dx.
+ * dx and dgu must not overlap the inputs.  Errors: as qlinear_gated. */
+ql_status qlinear_gated_backward(const ql_desc *desc, const ql_packed_const *w, const ql_saved8_const *saved,
+                                 const void *dh, int64_t M, int32_t act, void *dgu, void *dx, void *workspace,
+                                 size_t workspace_bytes, ql_stream_t stream);
+
 /* Synchronise `stream`, then read and clear the current device's status
  * word: QL_ERR_TIMEOUT if a kernel's bounded wait gave up since the last
  * call, QL_ERR_RANGE if qlinear_quantize_meta met an input outside its

@@ -19,6 +19,7 @@ QL_OK, QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_ALIGN, QL_ERR_RANGE, QL_ERR_UNSUPPORTED
     QL_ERR_TIMEOUT = range(8)
 FORMATS = {"int4": 1, "int6": 2, "affine": 3, "int6p": 4}  # int6p: int6 codes in planar storage
 QL_OUT_F32, QL_OUT_BF16 = 0, 1
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1, "gelu": 2}
 
 
 class QLinearError(RuntimeError):
@@ -45,6 +46,13 @@ class ql_unpacked(C.Structure):
 
 
 ql_unpacked_out = ql_unpacked
+
+
+class ql_saved8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("exps", C.c_void_p)]
+
+
+ql_saved8_const = ql_saved8
 
 _lib = None
 
@@ -75,6 +83,18 @@ _SIGNATURES = {
                           C.POINTER(ql_packed), C.c_void_p], C.c_int),
     "qlinear_quantize_meta": ([C.POINTER(ql_desc), C.c_void_p, C.c_void_p, C.POINTER(ql_unpacked), C.c_void_p],
                               C.c_int),
+    "qlinear_saved8_bytes": ([C.c_int64, C.c_int64, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)], C.c_int),
+    "qlinear_save8": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(ql_saved8), C.c_void_p], C.c_int),
+    "qlinear_restore8": ([C.POINTER(ql_saved8), C.c_int64, C.c_int64, C.c_void_p, C.c_void_p], C.c_int),
+    "qlinear_gated_workspace_bytes": ([C.POINTER(ql_desc), C.c_int64, C.POINTER(C.c_size_t)], C.c_int),
+    "qlinear_gated": ([C.POINTER(ql_desc), C.POINTER(ql_packed), C.c_void_p, C.c_int64, C.c_int32, C.c_void_p,
+                       C.POINTER(ql_saved8), C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
+    "qlinear_gemm_dx_workspace_bytes": ([C.POINTER(ql_desc), C.c_int64, C.POINTER(C.c_size_t)], C.c_int),
+    "qlinear_gemm_dx": ([C.POINTER(ql_desc), C.POINTER(ql_packed), C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                         C.c_size_t, C.c_void_p], C.c_int),
+    "qlinear_gated_backward": ([C.POINTER(ql_desc), C.POINTER(ql_packed), C.POINTER(ql_saved8), C.c_void_p,
+                                C.c_int64, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p],
+                               C.c_int),
 }
 
 
@@ -265,6 +285,196 @@ def qlinear_gemm_noalloc(desc: Desc, codes, gmeta, steps, x, M: int, y, stream=N
     w = ql_packed(_ptr(codes), _ptr(gmeta), _ptr(steps))
     _check(lib().qlinear_gemm_noalloc(C.byref(d), C.byref(w), _ptr(x), M, _ptr(y), _stream(stream)),
            "qlinear_gemm_noalloc")
+
+
+# ---- gated feed-forward block, 8-bit checkpoints, input gradients ------------------------------------------
+# These calls check their tensors before the library sees a pointer: contiguous CUDA tensors of one device, of
+# the type and at least the size that the call reads or writes.  They run on that device (also when it is not
+# the current one), on its current stream or on `stream`.
+
+def _need(where: str, t, dtype, numel: int, dev=None):
+    """Check one tensor and return its device."""
+    if not t.is_cuda or (dev is not None and t.device != dev):
+        raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: tensors must be on one CUDA device")
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
+        raise QLinearError(QL_ERR_SHAPE, f"{where}: expected a contiguous {dtype} tensor of at least {numel} "
+                                         f"elements, got {t.dtype} of shape {tuple(t.shape)}")
+    return t.device
+
+
+def _need_bytes(where: str, t, nbytes: int, dev):
+    if not t.is_cuda or t.device != dev:
+        raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: tensors must be on one CUDA device")
+    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise QLinearError(QL_ERR_SHAPE, f"{where}: expected a contiguous buffer of at least {nbytes} bytes")
+
+
+def _need_packed(where: str, desc: Desc, packed, dev):
+    for t, n in zip(packed, qlinear_packed_bytes(desc)):
+        if n:
+            if t is None:
+                raise QLinearError(QL_ERR_NULL, where)
+            _need_bytes(where, t, n, dev)
+
+
+def _activation(where: str, act: str) -> int:
+    a = ACTIVATIONS.get(act)
+    if a is None:
+        raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: unknown activation {act!r}")
+    return a
+
+
+def _workspace(workspace, nbytes: int, dev, stream, where: str):
+    """The caller's workspace, checked, or one from the pool that torch's allocator keeps for the call's stream (so
+    that it is handed on only to work behind this call's)."""
+    import torch
+    if workspace is not None:
+        _need_bytes(where, workspace, nbytes, dev)
+        return workspace
+    with torch.cuda.stream(stream):  # None: the current one
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def _run(where: str, dev, stream, name: str, *args):
+    import torch
+    if stream is not None and stream.device != dev:
+        raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: the stream belongs to another device than the tensors")
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        _check(f(*args, C.c_void_p(s.cuda_stream)), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, C.c_void_p(s.cuda_stream)), where)
+
+
+def _bytes2(name: str, *args):
+    a, b = C.c_size_t(), C.c_size_t()
+    _check(getattr(lib(), name)(*args, C.byref(a), C.byref(b)), name)
+    return a.value, b.value
+
+
+def _bytes_for(name: str, desc: Desc, M: int) -> int:
+    d, n = desc.c(), C.c_size_t()
+    _check(getattr(lib(), name)(C.byref(d), M, C.byref(n)), name)
+    return n.value
+
+
+def qlinear_saved8_bytes(rows: int, cols: int):
+    """Bytes of (codes, exps) of a [rows][cols] matrix in 8 bits."""
+    return _bytes2("qlinear_saved8_bytes", rows, cols)
+
+
+def alloc_saved8(rows: int, cols: int, device="cuda"):
+    """Allocate (uninitialised) buffers of a [rows][cols] matrix in 8 bits: codes int8 [rows][cols rounded up to
+    16] and exps uint8 [rows][that / 16].  A gated block's checkpoint has rows = 2 M, cols = F."""
+    import torch
+    c, e = qlinear_saved8_bytes(rows, cols)
+    return (torch.empty((rows, c // rows), dtype=torch.int8, device=device),
+            torch.empty((rows, e // rows), dtype=torch.uint8, device=device))
+
+
+def _need_saved8(where: str, saved, rows: int, cols: int, dev) -> ql_saved8:
+    import torch
+    c, e = qlinear_saved8_bytes(rows, cols)
+    _need(where, saved[0], torch.int8, c, dev)
+    _need(where, saved[1], torch.uint8, e, dev)
+    return ql_saved8(saved[0].data_ptr(), saved[1].data_ptr())
+
+
+def qlinear_save8(x, rows: int, cols: int, saved, stream=None):
+    """bf16 [rows][cols] -> its 8-bit form in ``saved`` = (codes, exps) of alloc_saved8()."""
+    import torch
+    w = "qlinear_save8"
+    dev = _need(w, x, torch.bfloat16, rows * cols)
+    s = _need_saved8(w, saved, rows, cols, dev)
+    _run(w, dev, stream, w, _ptr(x), rows, cols, C.byref(s))
+
+
+def qlinear_restore8(saved, rows: int, cols: int, out, stream=None):
+    """The 8-bit form -> bf16 [rows][cols]."""
+    import torch
+    w = "qlinear_restore8"
+    dev = _need(w, out, torch.bfloat16, rows * cols)
+    s = _need_saved8(w, saved, rows, cols, dev)
+    _run(w, dev, stream, w, C.byref(s), rows, cols, _ptr(out))
+
+
+def qlinear_gated_workspace_bytes(desc: Desc, M: int) -> int:
+    return _bytes_for("qlinear_gated_workspace_bytes", desc, M)
+
+
+def alloc_gated_workspace(desc: Desc, M: int, device="cuda"):
+    import torch
+    return torch.empty(qlinear_gated_workspace_bytes(desc, M), dtype=torch.uint8, device=device)
+
+
+def qlinear_gated(desc: Desc, codes, gmeta, steps, x, M: int, act: str, h, saved=None, workspace=None, stream=None):
+    """h[M][F] = act(x Wg^T) * (x Wu^T) for a packed layer of F gate rows and then F up rows (desc.N = 2 F, as
+    qlinear_concat_n stacks them).  ``act``: a key of ACTIVATIONS.  ``saved``: alloc_saved8(2 * M, F), where the
+    8-bit checkpoint for qlinear_gated_backward goes.  ``workspace``: a uint8 CUDA tensor of at least
+    qlinear_gated_workspace_bytes(desc, M) bytes; allocated here when omitted."""
+    import torch
+    w = "qlinear_gated"
+    need = qlinear_gated_workspace_bytes(desc, M)
+    a = _activation(w, act)
+    F = desc.N // 2
+    dev = _need(w, x, torch.bfloat16, M * desc.K)
+    _need(w, h, torch.bfloat16, M * F, dev)
+    _need_packed(w, desc, (codes, gmeta, steps), dev)
+    s = None if saved is None else C.byref(_need_saved8(w, saved, 2 * M, F, dev))
+    workspace = _workspace(workspace, need, dev, stream, w)
+    d, p = desc.c(), ql_packed(_ptr(codes), _ptr(gmeta), _ptr(steps))
+    _run(w, dev, stream, w, C.byref(d), C.byref(p), _ptr(x), M, a, _ptr(h), s, _ptr(workspace),
+         workspace.numel() * workspace.element_size())
+
+
+def qlinear_gemm_dx_workspace_bytes(desc: Desc, M: int) -> int:
+    return _bytes_for("qlinear_gemm_dx_workspace_bytes", desc, M)
+
+
+def alloc_gemm_dx_workspace(desc: Desc, M: int, device="cuda"):
+    """Workspace of qlinear_gemm_dx and qlinear_gated_backward."""
+    import torch
+    return torch.empty(qlinear_gemm_dx_workspace_bytes(desc, M), dtype=torch.uint8, device=device)
+
+
+def qlinear_gemm_dx(desc: Desc, codes, gmeta, steps, dy, M: int, dx, workspace=None, stream=None):
+    """dx[M][K] = dy[M][N] W: the input gradient of the layer.  ``workspace``: a uint8 CUDA tensor of at least
+    qlinear_gemm_dx_workspace_bytes(desc, M) bytes; allocated here when omitted."""
+    import torch
+    w = "qlinear_gemm_dx"
+    need = qlinear_gemm_dx_workspace_bytes(desc, M)
+    dev = _need(w, dy, torch.bfloat16, M * desc.N)
+    _need(w, dx, torch.bfloat16, M * desc.K, dev)
+    _need_packed(w, desc, (codes, gmeta, steps), dev)
+    workspace = _workspace(workspace, need, dev, stream, w)
+    d, p = desc.c(), ql_packed(_ptr(codes), _ptr(gmeta), _ptr(steps))
+    _run(w, dev, stream, w, C.byref(d), C.byref(p), _ptr(dy), M, _ptr(dx), _ptr(workspace),
+         workspace.numel() * workspace.element_size())
+
+
+def qlinear_gated_backward(desc: Desc, codes, gmeta, steps, saved, dh, M: int, act: str, dx, dgu=None,
+                           workspace=None, stream=None):
+    """Backward pass of qlinear_gated from its checkpoint ``saved`` and the gradient dh[M][F]: dx[M][K], and
+    (dg | du) in ``dgu`` [M][2 F] when given.  ``workspace``: as qlinear_gemm_dx."""
+    import torch
+    w = "qlinear_gated_backward"
+    need = qlinear_gemm_dx_workspace_bytes(desc, M)
+    a = _activation(w, act)
+    F = desc.N // 2
+    if F < 1:
+        raise QLinearError(QL_ERR_SHAPE, w)
+    dev = _need(w, dh, torch.bfloat16, M * F)
+    _need(w, dx, torch.bfloat16, M * desc.K, dev)
+    if dgu is not None:
+        _need(w, dgu, torch.bfloat16, M * desc.N, dev)
+    _need_packed(w, desc, (codes, gmeta, steps), dev)
+    s = _need_saved8(w, saved, 2 * M, F, dev)
+    workspace = _workspace(workspace, need, dev, stream, w)
+    d, p = desc.c(), ql_packed(_ptr(codes), _ptr(gmeta), _ptr(steps))
+    _run(w, dev, stream, w, C.byref(d), C.byref(p), C.byref(s), _ptr(dh), M, a, _ptr(dgu), _ptr(dx),
+         _ptr(workspace), workspace.numel() * workspace.element_size())
 
 
 def qlinear_set_withhold_copies(on: bool) -> None:

@@ -1,0 +1,801 @@
+// gemm_dx.cuh -- the input gradient of a quantized layer on the 5th-generation tensor core.
+//
+//   dx[M][K] = dy[M][N] . W[N][K],  dy bf16 (or the gated block's (dg | du)), W quantized, dx bf16
+//
+// The contraction runs over the weight rows n, along which the packed codes are strided, so the weight
+// tile is wanted transposed: D[128 k][TT tokens] += W^T[128 k][64 n] x dy^T.  The dequantisers decode whole
+// 32-weight runs of a row as in the forward kernels and store them as rows of an M-major (transposed) A
+// operand in shared memory; the tensor core does the transposition.
+//
+// Operands are fp16 with exact power-of-two scales, as in the forward GEMM (gemm_prep.cuh).  A weight row's
+// scale 2^b_n cannot be undone after a sum over rows, so its inverse goes into the other operand:
+//     dx[m][k] = 2^-a_m sum_n (dy[m][n] 2^(a_m - b_n)) (w[n][k] 2^b_n),
+// with a_m chosen so that the row's largest scaled magnitude lies in [2^14, 2^15).
+//
+// Passes: (1) row exponents b_n and the scaled group metadata, transposed so that a stage's words are one
+// TMA box; (2) dy to scaled fp16 rows; (3) the GEMM; (4) the sum of the parts of split tiles.
+//
+// A CTA an SM.  The tiles of whole waves (as many tiles as CTAs, again and again) are computed alone, all
+// CTAs moving along n together so that each code row and each dy column is fetched from memory about once
+// a wave; the tiles of the last, partial wave are cut along n into equal shares, one a CTA, whose fp32 sums
+// go to the workspace and are added in a fixed order (a full last wave costs as much as the others however
+// few tiles it has: at M = 2048, K = 5120 it would be a third wave for 24 of 148 CTAs).
+//
+// Workspace (256-byte aligned sections, Np = N rounded up to 64):
+//   dy16   fp16 [M][Np]      scaled dy, zeros past N
+//   dexp   s32  [M]          -a_m
+//   bexp   s8   [Np]         b_n
+//   meta   u32  [K / gran][Np]  scaled metadata of a run of gran weights: int4 (S, Z S) fp16 pair, int6 the
+//                            scales of its two 16-groups, affine (s, b); zeros past N
+//   partial f32 [2 DX_CTAS][TT][128]
+#pragma once
+#include "gated.cuh"
+#include "gemm_sm100.cuh"
+
+namespace ql {
+namespace dx {
+
+constexpr int BN = 64;    // weight rows a stage (the contraction)
+constexpr int BKT = 128;  // k a tile (the MMA's M)
+constexpr int DX_CTAS = 148;       // CTAs of a launch at most: the SMs of a B200
+constexpr int MIN_SHARE = 8;       // stages a share of a split tile has at least
+constexpr int TT_LARGE = 256, TT_SMALL = 32;
+
+inline int token_tile(int64_t M) { return M <= TT_SMALL ? TT_SMALL : TT_LARGE; }
+inline int64_t padded_n(int64_t N) { return (N + 63) / 64 * 64; }
+// weights a metadata word covers
+__host__ __device__ constexpr int gran(int fmt, int group) { return fmt == FMT_AFFINE ? group : 32; }
+
+struct Workspace {
+  __half *dy16;
+  int *dexp;
+  int8_t *bexp;
+  uint32_t *meta;
+  float *partial;
+};
+
+inline size_t workspace_bytes(int64_t M, int64_t N, int64_t K, int g) {
+  const size_t np = (size_t)padded_n(N);
+  return align256((size_t)M * np * 2) + align256((size_t)M * 4) + align256(np) + align256((size_t)(K / g) * np * 4) +
+         (size_t)2 * DX_CTAS * token_tile(M) * BKT * 4;
+}
+
+inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
+  const size_t np = (size_t)padded_n(N);
+  uint8_t *p = static_cast<uint8_t *>(base);
+  Workspace w;
+  w.dy16 = reinterpret_cast<__half *>(p);
+  p += align256((size_t)M * np * 2);
+  w.dexp = reinterpret_cast<int *>(p);
+  p += align256((size_t)M * 4);
+  w.bexp = reinterpret_cast<int8_t *>(p);
+  p += align256(np);
+  w.meta = reinterpret_cast<uint32_t *>(p);
+  p += align256((size_t)(K / g) * np * 4);
+  w.partial = reinterpret_cast<float *>(p);
+  return w;
+}
+
+// ---- pass 1: row exponents and transposed metadata ------------------------------------------------
+// A CTA takes 32 rows: each warp bounds four of them (as the forward's w_scale_row), then the words of 32
+// rows x 32 runs at a time are turned through shared memory, read along the row and written along n.
+constexpr int WP_ROWS = 32;
+
+template <int FMT, int BITS>
+QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t K, int G, int lane) {
+  float bound = 0.f;
+  if constexpr (FMT == FMT_INT4) {
+    const uint16_t *gm = reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32);
+    const uint32_t *st = reinterpret_cast<const uint32_t *>(steps) + n * (K / 256);
+    for (int64_t g = lane; g < K / 32; g += 32) {
+      const uint32_t s = __ldg(st + (g >> 3)), c = __ldg(gm + g);
+      const float S = (float)(c & 0xffu) * f16_bits_to_f32(s), Z = (float)(c >> 8) * f16_bits_to_f32(s >> 16);
+      bound = fmaxf(bound, fabsf(S) * fmaxf(fabsf(Z), fabsf(15.f - Z)));
+    }
+  } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
+    const int8_t *gm = reinterpret_cast<const int8_t *>(gmeta) + n * (K / 16);
+    const uint16_t *st = reinterpret_cast<const uint16_t *>(steps) + n * (K / 256);
+    for (int64_t g = lane; g < K / 16; g += 32)
+      bound = fmaxf(bound, 32.f * fabsf((float)__ldg(gm + g) * f16_bits_to_f32(__ldg(st + (g >> 4)))));
+  } else {
+    const uint32_t *gm = reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G);
+    const float qmax = (float)((1 << BITS) - 1);
+    for (int64_t g = lane; g < K / G; g += 32) {
+      const uint32_t c = __ldg(gm + g);
+      const float s = bf16_bits_to_f32(c), b = bf16_bits_to_f32(c >> 16);
+      bound = fmaxf(bound, fmaxf(fabsf(b), fabsf(fmaf(qmax, s, b))));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bound = fmaxf(bound, __shfl_xor_sync(0xffffffffu, bound, o));
+  return bound;
+}
+
+// The metadata word of run r (of gran weights) of row n, times sc = 2^b_n.
+template <int FMT>
+QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t r, int64_t K, int G,
+                             float sc) {
+  if constexpr (FMT == FMT_INT4) {
+    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32) + r);
+    const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3));
+    const float S = __fmul_rn((float)(c & 0xffu), f16_bits_to_f32(s)) * sc;
+    return pack_f16x2(S, __fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
+  } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
+    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta + n * (K / 16)) + r);
+    const float st = f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3)));
+    return pack_f16x2(__fmul_rn((float)(int8_t)c, st) * sc, __fmul_rn((float)(int8_t)(c >> 8), st) * sc);
+  } else {
+    const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G) + r);
+    return pack_f16x2(bf16_bits_to_f32(c) * sc, bf16_bits_to_f32(c >> 16) * sc);
+  }
+}
+
+template <int FMT, int BITS>
+__global__ void __launch_bounds__(256) w_prep_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N, int64_t K,
+                                                     int G, int64_t np, Workspace ws) {
+  __shared__ float scale[WP_ROWS];
+  __shared__ uint32_t turn[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS;
+  for (int i = warp; i < WP_ROWS; i += 8) {
+    const int64_t n = n0 + i;
+    int b = 0;
+    if (n < N) b = scale_exponent(meta_bound<FMT, BITS>(gmeta, steps, n, K, G, lane), 14);
+    if (lane == 0) {
+      scale[i] = exp2i(b);
+      ws.bexp[n] = (int8_t)b;
+    }
+  }
+  __syncthreads();
+  const int64_t runs = K / gran(FMT, G);
+  for (int64_t r0 = 0; r0 < runs; r0 += 32) {
+    for (int i = warp; i < WP_ROWS; i += 8) {
+      const int64_t n = n0 + i, r = r0 + lane;
+      turn[i][lane] = n < N && r < runs ? scaled_meta<FMT>(gmeta, steps, n, r, K, G, scale[i]) : 0u;
+    }
+    __syncthreads();
+    for (int i = warp; i < 32; i += 8)
+      if (r0 + i < runs) ws.meta[(r0 + i) * np + n0 + lane] = turn[lane][i];
+    __syncthreads();
+  }
+}
+
+// ---- pass 2: dy (or (dg | du)) to scaled fp16 rows ----------------------------------------------------
+constexpr int NO_EXP = -100000;  // exponent of a zero
+
+// floor(log2 |v|) for a normal v; a subnormal counts as 2^-126, and values that are not finite do not count
+// (they stay what they are under any scale)
+QL_DEVI int value_exp(float v) {
+  const int e = (int)((__float_as_uint(v) >> 23) & 0xffu);
+  return v == 0.f || e == 255 ? NO_EXP : max(e, 1) - 127;
+}
+
+// a_m from the row's largest exponent of dy 2^-b
+QL_DEVI int row_scale_exp(int emax) { return emax == NO_EXP ? 0 : 14 - emax; }
+
+// v * 2^e for results below 2^15 (so e <= 164 for any v but zero) that go to fp16 (zero there for
+// e < -252): two exact steps, the second of which may end in a subnormal
+QL_DEVI float scale_by(float v, int e) {
+  const int e1 = max(-126, min(126, e)), e2 = max(-126, min(126, e - e1));
+  return v * exp2i(e1) * exp2i(e2);
+}
+
+// The largest value of every thread's e over the CTA.
+template <int THREADS>
+QL_DEVI int block_max(int e, int *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = e;
+  __syncthreads();
+  e = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) e = max(e, red[w]);
+  return e;
+}
+
+// Eight values at element offset i of a bf16 row, the elements from `end` on as zeros.  VEC: the row's
+// elements are 16-byte aligned at every multiple of 8.
+template <bool VEC>
+QL_DEVI void load8(const __nv_bfloat16 *row, int64_t i, int64_t end, float (&v)[8]) {
+  if (VEC) {  // end is a multiple of 8
+    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(row + i));
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_bits_to_f32(u[j]);
+      v[2 * j + 1] = bf16_bits_to_f32(u[j] >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < end ? __bfloat162float(row[i + j]) : 0.f;
+  }
+}
+
+// Eight row exponents b_n from n on; those from `end` on are not used.
+template <bool VEC>
+QL_DEVI void load_bexp(const int8_t *b, int64_t n, int64_t end, int (&e)[8]) {
+  if (VEC) {
+    const uint2 q = *reinterpret_cast<const uint2 *>(b + n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      e[j] = (int)(int8_t)(q.x >> (8 * j));
+      e[4 + j] = (int)(int8_t)(q.y >> (8 * j));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = n + j < end ? (int)b[n + j] : 0;
+  }
+}
+
+template <bool VEC>
+QL_DEVI void store8_f16(__half *row, int64_t n, int64_t end, const float (&v)[8], const int (&e)[8], int a) {
+  if (VEC) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = pack_f16x2(scale_by(v[2 * j], a - e[2 * j]), scale_by(v[2 * j + 1], a - e[2 * j + 1]));
+    *reinterpret_cast<uint4 *>(row + n) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < end) row[n + j] = __float2half_rn(scale_by(v[j], a - e[j]));
+  }
+}
+
+QL_DEVI int max_exp8(const float (&v)[8], const int (&e)[8], int m) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int x = value_exp(v[j]);
+    if (x != NO_EXP) m = max(m, x - e[j]);
+  }
+  return m;
+}
+
+constexpr int DY_THREADS = 256;
+
+// One CTA a token row.
+template <bool VEC>
+__global__ void __launch_bounds__(DY_THREADS) dy_prep_kernel(const __nv_bfloat16 *dy, int64_t N, int64_t np,
+                                                             Workspace ws) {
+  __shared__ int red[DY_THREADS / 32];
+  const int64_t m = blockIdx.x;
+  const __nv_bfloat16 *row = dy + m * N;
+  __half *out = ws.dy16 + m * np;
+  int emax = NO_EXP;
+  for (int64_t i = 8 * threadIdx.x; i < N; i += 8 * DY_THREADS) {
+    float v[8];
+    int e[8];
+    load8<VEC>(row, i, N, v);
+    load_bexp<true>(ws.bexp, i, N, e);
+    emax = max_exp8(v, e, emax);
+  }
+  const int a = row_scale_exp(block_max<DY_THREADS>(emax, red));
+  for (int64_t i = 8 * threadIdx.x; i < np; i += 8 * DY_THREADS) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    int e[8];
+    if (i < N) load8<VEC>(row, i, N, v);
+    load_bexp<true>(ws.bexp, i, np, e);
+    store8_f16<true>(out, i, np, v, e, a);
+  }
+  if (threadIdx.x == 0) ws.dexp[m] = -a;
+}
+
+struct GatedGrad {
+  const int8_t *codes;   // checkpoint of (g, u)
+  const uint8_t *exps;
+  const __nv_bfloat16 *dh;  // [M][F]
+  __nv_bfloat16 *dgu;       // [M][2F] or NULL
+  int64_t F, np;
+  int act;
+};
+
+// dg and du of eight features from f on (f a multiple of 8, below F; those from F on are zeros).
+template <bool VEC>
+QL_DEVI void gated_grad8(const GatedGrad &p, int64_t m, int64_t f, float (&dg)[8], float (&du)[8]) {
+  const int64_t fp = save8_cols(p.F);
+  float dh[8];
+  load8<VEC>(p.dh + m * p.F, f, p.F, dh);
+  const int8_t *codes = p.codes + 2 * m * fp + f;
+  const uint8_t *exps = p.exps + 2 * m * (fp / 16) + (f >> 4);
+  const uint2 cg = __ldg(reinterpret_cast<const uint2 *>(codes)), cu = __ldg(reinterpret_cast<const uint2 *>(codes + fp));
+  const float sg = save8_scale(__ldg(exps)), su = save8_scale(__ldg(exps + fp / 16));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float g = (float)(int8_t)((j < 4 ? cg.x : cg.y) >> (8 * (j & 3))) * sg;
+    const float u = (float)(int8_t)((j < 4 ? cu.x : cu.y) >> (8 * (j & 3))) * su;
+    float a, d;
+    act_grad(p.act, g, a, d);
+    dg[j] = f + j < p.F ? dh[j] * u * d : 0.f;
+    du[j] = f + j < p.F ? dh[j] * a : 0.f;
+  }
+}
+
+constexpr int DGU_THREADS = 512;
+
+template <bool VEC>
+__global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Workspace ws) {
+  __shared__ int red[DGU_THREADS / 32];
+  const int64_t m = blockIdx.x, N = 2 * p.F;
+  int emax = NO_EXP;
+  for (int64_t f = 8 * threadIdx.x; f < p.F; f += 8 * DGU_THREADS) {
+    float dg[8], du[8];
+    int e[8];
+    gated_grad8<VEC>(p, m, f, dg, du);
+    load_bexp<true>(ws.bexp, f, N, e);
+    emax = max_exp8(dg, e, emax);
+    load_bexp<VEC>(ws.bexp, p.F + f, N, e);
+    emax = max_exp8(du, e, emax);
+  }
+  const int a = row_scale_exp(block_max<DGU_THREADS>(emax, red));
+  __half *out = ws.dy16 + m * p.np;
+  for (int64_t f = 8 * threadIdx.x; f < p.F; f += 8 * DGU_THREADS) {
+    float dg[8], du[8];
+    int e[8];
+    gated_grad8<VEC>(p, m, f, dg, du);
+    load_bexp<true>(ws.bexp, f, N, e);
+    store8_f16<VEC>(out, f, p.F, dg, e, a);
+    load_bexp<VEC>(ws.bexp, p.F + f, N, e);
+    store8_f16<VEC>(out + p.F, f, p.F, du, e, a);
+    if (p.dgu) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (f + j < p.F) {
+          p.dgu[m * N + f + j] = __float2bfloat16_rn(dg[j]);
+          p.dgu[m * N + p.F + f + j] = __float2bfloat16_rn(du[j]);
+        }
+    }
+  }
+  for (int64_t n = N + threadIdx.x; n < p.np; n += DGU_THREADS) out[n] = __float2half_rn(0.f);
+  if (threadIdx.x == 0) ws.dexp[m] = -a;
+}
+
+// ---- pass 3: the GEMM ------------------------------------------------------------------------------
+constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, WARP_DEQ0 = 8;
+__host__ __device__ constexpr int deq_groups(int tt) { return tt == TT_LARGE ? 2 : 4; }
+__host__ __device__ constexpr int num_threads(int tt) { return (WARP_DEQ0 + 4 * deq_groups(tt)) * 32; }
+
+// A stage: the transposed weight tile (A), the dy tile (B), the packed codes and the metadata words.
+__host__ __device__ constexpr int code_row(int fmt, int bits) { return BKT * gemm::code_bits(fmt, bits) / 8; }
+constexpr int A_BYTES = BN * BKT * 2;
+__host__ __device__ constexpr int b_bytes(int tt) { return tt * BN * 2; }
+__host__ __device__ constexpr int p_bytes(int fmt, int bits) { return BN * code_row(fmt, bits); }
+constexpr int META_BYTES = BN * 4 * 4;  // up to four runs of 32 k
+__host__ __device__ constexpr int stage_bytes(int fmt, int bits, int tt) {
+  return A_BYTES + b_bytes(tt) + p_bytes(fmt, bits) + META_BYTES;
+}
+__host__ __device__ constexpr int smem_need(int fmt, int bits, int tt, int st) {
+  return st * stage_bytes(fmt, bits, tt) + (3 * st + 5) * 8 + 16 + 1024;
+}
+__host__ __device__ constexpr int stages(int fmt, int bits, int tt) {
+  return smem_need(fmt, bits, tt, 6) <= gemm::SMEM_LIMIT ? 6
+       : smem_need(fmt, bits, tt, 5) <= gemm::SMEM_LIMIT ? 5
+       : smem_need(fmt, bits, tt, 4) <= gemm::SMEM_LIMIT ? 4 : 3;
+}
+__host__ __device__ constexpr int smem_bytes(int fmt, int bits, int tt) {
+  return smem_need(fmt, bits, tt, stages(fmt, bits, tt));
+}
+
+// How the tiles are dealt: `waves` whole waves of `ctas` tiles, then the `rest` tiles that are left, their
+// rest * steps stages cut into `shares` equal ranges, one a CTA.
+struct Deal {
+  int64_t m_tiles, k_tiles;
+  int steps;  // stages a tile: Np / 64
+  int ctas, waves, rest, shares;
+  __host__ __device__ bool joins() const { return shares != rest; }  // else a share is a whole tile
+  __host__ __device__ int64_t share_begin(int c) const { return (int64_t)rest * steps * c / shares; }
+};
+
+inline Deal deal(int64_t M, int64_t N, int64_t K, int tt, int sms) {
+  Deal d;
+  d.m_tiles = (M + tt - 1) / tt;
+  d.k_tiles = (K + BKT - 1) / BKT;
+  d.steps = (int)(padded_n(N) / BN);
+  d.ctas = sms < DX_CTAS ? sms : DX_CTAS;
+  const int64_t tiles = d.m_tiles * d.k_tiles;
+  d.waves = (int)(tiles / d.ctas);
+  d.rest = (int)(tiles % d.ctas);
+  const int64_t left = (int64_t)d.rest * d.steps;
+  int64_t s = left / MIN_SHARE;
+  if (s > d.ctas) s = d.ctas;
+  if (s < d.rest) s = d.rest;  // at most a tile a share
+  d.shares = d.rest ? (int)s : 0;
+  return d;
+}
+
+// The i-th piece of work of CTA c: stages [step0, step1) of a tile; slot < 0: the whole tile, stored as dx;
+// otherwise the slot of its partial sums.  A share is at most a tile long, so it has at most two pieces.
+struct Piece {
+  int64_t tile;
+  int step0, step1, slot;
+};
+QL_DEVI bool get_piece(const Deal &d, int c, int i, Piece &p) {
+  if (i < d.waves) {
+    p = Piece{(int64_t)i * d.ctas + c, 0, d.steps, -1};
+    return true;
+  }
+  if (c >= d.shares) return false;
+  const int64_t b = d.share_begin(c), e = d.share_begin(c + 1), t0 = b / d.steps, cut = (t0 + 1) * d.steps;
+  const int64_t first = (int64_t)d.waves * d.ctas;
+  if (i == d.waves && b < e) {
+    p = Piece{first + t0, (int)(b - t0 * d.steps), (int)((e < cut ? e : cut) - t0 * d.steps),
+              d.joins() ? 2 * c : -1};
+    return true;
+  }
+  if (i == d.waves + 1 && e > cut) {
+    p = Piece{first + t0 + 1, 0, (int)(e - cut), 2 * c + 1};
+    return true;
+  }
+  return false;
+}
+
+struct Params {
+  int64_t M, N, K;
+  int G;
+  Deal deal;
+  const int *dexp;
+  float *partial;
+  __nv_bfloat16 *dx;
+};
+
+// Eight weights of a run -> four words of fp16 pairs (k, k + 4), k = 0..3, scaled: the order in which one
+// bit operation takes pairs out of a code word.  The k order inside 8 is free here (it is the order of
+// the tile's output rows), see out_k.
+template <int FMT, int BITS>
+QL_DEVI void codes8_to_pairs(const uint32_t (&c)[3], uint32_t (&pr)[4]) {  // -> 1024 + q (+ 32 for int6)
+  if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pr[e] = ((c[0] >> (4 * e)) & 0x000F000Fu) | 0x64006400u;
+  } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {
+    const uint32_t t0 = __byte_perm(c[0], c[1], 0x5140), t1 = __byte_perm(c[0], c[1], 0x7362);
+    pr[0] = __byte_perm(t0, 0x64646464u, 0x4140);
+    pr[1] = __byte_perm(t0, 0x64646464u, 0x4342);
+    pr[2] = __byte_perm(t1, 0x64646464u, 0x4140);
+    pr[3] = __byte_perm(t1, 0x64646464u, 0x4342);
+  } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: 16 bits of codes
+    const uint32_t u = __byte_perm(c[0], 0u, 0x4140);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pr[e] = ((u >> (2 * e)) & 0x00030003u) | 0x64006400u;
+  } else if constexpr (FMT == FMT_INT6P) {  // nibbles, then 16 bits of high fields
+    const uint32_t u = __byte_perm(c[1], 0u, 0x4140);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t f = ((c[0] >> (4 * e)) & 0x000F000Fu) | (((u >> (2 * e)) & 0x00030003u) << 4);
+      pr[e] = (f ^ 0x00200020u) | 0x64006400u;
+    }
+  } else {  // int6: two 24-bit units
+    const uint32_t u0 = c[0] & 0xFFFFFFu, u1 = c[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t f = ((u0 >> (6 * e)) & 0x3Fu) | (((u1 >> (6 * e)) & 0x3Fu) << 16);
+      pr[e] = (f ^ 0x00200020u) | 0x64006400u;
+    }
+  }
+}
+
+// (1024 + q) pairs -> scaled weights: int4 q S - Z S and affine q s + b, one rounding each; int6 q S
+template <int FMT>
+QL_DEVI uint32_t scale_pair(uint32_t pr, __half2 s, __half2 o) {
+  const __half2 v = *reinterpret_cast<const __half2 *>(&pr);
+  __half2 w;
+  if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) w = __hmul2(__hsub2(v, __float2half2_rn(1056.f)), s);
+  else w = __hfma2(__hsub2(v, __float2half2_rn(1024.f)), s, o);
+  return *reinterpret_cast<const uint32_t *>(&w);
+}
+
+// k of row r of the tile: within 8 rows the pairs' order 0,4,1,5,2,6,3,7
+QL_DEVI int out_k(int r) { return (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2); }
+
+// Shared-memory matrix descriptor of an M-major operand in the 128-byte-swizzled layout: for each
+// contraction index a row of 128 bytes (64 fp16 along M), 16-byte chunks XOR-ed with (row % 8); the next 8
+// contraction indices 1024 bytes on, the next 64 of M BN * 128 bytes on.
+QL_DEVI uint64_t umma_desc_m_sw128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);
+  d |= (uint64_t)((BN * 128) >> 4) << 16;  // leading byte offset: next 64 of M
+  d |= (uint64_t)(1024 >> 4) << 32;        // stride byte offset: next 8 of the contraction
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t IDESC_A_M_MAJOR = 1u << 15;
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16
+QL_DEVI void umma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Warp roles as in the forward GEMM: 0 TMA producer, 1 tensor memory and MMA issue, 4-7 epilogue (one k a
+// lane), 8.. dequantisers in groups of four warps that take the stages in turn.  A thread of a group
+// decodes 64 weights of one row n: 128 bytes of A.
+template <int FMT, int BITS, int TT>
+__global__ void __launch_bounds__(num_threads(TT), 1)
+    gemm_dx_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_codes,
+                   const __grid_constant__ CUtensorMap map_codes_hi, const __grid_constant__ CUtensorMap map_meta,
+                   Params p) {
+  constexpr int STAGES = stages(FMT, BITS, TT), NG = deq_groups(TT);
+  constexpr int PROW = code_row(FMT, BITS);
+  constexpr int OFF_B = A_BYTES, OFF_P = OFF_B + b_bytes(TT), OFF_M = OFF_P + p_bytes(FMT, BITS);
+  constexpr int STAGE = stage_bytes(FMT, BITS, TT);
+  static_assert(STAGE % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
+  constexpr uint32_t TMEM_COLS = 2 * TT;
+  static_assert(NG < STAGES, "a group's step through the ring crosses its end at most once");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 3 * STAGES + 5);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  auto bar_tma_full = [&](int s) { return smem_u32(bars + s); };
+  auto bar_a_full = [&](int s) { return smem_u32(bars + STAGES + s); };
+  auto bar_empty = [&](int s) { return smem_u32(bars + 2 * STAGES + s); };
+  auto bar_acc_full = [&](int a) { return smem_u32(bars + 3 * STAGES + a); };
+  auto bar_acc_empty = [&](int a) { return smem_u32(bars + 3 * STAGES + 2 + a); };
+  const uint32_t bar_final = smem_u32(bars + 3 * STAGES + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = (int)blockIdx.x;
+  // runs of a tile and bytes of its metadata box
+  const int runs = FMT == FMT_AFFINE ? (p.G >= BKT ? 1 : BKT / p.G) : 4;
+  const uint32_t stage_tx = (uint32_t)(b_bytes(TT) + p_bytes(FMT, BITS) + runs * BN * 4);
+
+  auto step_ring = [](int &slot, uint32_t &phase, int by, int depth) {
+    slot += by;
+    if (slot >= depth) {
+      slot -= depth;
+      phase ^= 1u;
+    }
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_tma_full(s), 1);
+      mbar_init(bar_a_full(s), 4);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar_acc_full(a), 1);
+      mbar_init(bar_acc_empty(a), 4);
+    }
+    mbar_init(bar_final, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp == WARP_TMA) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_dy);
+      tma_prefetch_desc(&map_codes);
+      tma_prefetch_desc(&map_meta);
+      if constexpr (FMT == FMT_INT6P) tma_prefetch_desc(&map_codes_hi);
+      int s = 0;
+      uint32_t ph = 0;
+      int64_t it = 0;
+      bool ok = true;
+      const bool start = !copies_withheld();
+      Piece pc;
+      for (int i = 0; ok && start && get_piece(p.deal, cta, i, pc); ++i) {
+        const int64_t k_tile = pc.tile / p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
+        for (int st = pc.step0; st < pc.step1; ++st, ++it) {
+          if (!mbar_wait_bounded(bar_empty(s), ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t b = bar_tma_full(s), dst = sbase + s * STAGE;
+          mbar_arrive_expect_tx(b, stage_tx);
+          tma_load_2d(dst + OFF_B, &map_dy, b, st * BN, (int32_t)(m_tile * TT));
+          if constexpr (FMT == FMT_INT6P) {  // half a super-block: 64 low-plane bytes, 32 high-plane bytes
+            const int32_t sb = (int32_t)(192 * (k_tile >> 1)), h = (int32_t)(k_tile & 1);
+            tma_load_2d(dst + OFF_P, &map_codes, b, sb + 64 * h, st * BN);
+            tma_load_2d(dst + OFF_P + BN * 64, &map_codes_hi, b, sb + 128 + 32 * h, st * BN);
+          } else {
+            tma_load_2d(dst + OFF_P, &map_codes, b, (int32_t)(k_tile * PROW), st * BN);
+          }
+          tma_load_2d(dst + OFF_M, &map_meta, b, st * BN, (int32_t)(k_tile * BKT / gran(FMT, p.G)));
+          step_ring(s, ph, 1, STAGES);
+        }
+      }
+      if (!ok) {  // let copies already issued land before the CTA can exit
+        for (int64_t j = it - 1; j >= 0 && j >= it - STAGES; --j) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(bar_tma_full((int)(j % STAGES)), (uint32_t)((j / STAGES) & 1)) &&
+                 clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
+          }
+        }
+      }
+    }
+  } else if (warp == WARP_MMA) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_f16_f32(BKT, TT) | IDESC_A_M_MAJOR;
+      int s = 0, n = 0;
+      uint32_t ph = 0;
+      bool ok = true, issued = false;
+      Piece pc;
+      for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i, ++n) {
+        const int a = n & 1;
+        if (!mbar_wait_bounded(bar_acc_empty(a), ((n >> 1) & 1) ^ 1, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(a * TT);
+        for (int st = pc.step0; st < pc.step1; ++st) {
+          // the dequantisers waited for this stage's copies, so the dy tile has landed too
+          if (!mbar_wait_bounded(bar_a_full(s), ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = umma_desc_m_sw128(sbase + s * STAGE), bd = umma_desc_k_sw128(sbase + s * STAGE + OFF_B);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)  // 16 rows n: 2048 bytes of A, 32 bytes along B's rows
+            umma_f16_ss(d_tmem, ad + (uint64_t)(kk * (2048 >> 4)), bd + (uint64_t)(kk * (32 >> 4)), idesc,
+                        st != pc.step0 || kk != 0);
+          umma_commit(bar_empty(s));
+          issued = true;
+          step_ring(s, ph, 1, STAGES);
+        }
+        if (ok) umma_commit(bar_acc_full(a));
+      }
+      if (issued) {  // all MMAs retired before teardown
+        umma_commit(bar_final);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar_final, 0) && clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
+        }
+      }
+    }
+  } else if (warp >= WARP_EPI0 && warp < WARP_EPI0 + 4) {
+    const int e = warp - WARP_EPI0;  // TMEM lane quarter
+    Piece pc;
+    for (int i = 0; get_piece(p.deal, cta, i, pc); ++i) {
+      const int a = i & 1;
+      const int64_t k_tile = pc.tile / p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
+      const int64_t k = k_tile * BKT + out_k(32 * e + lane);
+      const int tokens = (int)(p.M - m_tile * TT < TT ? p.M - m_tile * TT : TT);
+      if (!mbar_wait_bounded(bar_acc_full(a), (i >> 1) & 1, abort_flag)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < TT / 16; ++c) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * e) << 16) + (uint32_t)(a * TT + 16 * c), r);
+        tmem_ld_wait();
+        if (c == TT / 16 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_acc_empty(a));
+        }
+        if (pc.slot < 0) {
+          if (k < p.K) {
+            __nv_bfloat16 *dst = p.dx + (m_tile * TT + 16 * c) * p.K + k;
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+              if (16 * c + t < tokens)
+                *dst = __float2bfloat16_rn(
+                    mul_pow2(__uint_as_float(r[t]), __ldg(p.dexp + m_tile * TT + 16 * c + t)));
+              dst += p.K;
+            }
+          }
+        } else {
+          float *dst = p.partial + ((int64_t)pc.slot * TT + 16 * c) * BKT + 32 * e + lane;
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            if (16 * c + t < tokens) dst[t * BKT] = __uint_as_float(r[t]);
+        }
+      }
+    }
+  } else if (warp >= WARP_DEQ0) {
+    const int wd = warp - WARP_DEQ0, g = wd >> 2;
+    const int tau = 32 * (wd & 3) + lane;
+    const int n = tau & 63, half = tau >> 6;  // row of the stage, 64-k half of the tile
+    int s = 0, turn = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    Piece pc;
+    for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i) {
+      for (int st = pc.step0; st < pc.step1; ++st) {
+        if (turn == g) {
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tma_full(s), ph, abort_flag))) {
+            ok = false;
+            break;
+          }
+          const uint8_t *stg = smem + s * STAGE;
+          const uint32_t *meta = reinterpret_cast<const uint32_t *>(stg + OFF_M) + n;
+          uint8_t *arow = smem + s * STAGE + half * (BN * 128) + n * 128;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // the half's 32-weight runs
+            const int run = 2 * half + h;
+            const uint32_t mw = meta[(FMT == FMT_AFFINE ? 32 * run / p.G : run) * BN];
+            const __half2 mv = *reinterpret_cast<const __half2 *>(&mw);
+            // 32 codes: words of 8 codes each (8-bit: two words each)
+            uint32_t cw[4][3];
+            const uint8_t *prow = stg + OFF_P + n * PROW;
+            if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {  // 64-byte swizzle
+              const uint4 v = *reinterpret_cast<const uint4 *>(prow + ((run ^ ((n >> 1) & 3)) << 4));
+              cw[0][0] = v.x; cw[1][0] = v.y; cw[2][0] = v.z; cw[3][0] = v.w;
+            } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {  // 128-byte swizzle
+              const uint4 v = *reinterpret_cast<const uint4 *>(prow + (((2 * run) ^ (n & 7)) << 4));
+              const uint4 u = *reinterpret_cast<const uint4 *>(prow + (((2 * run + 1) ^ (n & 7)) << 4));
+              cw[0][0] = v.x; cw[0][1] = v.y; cw[1][0] = v.z; cw[1][1] = v.w;
+              cw[2][0] = u.x; cw[2][1] = u.y; cw[3][0] = u.z; cw[3][1] = u.w;
+            } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: 8 bytes, no swizzle
+              const uint2 v = *reinterpret_cast<const uint2 *>(prow + 8 * run);
+              cw[0][0] = v.x; cw[1][0] = v.x >> 16; cw[2][0] = v.y; cw[3][0] = v.y >> 16;
+            } else if constexpr (FMT == FMT_INT6P) {  // low plane 64-byte swizzle, high plane 32 bytes a row
+              const uint4 v = *reinterpret_cast<const uint4 *>(stg + OFF_P + n * 64 + ((run ^ ((n >> 1) & 3)) << 4));
+              const uint2 u = *reinterpret_cast<const uint2 *>(stg + OFF_P + BN * 64 + n * 32 + 8 * run);
+              cw[0][0] = v.x; cw[1][0] = v.y; cw[2][0] = v.z; cw[3][0] = v.w;
+              cw[0][1] = u.x; cw[1][1] = u.x >> 16; cw[2][1] = u.y; cw[3][1] = u.y >> 16;
+            } else {  // int6: 24 bytes = eight 24-bit units, two a word group
+              const uint2 *src = reinterpret_cast<const uint2 *>(prow + 24 * run);
+              const uint2 a = src[0], b = src[1], c = src[2];
+              cw[0][0] = a.x; cw[0][1] = __funnelshift_r(a.x, a.y, 24);
+              cw[1][0] = __funnelshift_r(a.y, b.x, 16); cw[1][1] = b.x >> 8;
+              cw[2][0] = b.y; cw[2][1] = __funnelshift_r(b.y, c.x, 24);
+              cw[3][0] = __funnelshift_r(c.x, c.y, 16); cw[3][1] = c.y >> 8;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pr[4];
+              codes8_to_pairs<FMT, BITS>(cw[q], pr);
+              __half2 sv, ov;
+              if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {  // 16-weight groups
+                sv = q < 2 ? __low2half2(mv) : __high2half2(mv);
+                ov = sv;
+              } else {
+                sv = __low2half2(mv);
+                ov = FMT == FMT_INT4 ? __hneg2(__high2half2(mv)) : __high2half2(mv);
+              }
+              const uint4 o = make_uint4(scale_pair<FMT>(pr[0], sv, ov), scale_pair<FMT>(pr[1], sv, ov),
+                                         scale_pair<FMT>(pr[2], sv, ov), scale_pair<FMT>(pr[3], sv, ov));
+              *reinterpret_cast<uint4 *>(arow + (((4 * h + q) ^ (n & 7)) << 4)) = o;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_a_full(s));
+        }
+        if (++turn == NG) turn = 0;
+        step_ring(s, ph, 1, STAGES);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ---- pass 4: the sums of the split tiles' parts -------------------------------------------------------
+// One CTA of 128 threads a (tile, token): thread r adds row r's parts in the order of the shares.
+template <int TT>
+__global__ void __launch_bounds__(BKT) join_kernel(Params p) {
+  const Deal &d = p.deal;
+  const int64_t rest_tile = blockIdx.x, tile = (int64_t)d.waves * d.ctas + rest_tile;
+  const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
+  const int64_t m = m_tile * TT + blockIdx.y, k = k_tile * BKT + out_k((int)threadIdx.x);
+  if (m >= p.M) return;
+  const int64_t lo = rest_tile * d.steps, hi = lo + d.steps, all = (int64_t)d.rest * d.steps;
+  int c = (int)(lo * d.shares / all);  // at or just before the share that holds stage lo
+  while (d.share_begin(c + 1) <= lo) ++c;
+  float sum = 0.f;
+  for (; c < d.shares && d.share_begin(c) < hi; ++c) {
+    const int64_t b = d.share_begin(c);
+    if (b == d.share_begin(c + 1)) continue;
+    const int slot = 2 * c + (b < lo ? 1 : 0);  // the share's second piece when it began in the tile before
+    sum += __ldcg(p.partial + ((int64_t)slot * TT + blockIdx.y) * BKT + threadIdx.x);
+  }
+  if (k < p.K) p.dx[m * p.K + k] = __float2bfloat16_rn(mul_pow2(sum, __ldg(p.dexp + m)));
+}
+
+}  // namespace dx
+}  // namespace ql

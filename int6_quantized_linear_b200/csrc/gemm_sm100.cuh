@@ -41,6 +41,7 @@
 // Every mbarrier wait is bounded; a wait that gives up sets the device status
 // word and makes every role leave its loop.
 #pragma once
+#include "gated.cuh"
 #include "gemm_prep.cuh"
 #include "pack_dequant.cuh"
 
@@ -132,7 +133,28 @@ struct Params {
   const uint8_t *steps;
   __nv_bfloat16 *y;
   GemmWorkspace ws;
+  // the gated form only (y is then h [M][N / 2])
+  int act;
+  int8_t *saved;        // codes [M][2][save8_cols(N / 2)] of (g, u), or NULL
+  uint8_t *saved_exps;  // [M][2][save8_cols(N / 2) / 16]
 };
+
+// The gated form: the layer's rows are F = N / 2 gate rows, then F up rows, and a tile is 64 features:
+// their 64 gate rows and 64 up rows (two code boxes of 64 rows).  Which of the tile's rows goes to which
+// TMEM lane is the dequantisers' choice, and they give each lane quarter 16 features, gate rows in its
+// lanes 0-15 and up rows in lanes 16-31: g and u of a feature then meet in one epilogue warp by a
+// shuffle, without shared memory.  Box row (and metadata slot row) of lane r of the tile:
+constexpr int GATED_F = BN / 2;  // features a tile
+template <bool GATED>
+QL_DEVI int box_row(int r) {
+  return GATED ? ((r & 16) ? GATED_F : 0) + 16 * (r >> 5) + (r & 15) : r;
+}
+// Layer row of box row br.  A tile's last features may be past F: their gate rows are then up rows (or,
+// like their up rows, past N) whose results are not stored.
+template <bool GATED>
+QL_DEVI int64_t layer_row(int64_t n_tile, int br, int64_t N) {
+  return GATED ? (br < GATED_F ? n_tile * GATED_F + br : N / 2 + n_tile * GATED_F + br - GATED_F) : n_tile * BN + br;
+}
 
 // Metadata of one 32-weight chunk (see formats.cuh): int4 (gm, st); int6
 // (two scale codes, st); affine (gm, unused).
@@ -285,7 +307,69 @@ QL_DEVI void chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], const uint
   }
 }
 
-template <int FMT, int BITS, int TT, int CPS = 1>
+// Epilogue of the gated form for 16 tokens (m0 ..) of one feature f: lanes 0-15 of the warp hold the 16
+// tokens' g in r, lanes 16-31 the same features' u.  Each lane sends half of its tokens to its partner
+// (lane ^ 16) and receives the other projection of the half it keeps: lanes 0-15 finish tokens 0-7, lanes
+// 16-31 tokens 8-15, and the 16 lanes' features are contiguous in h.  With a checkpoint, the 16 features
+// are also one group of its scales: a group's key is the maximum over the half-warp, taken for four
+// values at once in the bytes of a word.
+QL_DEVI void gated_store(const Params &p, const uint32_t (&r)[16], int64_t f, int64_t m0, int lane) {
+  const int64_t F = p.N / 2;
+  const bool up = lane >= 16, live = f < F;
+  float g[8], u[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, up ? r[t] : r[8 + t], 16));
+    g[t] = up ? other : __uint_as_float(r[t]);
+    u[t] = up ? __uint_as_float(r[8 + t]) : other;
+  }
+  m0 += up ? 8 : 0;
+  const int64_t rows_left = p.M - m0;
+  if (live) {
+    __nv_bfloat16 *dst = p.y + m0 * F + f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      if (t < rows_left) *dst = __float2bfloat16_rn(act_value(p.act, g[t]) * u[t]);
+      dst += F;
+    }
+  }
+  if (p.saved) {
+    uint32_t k[4] = {0u, 0u, 0u, 0u};  // keys of g (tokens 0-3, 4-7), then of u
+    if (live) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        k[t >> 2] |= save8_key(g[t]) << (8 * (t & 3));
+        k[2 + (t >> 2)] |= save8_key(u[t]) << (8 * (t & 3));
+      }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = __vmaxu4(k[j], __shfl_xor_sync(0xffffffffu, k[j], o));
+    const int64_t fp = save8_cols(F);
+    if (f < fp) {  // columns F .. fp - 1 hold zeros
+      int8_t *dst = p.saved + 2 * m0 * fp + f;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        if (t < rows_left) {
+          const float ig = save8_inverse(save8_exponent((k[t >> 2] >> (8 * (t & 3))) & 0xffu));
+          const float iu = save8_inverse(save8_exponent((k[2 + (t >> 2)] >> (8 * (t & 3))) & 0xffu));
+          dst[0] = (int8_t)(live ? save8_code(g[t], ig) : 0);
+          dst[fp] = (int8_t)(live ? save8_code(u[t], iu) : 0);
+        }
+        dst += 2 * fp;
+      }
+      // lane l of the half-warp stores the exponent of value l: g of tokens 0-7, then u
+      const int l = lane & 15, t = l & 7;
+      const uint32_t kw = l < 4 ? k[0] : l < 8 ? k[1] : l < 12 ? k[2] : k[3];
+      if (t < rows_left)
+        p.saved_exps[((m0 + t) * 2 + (l >> 3)) * (fp / 16) + (f >> 4)] =
+            (uint8_t)save8_exponent((kw >> (8 * (l & 3))) & 0xffu);
+    }
+  }
+}
+
+template <int FMT, int BITS, int TT, int CPS = 1, bool GATED = false>
 __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
     gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_codes,
                 Params p) {
@@ -320,7 +404,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
   auto bar_meta_empty = [&](int s) { return smem_u32(bars + 3 * STAGES + 5 + MSLOTS + s); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t m_tiles = (p.M + TT - 1) / TT, n_tiles = (p.N + BN - 1) / BN;
+  const int64_t m_tiles = (p.M + TT - 1) / TT, n_tiles = GATED ? (p.N / 2 + GATED_F - 1) / GATED_F : (p.N + BN - 1) / BN;
   const int64_t num_tiles = m_tiles * n_tiles;
   const int num_kb = (int)(p.K / BK);
   const int64_t my_tiles = (num_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x;
@@ -404,17 +488,26 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
         }
         mbar_arrive_expect_tx(bar_tma_full(s), STAGE_TX);
         tma_load_2d(sbase + off_a(TT, s), &map_x, bar_tma_full(s), cur.kb * BK, (int32_t)(cur.m_tile * TT));
+        // the tile's code rows, as one box (or, gated, as a gate box and an up box of 64 rows)
+        auto load_codes = [&](int box_bytes, int off, int32_t x) {
+          if constexpr (GATED) {
+            const uint32_t dst = sbase + off_p(FMT, BITS, TT, s) + off;
+            tma_load_2d(dst, &map_codes, bar_tma_full(s), x, (int32_t)(cur.n_tile * GATED_F));
+            tma_load_2d(dst + GATED_F * box_bytes, &map_codes, bar_tma_full(s), x,
+                        (int32_t)(p.N / 2 + cur.n_tile * GATED_F));
+          } else {
+            tma_load_2d(sbase + off_p(FMT, BITS, TT, s) + off, &map_codes, bar_tma_full(s), x,
+                        (int32_t)(cur.n_tile * BN));
+          }
+        };
         if constexpr (FMT == FMT_INT6P) {  // k-step kb: low-plane bytes 32 (kb % 4) .. and high-plane
                                            // bytes 128 + 16 (kb % 4) .. of super-block kb / 4, by 16-byte boxes
           const int32_t x0 = 192 * (cur.kb >> 2) + 32 * (cur.kb & 3), xh = 192 * (cur.kb >> 2) + 128 + 16 * (cur.kb & 3);
-          tma_load_2d(sbase + off_p(FMT, BITS, TT, s), &map_codes, bar_tma_full(s), x0, (int32_t)(cur.n_tile * BN));
-          tma_load_2d(sbase + off_p(FMT, BITS, TT, s) + 16 * BN, &map_codes, bar_tma_full(s), x0 + 16,
-                      (int32_t)(cur.n_tile * BN));
-          tma_load_2d(sbase + off_p(FMT, BITS, TT, s) + 32 * BN, &map_codes, bar_tma_full(s), xh,
-                      (int32_t)(cur.n_tile * BN));
+          load_codes(16, 0, x0);
+          load_codes(16, 16 * BN, x0 + 16);
+          load_codes(16, 32 * BN, xh);
         } else {
-          tma_load_2d(sbase + off_p(FMT, BITS, TT, s), &map_codes, bar_tma_full(s), cur.kb * PROW,
-                      (int32_t)(cur.n_tile * BN));
+          load_codes(PROW, 0, cur.kb * PROW);
         }
         step_ring(s, ph, STAGES);
         advance(cur);
@@ -502,7 +595,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
 #pragma unroll
         for (int i = 0; i < BN / 64; ++i) {
           const int r = t + 64 * i;
-          const int64_t n = cur.n_tile * BN + r;
+          const int64_t n = layer_row<GATED>(cur.n_tile, r, p.N);
           const bool valid = n < p.N;
           const int64_t nn = valid ? n : p.N - 1;
           cp_async16(dst + r * 16, p.gmeta + nn * (p.K / 16) + 16 * (cur.kb >> 2), valid);
@@ -524,7 +617,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       const uint32_t ause = (uint32_t)(tcount / NACC);
       // the tile's scale exponents and bias, loaded while its MMAs run: lane l holds the exponents of
       // tokens l, l + 32, .. (a load per column chunk would put an L2 round trip between the chunks)
-      const int64_t n = n_tile * BN + 32 * e + lane;
+      const int64_t n = layer_row<GATED>(n_tile, box_row<GATED>(32 * e + lane), p.N);
       const int we = n < p.N ? p.ws.wexp[n] : 0;
       const float bn = (p.bias && n < p.N) ? __bfloat162float(p.bias[n]) : 0.f;
       // (each exponent lies in [-126, 126], so one signed byte holds it: a chunk's 16 are one broadcast
@@ -579,7 +672,9 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
             r[t] = __float_as_uint(mul_pow2(__uint_as_float(r[t]), xe + we) + bn);
           }
         }
-        if (n < p.N) {  // token t of row n: the warp's 32 rows are 64 contiguous bytes of y's row m0 + t
+        if constexpr (GATED) {
+          gated_store(p, r, n_tile * GATED_F + 16 * e + (lane & 15), m0, lane);
+        } else if (n < p.N) {  // token t of row n: the warp's 32 rows are 64 contiguous bytes of y's row m0 + t
           __nv_bfloat16 *dst = p.y + m0 * p.N + n;
           const int64_t rows_left = p.M - m0;
 #pragma unroll
@@ -598,7 +693,9 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
     // the A operand of that stage's MMAs.
     const int wd = warp - WARP_DEQ0;     // 0 .. DEQ_WARPS - 1
     const int g = wd >> 2;               // stages it = g, g + NG, ...
-    const int r = 32 * (wd & 3) + lane;  // tile row
+    const int r = 32 * (wd & 3) + lane;  // lane of the tile
+    const int br = box_row<GATED>(r);    // its row in the code box and the metadata slots
+    auto row_of = [&](int64_t n_tile) { return layer_row<GATED>(n_tile, br, p.N); };
     const uint32_t t_row = tmem_base + ((uint32_t)(32 * (wd & 3)) << 16) + A_COL0;
     auto step_ng = [](int &slot, uint32_t &phase, int depth) {
       slot += NG;
@@ -615,10 +712,10 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
     float sc = 0.f;
     if (g < total_it) {
       if constexpr (FMT != FMT_INT4) {
-        load_meta<FMT>(p, cur.n_tile * BN + r, (int64_t)cur.kb * 2, gm[0], st[0]);
-        load_meta<FMT>(p, cur.n_tile * BN + r, (int64_t)cur.kb * 2 + 1, gm[1], st[1]);
+        load_meta<FMT>(p, row_of(cur.n_tile), (int64_t)cur.kb * 2, gm[0], st[0]);
+        load_meta<FMT>(p, row_of(cur.n_tile), (int64_t)cur.kb * 2 + 1, gm[1], st[1]);
       }
-      sc = row_scale(cur.n_tile * BN + r);
+      sc = row_scale(row_of(cur.n_tile));
     }
     for (int64_t it = g; it < total_it; it += NG) {
       Cursor nx = cur;  // this group's next stage
@@ -626,7 +723,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       uint32_t ngm[2] = {0, 0}, nst[2] = {0, 0};
       float nsc = sc;
       if (it + NG < total_it) {  // its metadata (int6, affine) and row scale, loaded ahead
-        const int64_t n = nx.n_tile * BN + r;
+        const int64_t n = row_of(nx.n_tile);
         if constexpr (FMT != FMT_INT4) {
           load_meta<FMT>(p, n, (int64_t)nx.kb * 2, ngm[0], nst[0]);
           load_meta<FMT>(p, n, (int64_t)nx.kb * 2 + 1, ngm[1], nst[1]);
@@ -637,10 +734,10 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
         const int q = (int)(it & 3);  // stage of the super-block: this group sees q = g, g + NG, ..
         if (q == g && !__all_sync(0xffffffffu, mbar_wait_bounded(bar_meta_full(ms), phm, abort_flag))) break;
         const uint8_t *slot = smem + off_meta(FMT, BITS, TT, ms);
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(slot + r * 16 + 4 * q);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(slot + br * 16 + 4 * q);
         gm[0] = w & 0xffffu;
         gm[1] = w >> 16;
-        st[0] = st[1] = *reinterpret_cast<const uint32_t *>(slot + BN * 16 + r * 4);
+        st[0] = st[1] = *reinterpret_cast<const uint32_t *>(slot + BN * 16 + br * 4);
         if (q == g + 4 - NG) {  // this group's last stage of the super-block: release the slot
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_meta_empty(ms));
@@ -651,12 +748,12 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       // released the stage before TMA refilled it)
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tma_full(s), ph, abort_flag))) break;
       tc_fence_after();
-      const uint8_t *prow = smem + off_p(FMT, BITS, TT, s) + r * PROW;
+      const uint8_t *prow = smem + off_p(FMT, BITS, TT, s) + br * PROW;
       uint32_t o[32];
       if constexpr (PROW == 32 && (FMT == FMT_INT4 || FMT == FMT_AFFINE)) {
-        // the row's two 16-byte chunks, read in the order (h ^ bit 2 of r) so that the 32 lanes'
+        // the row's two 16-byte chunks, read in the order (h ^ bit 2 of the row) so that the 32 lanes'
         // first reads cover all 32 banks in four wavefronts (rows are 32 bytes apart)
-        const int sw = (r >> 2) & 1;
+        const int sw = (br >> 2) & 1;
         const uint4 va = reinterpret_cast<const uint4 *>(prow)[sw];
         const uint4 vb = reinterpret_cast<const uint4 *>(prow)[sw ^ 1];
         const uint4 c0 = sw ? vb : va, c1 = sw ? va : vb;
@@ -675,8 +772,8 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
           const uint8_t *src = prow + h * (PROW / 2);
           const uint8_t *src_hi = nullptr;
           if constexpr (FMT == FMT_INT6P) {
-            src = smem + off_p(FMT, BITS, TT, s) + h * 16 * BN + r * 16;
-            src_hi = smem + off_p(FMT, BITS, TT, s) + 32 * BN + r * 16 + 8 * h;
+            src = smem + off_p(FMT, BITS, TT, s) + h * 16 * BN + br * 16;
+            src_hi = smem + off_p(FMT, BITS, TT, s) + 32 * BN + br * 16 + 8 * h;
           }
           uint32_t cw[code_bits(FMT, BITS)];
           if constexpr (FMT == FMT_INT4 || FMT == FMT_AFFINE) load_code_words<FMT, BITS>(src, cw);

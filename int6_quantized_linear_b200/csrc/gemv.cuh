@@ -7,6 +7,7 @@
 // trip count over chunks is the same for every lane of a warp, so full-mask
 // shuffles are always reached.
 #pragma once
+#include "gated.cuh"
 #include "gemm_prep.cuh"
 #include "pack_dequant.cuh"
 
@@ -14,6 +15,41 @@ namespace ql {
 
 // Optional per-output-row bias (bf16 [N], may be NULL), added in fp32 before the one rounding.
 QL_DEVI float bias_at(const __nv_bfloat16 *bias, int64_t n) { return bias ? __bfloat162float(bias[n]) : 0.f; }
+
+// The gated form of the decode kernels: the layer's rows are F = N / 2 gate rows, then F up rows, and a
+// CTA's 64 rows are 32 features' gate rows (local rows 0-31) and up rows (32-63).  Layer row of local row
+// r of group rg; the last group's rows may be past F (their results are not stored) or past N.
+constexpr int GATED_ROWS = 32;  // features a CTA
+template <bool GATED>
+QL_DEVI int64_t group_row(int64_t rg, int r, int64_t N) {
+  return GATED ? (r < GATED_ROWS ? rg * GATED_ROWS + r : N / 2 + rg * GATED_ROWS + r - GATED_ROWS) : rg * 64 + r;
+}
+// TMA of a group's box: 64 rows, or (gated) 32 gate rows and 32 up rows, row_bytes each in shared memory
+template <bool GATED>
+QL_DEVI void load_group_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int64_t rg, int64_t N,
+                            int row_bytes) {
+  if constexpr (GATED) {
+    tma_load_2d(dst, map, bar, x, (int32_t)(rg * GATED_ROWS));
+    tma_load_2d(dst + GATED_ROWS * row_bytes, map, bar, x, (int32_t)(N / 2 + rg * GATED_ROWS));
+  } else {
+    tma_load_2d(dst, map, bar, x, (int32_t)(rg * 64));
+  }
+}
+// The consumer warps of a CTA (128 threads) meet without its producer; they all come here, also when a
+// wait gave up.
+QL_DEVI void consumer_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+// h of a CTA's 32 features for M tokens from its 64 rows' sums: sums(token, row)
+template <class Sums>
+QL_DEVI void gated_finish(const Sums &sums, int64_t rg, int64_t F, int M, int act, __nv_bfloat16 *h) {
+  for (int e = threadIdx.x; e < M * GATED_ROWS; e += 128) {
+    const int tk = e >> 5, r = e & 31;
+    const int64_t f = rg * GATED_ROWS + r;
+    if (f < F) h[(int64_t)tk * F + f] = __float2bfloat16_rn(act_value(act, sums(tk, r)) * sums(tk, r + GATED_ROWS));
+  }
+}
 
 template <int FMT, int BITS, int MT>
 __global__ void __launch_bounds__(256) gemv_simple_kernel(WeightPtrs p, int64_t N, const __nv_bfloat16 *x,
@@ -416,7 +452,8 @@ struct GemvTcParams {
   int64_t N, K;
   int P;           // parts of K: CTA b takes part b % P of tiles 4 (b / P) .. + 3
   float *partial;  // P > 1: [tile][part][16 rows], added by gemv_m1_sum_parts
-  __nv_bfloat16 *y;
+  __nv_bfloat16 *y;  // [N]; gated: h [N / 2]
+  int act;           // gated only
 };
 
 // The low bytes of 24-bit x for one warp of the M = 1 kernel: S G_x 2^-8 D_lo per (row, 32-k slice) of
@@ -496,7 +533,9 @@ __device__ __noinline__ float2 gemv_m1_low_bytes(const uint8_t *q0, const uint8_
 // shared-memory offset inside a stage is a constant; step words come through the L1 cache RING - 1
 // super-blocks ahead.  With K split (P > 1), each part's row sums go to the workspace and a small
 // dependent kernel adds them in part order, so the result does not depend on timing.
-template <int FMT, int G>
+//
+// GATED: a CTA's four tiles are two 16-feature tiles' gate rows (warps 0, 1) and up rows (warps 2, 3).
+template <int FMT, int G, bool GATED = false>
 __device__ __forceinline__ void gemv_m1_body(const CUtensorMap &map_codes, const CUtensorMap &map_gmeta,
                                              const GemvTcParams &p) {
   using L = M1Layout<FMT, G>;
@@ -509,13 +548,17 @@ __device__ __forceinline__ void gemv_m1_body(const CUtensorMap &map_codes, const
   uint8_t *zero_blk = xflag + 32;
   uint64_t *bars = reinterpret_cast<uint64_t *>(zero_blk + GEMV_ZERO_BYTES);
   __shared__ int abort_flag;
+  __shared__ float gated_sums[GATED ? 16 * GEMV_WARPS : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t n_tiles = (p.N + 15) / 16;
   const int P = p.P;
   const int part = (int)(blockIdx.x % (unsigned)P);
   const int64_t tile = (int64_t)(blockIdx.x / (unsigned)P) * GEMV_WARPS + warp;
   const int g = lane >> 2, c = lane & 3;
-  const bool active = tile < n_tiles;  // warps past the last tile stream nothing
+  // first layer row of the warp's tile, and whether any of its rows is wanted (warps past the last
+  // tile stream nothing)
+  const int64_t row0 = GATED ? group_row<true>(blockIdx.x / (unsigned)P, 16 * warp, p.N) : tile * 16;
+  const bool active = GATED ? (int64_t)(blockIdx.x / (unsigned)P) * GATED_ROWS + 16 * (warp & 1) < p.N / 2 : tile < n_tiles;
   const int NS = (int)(p.K / 256);
   const int sb0 = part * NS / P, nsb = (part + 1) * NS / P - sb0;  // the CTA's part of K
   const int nsw = active ? nsb : 0;                                // super-blocks this warp streams
@@ -537,8 +580,8 @@ __device__ __forceinline__ void gemv_m1_body(const CUtensorMap &map_codes, const
   auto issue_w = [&](int i, int s) {
     const uint32_t bar = bar0 + 8 * s;
     mbar_arrive_expect_tx(bar, L::STAGE_TX);
-    tma_load_2d(cring + s * 2048, &map_codes, bar, (sb0 + i) * 128, (int32_t)(tile * 16));
-    tma_load_2d(gring + s * L::GM_STAGE, &map_gmeta, bar, (sb0 + i) * GM_ROW, (int32_t)(tile * 16));
+    tma_load_2d(cring + s * 2048, &map_codes, bar, (sb0 + i) * 128, (int32_t)row0);
+    tma_load_2d(gring + s * L::GM_STAGE, &map_gmeta, bar, (sb0 + i) * GM_ROW, (int32_t)row0);
   };
   const int nis = copies_withheld() ? 0 : nsw;  // super-blocks whose copies this warp starts
   const int pre = nis < GEMV_RING - 1 ? nis : GEMV_RING - 1;
@@ -549,7 +592,7 @@ __device__ __forceinline__ void gemv_m1_body(const CUtensorMap &map_codes, const
     for (int i = 0; i < pre; ++i) issue_w(i, i);
   }
   const int pg = (g >> 1) | ((g & 1) << 2);
-  int64_t r0 = tile * 16 + pg, r1 = r0 + 8;
+  int64_t r0 = row0 + pg, r1 = r0 + 8;
   if (r0 >= p.N) r0 = p.N - 1;  // rows past the end are computed on a valid row and discarded
   if (r1 >= p.N) r1 = p.N - 1;
   const uint32_t *st0 = reinterpret_cast<const uint32_t *>(p.steps) + r0 * NS + sb0;
@@ -729,6 +772,18 @@ __device__ __forceinline__ void gemv_m1_body(const CUtensorMap &map_codes, const
   acc0 += __shfl_xor_sync(0xffffffffu, acc0, 2);
   acc1 += __shfl_xor_sync(0xffffffffu, acc1, 1);
   acc1 += __shfl_xor_sync(0xffffffffu, acc1, 2);
+  if constexpr (GATED) {
+    if (P == 1) {
+      if (c == 0) {
+        gated_sums[16 * warp + pg] = acc0;
+        gated_sums[16 * warp + pg + 8] = acc1;
+      }
+      __syncthreads();
+      if (!abort_flag)
+        gated_finish([&](int, int r) { return gated_sums[r]; }, blockIdx.x, p.N / 2, 1, p.act, p.y);
+      return;
+    }
+  }
   if (P == 1) {
     if (active && ok && c == 0) {
       const int64_t ra = tile * 16 + pg, rb = ra + 8;
@@ -762,19 +817,37 @@ __global__ void __launch_bounds__(256) gemv_m1_sum_parts(const float *partial, i
   y[r] = __float2bfloat16_rn(sum + bias_at(bias, r));
 }
 
+// The same for the gated form: one thread per feature adds the parts of its gate row and of its up row
+// (tiles 4 j, 4 j + 1 are gate tiles, 4 j + 2, 4 j + 3 their up tiles).
+__global__ void __launch_bounds__(256) gemv_m1_sum_parts_gated(const float *partial, int P, int64_t F, int act,
+                                                               __nv_bfloat16 *h) {
+  pdl_launch_dependents();
+  const int64_t f = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  pdl_wait();
+  if (f >= F) return;
+  const float *src = partial + (4 * (f >> 5) + ((f >> 4) & 1)) * P * 16 + (f & 15);
+  float g = 0.f, u = 0.f;
+  for (int q = 0; q < P; ++q) {
+    g += src[q * 16];
+    u += src[(2 * P + q) * 16];
+  }
+  h[f] = __float2bfloat16_rn(act_value(act, g) * u);
+}
+
 // int4 (nested superscale) at M = 1
+template <bool GATED>
 __global__ void __launch_bounds__(32 * GEMV_WARPS, GEMV_CTAS_PER_SM)
     gemv_int4_m1_tc_kernel(const __grid_constant__ CUtensorMap map_codes,
                            const __grid_constant__ CUtensorMap map_gmeta, GemvTcParams p) {
-  gemv_m1_body<FMT_INT4, 32>(map_codes, map_gmeta, p);
+  gemv_m1_body<FMT_INT4, 32, GATED>(map_codes, map_gmeta, p);
 }
 
 // 4-bit affine (group G = 32 or 64) at M = 1: the same nibble layout, (s, b) per group
-template <int G>
+template <int G, bool GATED>
 __global__ void __launch_bounds__(32 * GEMV_WARPS, GEMV_CTAS_PER_SM)
     gemv_affine4_m1_tc_kernel(const __grid_constant__ CUtensorMap map_codes,
                               const __grid_constant__ CUtensorMap map_gmeta, GemvTcParams p) {
-  gemv_m1_body<FMT_AFFINE, G>(map_codes, map_gmeta, p);
+  gemv_m1_body<FMT_AFFINE, G, GATED>(map_codes, map_gmeta, p);
 }
 
 
@@ -922,7 +995,8 @@ struct GemvMtParams {
   int M;  // 1 .. 8 tokens (int4: 2 .. 8)
   SplitK split;  // of K over the CTAs of the grid, per 64-row group
   GemvWorkspace ws;
-  __nv_bfloat16 *y;
+  __nv_bfloat16 *y;  // [M][N]; gated: h [M][N / 2]
+  int act;           // gated only
 };
 
 template <int FMT, int BITS, int G>
@@ -1011,7 +1085,7 @@ __device__ __noinline__ float4 gemv_mt_low_bytes(const uint8_t *codes, const uin
 // gives T = sum_k A_k x_int_k with A = 16 q (nibbles) or q (2-bit fields, bytes); then
 //   int4:   y += S (2^-a / 16) (T - 16 Z X)
 //   affine: y += s' (2^-a / 16) T + b 2^-a X      (s' = s for nibbles, 16 s otherwise)
-template <int FMT, int BITS, int G>
+template <int FMT, int BITS, int G, bool GATED = false>
 __device__ __forceinline__ void gemv_mt_body(const CUtensorMap &map_codes, const CUtensorMap &map_gmeta,
                                              const GemvMtParams &p) {
   using L = MtLayout<FMT, BITS, G>;
@@ -1059,9 +1133,9 @@ __device__ __forceinline__ void gemv_mt_body(const CUtensorMap &map_codes, const
         mbar_arrive_expect_tx(bar_full(s), tx);
 #pragma unroll
         for (int bx = 0; bx < L::CODE_BOXES; ++bx)
-          tma_load_2d(st + bx * 64 * L::CODE_BOX, &map_codes, bar_full(s), (sb0 + i) * L::CODE_ROW + bx * L::CODE_BOX,
-                      (int32_t)(rg * 64));
-        tma_load_2d(st + L::ST_GMETA, &map_gmeta, bar_full(s), (sb0 + i) * L::META_ROW, (int32_t)(rg * 64));
+          load_group_box<GATED>(st + bx * 64 * L::CODE_BOX, &map_codes, bar_full(s),
+                                (sb0 + i) * L::CODE_ROW + bx * L::CODE_BOX, rg, p.N, L::CODE_BOX);
+        load_group_box<GATED>(st + L::ST_GMETA, &map_gmeta, bar_full(s), (sb0 + i) * L::META_ROW, rg, p.N, L::META_ROW);
       };
       auto issue_x = [&](int i, int s) {
         const uint32_t st = sbase + s * L::STAGE;
@@ -1102,7 +1176,7 @@ __device__ __forceinline__ void gemv_mt_body(const CUtensorMap &map_codes, const
   } else {  // consumers: warp w owns box rows 16w + g and 16w + g + 8
     const int g = lane >> 2, c = lane & 3;
     const int r0 = 16 * warp + g, r1 = r0 + 8;
-    int64_t n0 = rg * 64 + r0, n1 = n0 + 8;
+    const int64_t n0 = group_row<GATED>(rg, r0, p.N), n1 = n0 + 8;
     const int64_t c0 = n0 < p.N ? n0 : p.N - 1, c1 = n1 < p.N ? n1 : p.N - 1;
     const uint32_t *st0 = reinterpret_cast<const uint32_t *>(p.steps) + c0 * NS + sb0;
     const uint32_t *st1 = reinterpret_cast<const uint32_t *>(p.steps) + c1 * NS + sb0;
@@ -1240,8 +1314,15 @@ __device__ __forceinline__ void gemv_mt_body(const CUtensorMap &map_codes, const
       acc[2] += lb.z;
       acc[3] += lb.w;
     }
+    float *mine = p.ws.partial + (int64_t)blockIdx.x * M * 64;
+    if constexpr (GATED) {
+      if (P == 1) {  // the sums meet in shared memory, once every stage has been read
+        consumer_sync();
+        mine = reinterpret_cast<float *>(smem);
+      }
+    }
     if (ok) {
-      if (P == 1) {
+      if (P == 1 && !GATED) {
         if (n0 < p.N) {
           const float b0 = bias_at(p.bias, n0);
           if (tk0 < M) p.y[(int64_t)tk0 * p.N + n0] = __float2bfloat16_rn(acc[0] + b0);
@@ -1253,7 +1334,6 @@ __device__ __forceinline__ void gemv_mt_body(const CUtensorMap &map_codes, const
           if (tk1 < M) p.y[(int64_t)tk1 * p.N + n1] = __float2bfloat16_rn(acc[3] + b1);
         }
       } else {
-        float *mine = p.ws.partial + (int64_t)blockIdx.x * M * 64;
         if (tk0 < M) {
           mine[tk0 * 64 + r0] = acc[0];
           mine[tk0 * 64 + r1] = acc[2];
@@ -1264,6 +1344,12 @@ __device__ __forceinline__ void gemv_mt_body(const CUtensorMap &map_codes, const
         }
       }
     }
+    if constexpr (GATED) {
+      if (P == 1) {
+        consumer_sync();
+        if (!*abort_flag) gated_finish([&](int tk, int r) { return mine[tk * 64 + r]; }, rg, p.N / 2, M, p.act, p.y);
+      }
+    }
   }
   if (P > 1) {  // the CTA that completes a row group adds its P parts in part order
     __syncthreads();  // every partial store precedes thread 0's release
@@ -1271,29 +1357,40 @@ __device__ __forceinline__ void gemv_mt_body(const CUtensorMap &map_codes, const
     __syncthreads();  // thread 0's acquire precedes the reads of the other parts
     if (flags[1] && warp < GEMV_MT_WARPS) {
       const float *base = p.ws.partial + first * M * 64;
-      for (int e = threadIdx.x; e < M * 64; e += GEMV_MT_WARPS * 32) {
-        const int tk = e >> 6, r = e & 63;
-        float sum = 0.f;
-        for (int q = 0; q < P; ++q) sum += __ldcg(base + (int64_t)q * M * 64 + e);
-        const int64_t n = rg * 64 + r;
-        if (n < p.N) p.y[(int64_t)tk * p.N + n] = __float2bfloat16_rn(sum + bias_at(p.bias, n));
+      if constexpr (GATED) {
+        gated_finish(
+            [&](int tk, int r) {
+              float sum = 0.f;
+              for (int q = 0; q < P; ++q) sum += __ldcg(base + ((int64_t)q * M + tk) * 64 + r);
+              return sum;
+            },
+            rg, p.N / 2, M, p.act, p.y);
+      } else {
+        for (int e = threadIdx.x; e < M * 64; e += GEMV_MT_WARPS * 32) {
+          const int tk = e >> 6, r = e & 63;
+          float sum = 0.f;
+          for (int q = 0; q < P; ++q) sum += __ldcg(base + (int64_t)q * M * 64 + e);
+          const int64_t n = rg * 64 + r;
+          if (n < p.N) p.y[(int64_t)tk * p.N + n] = __float2bfloat16_rn(sum + bias_at(p.bias, n));
+        }
       }
     }
   }
 }
 
 // The kernels: the same body under the register budget of each format (see gemv_mt_ctas_per_sm).
+template <bool GATED>
 __global__ void __launch_bounds__(GEMV_MT_THREADS, GEMV_MT_CTAS_PER_SM)
     gemv_mt_int4_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_gmeta,
                         GemvMtParams p) {
-  gemv_mt_body<FMT_INT4, 4, 32>(map_codes, map_gmeta, p);
+  gemv_mt_body<FMT_INT4, 4, 32, GATED>(map_codes, map_gmeta, p);
 }
 
-template <int BITS, int G>
+template <int BITS, int G, bool GATED>
 __global__ void __maxnreg__(GEMV_MT_AFFINE_NREG)
     gemv_mt_affine_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_gmeta,
                           GemvMtParams p) {
-  gemv_mt_body<FMT_AFFINE, BITS, G>(map_codes, map_gmeta, p);
+  gemv_mt_body<FMT_AFFINE, BITS, G, GATED>(map_codes, map_gmeta, p);
 }
 
 }  // namespace ql

@@ -69,7 +69,8 @@ struct GemvF16Params {
   int M;
   SplitK split;  // of K over the CTAs of the grid, per 64-row group
   GemvWorkspace ws;  // partial sums and counters of a K split
-  __nv_bfloat16 *y;
+  __nv_bfloat16 *y;  // [M][N]; gated: h [M][N / 2]
+  int act;           // gated only
 };
 
 #define QL_HMMA(D, A0, A1, A2, A3, B0, B1)                                                                \
@@ -109,7 +110,7 @@ QL_DEVI void slice_pairs(uint32_t stg, int r, int sl, int c, uint32_t (&m)[4]) {
   }
 }
 
-template <int BITS, int G, int NT>
+template <int BITS, int G, int NT, bool GATED = false>
 __global__ void __launch_bounds__(GEMV_MT_THREADS, 2)
     gemv_f16_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_meta,
                     const __grid_constant__ CUtensorMap map_x, GemvF16Params p) {
@@ -153,9 +154,9 @@ __global__ void __launch_bounds__(GEMV_MT_THREADS, 2)
         mbar_arrive_expect_tx(bar_full(s), L::TX);
 #pragma unroll
         for (int bx = 0; bx < L::CODE_BOXES; ++bx)
-          tma_load_2d(st + bx * 64 * L::CODE_BOX, &map_codes, bar_full(s), (sb0 + i) * L::CODE_ROW + bx * L::CODE_BOX,
-                      (int32_t)(rg * 64));
-        tma_load_2d(st + L::ST_META, &map_meta, bar_full(s), (sb0 + i) * L::META_ROW, (int32_t)(rg * 64));
+          load_group_box<GATED>(st + bx * 64 * L::CODE_BOX, &map_codes, bar_full(s),
+                                (sb0 + i) * L::CODE_ROW + bx * L::CODE_BOX, rg, p.N, L::CODE_BOX);
+        load_group_box<GATED>(st + L::ST_META, &map_meta, bar_full(s), (sb0 + i) * L::META_ROW, rg, p.N, L::META_ROW);
       };
       auto issue_x = [&](int i, int s) {
         const uint32_t st = sbase + s * L::STAGE;
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(GEMV_MT_THREADS, 2)
   } else {  // consumers: warp w owns box rows 16w + g and 16w + g + 8
     const int g = lane >> 2, c = lane & 3;
     const int r0 = 16 * warp + g, r1 = r0 + 8;
-    const int64_t n0 = rg * 64 + r0, n1 = n0 + 8;
+    const int64_t n0 = group_row<GATED>(rg, r0, p.N), n1 = n0 + 8;
     // the rows' weight exponents: lane c takes groups c, c + 4, .. of rows n0, n1 (rows past N read
     // row N - 1; their sums are never stored), the four lanes of a row combine by shuffles
     constexpr int NG = 256 / G;
@@ -276,6 +277,13 @@ __global__ void __launch_bounds__(GEMV_MT_THREADS, 2)
         if (lane == 0) mbar_arrive(bar_empty(s));
       }
     }
+    float *mine = p.ws.partial + (int64_t)blockIdx.x * M * 64;
+    if constexpr (GATED) {
+      if (P == 1) {  // the sums meet in shared memory, once every stage has been read
+        consumer_sync();
+        mine = reinterpret_cast<float *>(smem);
+      }
+    }
     if (ok) {  // rows n0, n1 x tokens n*8 + 2c, n*8 + 2c + 1
       const float p0 = exp2i(-e0), p1 = exp2i(-e1);
 #pragma unroll
@@ -285,16 +293,23 @@ __global__ void __launch_bounds__(GEMV_MT_THREADS, 2)
           const int t = n * 8 + 2 * c + h;
           if (t >= M) continue;
           const float v0 = (D[0][n][h] + D[1][n][h]) * p0, v1 = (D[0][n][2 + h] + D[1][n][2 + h]) * p1;
-          if (P == 1) {
+          if (P == 1 && !GATED) {
             const float xs = exp2i(__ldg(p.xexp + t));
             if (n0 < p.N) p.y[(int64_t)t * p.N + n0] = __float2bfloat16_rn(fmaf(v0, xs, bias_at(p.bias, n0)));
             if (n1 < p.N) p.y[(int64_t)t * p.N + n1] = __float2bfloat16_rn(fmaf(v1, xs, bias_at(p.bias, n1)));
           } else {
-            float *mine = p.ws.partial + (int64_t)blockIdx.x * M * 64;
             mine[t * 64 + r0] = v0;
             mine[t * 64 + r1] = v1;
           }
         }
+      }
+    }
+    if constexpr (GATED) {
+      if (P == 1) {
+        consumer_sync();
+        if (!*abort_flag)
+          gated_finish([&](int tk, int r) { return mine[tk * 64 + r] * exp2i(__ldg(p.xexp + tk)); }, rg, p.N / 2, M,
+                       p.act, p.y);
       }
     }
   }
@@ -304,13 +319,23 @@ __global__ void __launch_bounds__(GEMV_MT_THREADS, 2)
     __syncthreads();  // thread 0's acquire precedes the reads of the other parts
     if (flags[1] && warp < GEMV_MT_WARPS) {
       const float *pbase = p.ws.partial + first * M * 64;
-      for (int e = threadIdx.x; e < M * 64; e += GEMV_MT_WARPS * 32) {
-        const int tk = e >> 6, r = e & 63;
-        float sum = 0.f;
-        for (int q = 0; q < P; ++q) sum += __ldcg(pbase + (int64_t)q * M * 64 + e);
-        const int64_t n = rg * 64 + r;
-        if (n < p.N)
-          p.y[(int64_t)tk * p.N + n] = __float2bfloat16_rn(fmaf(sum, exp2i(__ldg(p.xexp + tk)), bias_at(p.bias, n)));
+      if constexpr (GATED) {
+        gated_finish(
+            [&](int tk, int r) {
+              float sum = 0.f;
+              for (int q = 0; q < P; ++q) sum += __ldcg(pbase + ((int64_t)q * M + tk) * 64 + r);
+              return sum * exp2i(__ldg(p.xexp + tk));
+            },
+            rg, p.N / 2, M, p.act, p.y);
+      } else {
+        for (int e = threadIdx.x; e < M * 64; e += GEMV_MT_WARPS * 32) {
+          const int tk = e >> 6, r = e & 63;
+          float sum = 0.f;
+          for (int q = 0; q < P; ++q) sum += __ldcg(pbase + (int64_t)q * M * 64 + e);
+          const int64_t n = rg * 64 + r;
+          if (n < p.N)
+            p.y[(int64_t)tk * p.N + n] = __float2bfloat16_rn(fmaf(sum, exp2i(__ldg(p.xexp + tk)), bias_at(p.bias, n)));
+        }
       }
     }
   }

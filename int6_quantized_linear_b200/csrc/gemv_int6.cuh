@@ -202,7 +202,8 @@ struct Gemv6Params {
   int M;  // 1 .. TM tokens
   SplitK split;  // of K over the CTAs of the grid, per 64-row group
   GemvWorkspace ws;
-  __nv_bfloat16 *y;
+  __nv_bfloat16 *y;  // [M][N]; gated: h [M][N / 2]
+  int act;           // gated only
 };
 
 // The low bytes of 24-bit x for one consumer warp of the int6 kernel: S G 2^-8 D_lo per (row, token,
@@ -285,7 +286,7 @@ __device__ __noinline__ Int6LowBytes<TM> gemv_int6_low_bytes(const uint8_t *code
   return out;
 }
 
-template <int TM, bool PLANAR>
+template <int TM, bool PLANAR, bool GATED = false>
 __global__ void __launch_bounds__(GEMV6_THREADS, GEMV6_CTAS_PER_SM)
     gemv_int6_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_sc,
                      Gemv6Params p) {
@@ -336,8 +337,8 @@ __global__ void __launch_bounds__(GEMV6_THREADS, GEMV6_CTAS_PER_SM)
       auto issue_w = [&](int i, int s) {
         const uint32_t st = sbase + s * L::STAGE;
         mbar_arrive_expect_tx(bar_full(s), tx);
-        tma_load_2d(st, &map_codes, bar_full(s), (sb0 + i) * 192, (int32_t)(rg * 64));
-        tma_load_2d(st + L::ST_SC, &map_sc, bar_full(s), (sb0 + i) * 16, (int32_t)(rg * 64));
+        load_group_box<GATED>(st, &map_codes, bar_full(s), (sb0 + i) * 192, rg, p.N, GEMV6_CODE_ROW);
+        load_group_box<GATED>(st + L::ST_SC, &map_sc, bar_full(s), (sb0 + i) * 16, rg, p.N, 16);
       };
       auto issue_x = [&](int i, int s) {
         const uint32_t st = sbase + s * L::STAGE;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(GEMV6_THREADS, GEMV6_CTAS_PER_SM)
   } else {  // consumers: warp w owns box rows 16w + g and 16w + g + 8
     const int g = lane >> 2, c = lane & 3;
     const int r0 = 16 * warp + g, r1 = r0 + 8;
-    const int64_t n0 = rg * 64 + r0, n1 = n0 + 8;
+    const int64_t n0 = group_row<GATED>(rg, r0, p.N), n1 = n0 + 8;
     const int64_t c0 = n0 < p.N ? n0 : p.N - 1, c1 = n1 < p.N ? n1 : p.N - 1;
     const uint16_t *st0 = p.steps + c0 * NS + sb0, *st1 = p.steps + c1 * NS + sb0;
     uint32_t sr0[RING], sr1[RING];  // step bits by stage, RING - 1 super-blocks ahead
@@ -519,19 +520,32 @@ __global__ void __launch_bounds__(GEMV6_THREADS, GEMV6_CTAS_PER_SM)
         acc[m][r] += __shfl_xor_sync(0xffffffffu, acc[m][r], 2);
       }
     }
+    float *sums = p.ws.partial + (int64_t)blockIdx.x * M * 64;
+    if constexpr (GATED) {
+      if (P == 1) {  // the sums meet in shared memory, once every stage has been read
+        consumer_sync();
+        sums = reinterpret_cast<float *>(smem);
+      }
+    }
     if (ok) {
 #pragma unroll
       for (int m = 0; m < TM; ++m) {
         if (m < M && (m & 3) == c) {  // lane c publishes tokens c, c + 4
-          if (P == 1) {
+          if (P == 1 && !GATED) {
             if (n0 < p.N) p.y[(int64_t)m * p.N + n0] = __float2bfloat16_rn(acc[m][0] + bias_at(p.bias, n0));
             if (n1 < p.N) p.y[(int64_t)m * p.N + n1] = __float2bfloat16_rn(acc[m][1] + bias_at(p.bias, n1));
           } else {
-            float *mine = p.ws.partial + ((int64_t)blockIdx.x * M + m) * 64;
+            float *mine = sums + m * 64;
             mine[r0] = acc[m][0];
             mine[r1] = acc[m][1];
           }
         }
+      }
+    }
+    if constexpr (GATED) {
+      if (P == 1) {
+        consumer_sync();
+        if (!*abort_flag) gated_finish([&](int tk, int r) { return sums[tk * 64 + r]; }, rg, p.N / 2, M, p.act, p.y);
       }
     }
   }
@@ -541,12 +555,22 @@ __global__ void __launch_bounds__(GEMV6_THREADS, GEMV6_CTAS_PER_SM)
     __syncthreads();  // thread 0's acquire precedes the reads of the other parts
     if (flags[1] && warp < GEMV6_WARPS) {
       const float *base = p.ws.partial + first * M * 64;
-      for (int e = threadIdx.x; e < M * 64; e += GEMV6_WARPS * 32) {
-        const int tk = e >> 6, r = e & 63;
-        float sum = 0.f;
-        for (int q = 0; q < P; ++q) sum += __ldcg(base + (int64_t)q * M * 64 + e);
-        const int64_t n = rg * 64 + r;
-        if (n < p.N) p.y[(int64_t)tk * p.N + n] = __float2bfloat16_rn(sum + bias_at(p.bias, n));
+      if constexpr (GATED) {
+        gated_finish(
+            [&](int tk, int r) {
+              float sum = 0.f;
+              for (int q = 0; q < P; ++q) sum += __ldcg(base + ((int64_t)q * M + tk) * 64 + r);
+              return sum;
+            },
+            rg, p.N / 2, M, p.act, p.y);
+      } else {
+        for (int e = threadIdx.x; e < M * 64; e += GEMV6_WARPS * 32) {
+          const int tk = e >> 6, r = e & 63;
+          float sum = 0.f;
+          for (int q = 0; q < P; ++q) sum += __ldcg(base + (int64_t)q * M * 64 + e);
+          const int64_t n = rg * 64 + r;
+          if (n < p.N) p.y[(int64_t)tk * p.N + n] = __float2bfloat16_rn(sum + bias_at(p.bias, n));
+        }
       }
     }
   }

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "../../include/qlinear.h"
+#include "gemm_dx.cuh"
 #include "gemm_sm100.cuh"
 #include "gemv.cuh"
 #include "gemv_int6.cuh"
@@ -167,9 +168,31 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint6
   return true;
 }
 
-template <int FMT, int BITS, int TT, int CPS = 1>
+// Row tiles of the GEMM: 128 rows, or 64 features of the gated form (64 gate rows and 64 up rows).
+template <bool GATED>
+inline int64_t gemm_row_tiles(int64_t N) {
+  return GATED ? (N / 2 + gemm::GATED_F - 1) / gemm::GATED_F : (N + gemm::BN - 1) / gemm::BN;
+}
+
+// Row groups of the GEMVs, one CTA's rows: 64 rows, or 32 features of the gated form; its code and
+// group-word boxes then have 32 rows.
+template <bool GATED>
+inline int64_t gemv_row_groups(int64_t N) {
+  return GATED ? (N / 2 + GATED_ROWS - 1) / GATED_ROWS : (N + 63) / 64;
+}
+template <bool GATED>
+constexpr uint32_t gemv_box_rows() { return GATED ? GATED_ROWS : 64; }
+
+// What the gated forms of the launches take besides the layer's arguments (y is then h [M][N / 2]).
+struct GatedArgs {
+  int act = ACT_SILU;
+  int8_t *saved = nullptr;  // checkpoint of (g, u), or NULL (the GEMM forms write it)
+  uint8_t *saved_exps = nullptr;
+};
+
+template <int FMT, int BITS, int TT, int CPS = 1, bool GATED = false>
 ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, const void *bias,
-                         void *y, void *workspace, cudaStream_t st, int sms) {
+                         void *y, void *workspace, cudaStream_t st, int sms, const GatedArgs &ga) {
   using namespace ql::gemm;
   const int64_t N = d->N, K = d->K;
   const uint64_t row_bytes = (uint64_t)K * code_bits(FMT, BITS) / 8;
@@ -200,7 +223,8 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
   // int6 planar: a k-step's codes are three 16-byte pieces of its super-block (two of the low plane,
   // one of the high plane), loaded as three boxes of 16 bytes x BN rows
   if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes,
-                 FMT == FMT_INT6P ? 16u : (uint32_t)p_row_bytes(FMT, BITS), BN, CU_TENSOR_MAP_SWIZZLE_NONE))
+                 FMT == FMT_INT6P ? 16u : (uint32_t)p_row_bytes(FMT, BITS), GATED ? GATED_F : BN,
+                 CU_TENSOR_MAP_SWIZZLE_NONE))
     return cuda_failed();
   Params p;
   p.M = M; p.N = N; p.K = K; p.G = d->group;
@@ -209,8 +233,11 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
   p.steps = static_cast<const uint8_t *>(w->steps);
   p.y = static_cast<__nv_bfloat16 *>(y);
   p.ws = ws;
+  p.act = ga.act;
+  p.saved = ga.saved;
+  p.saved_exps = ga.saved_exps;
   const int smem = smem_bytes(FMT, BITS, TT);
-  auto kern = gemm_kernel<FMT, BITS, TT, CPS>;
+  auto kern = gemm_kernel<FMT, BITS, TT, CPS, GATED>;
   static thread_local int configured_dev = -1;  // per (kernel instantiation, thread)
   int dev = 0;
   cudaGetDevice(&dev);
@@ -219,7 +246,7 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
       return cuda_failed();
     configured_dev = dev;
   }
-  const int64_t tiles = ((M + TT - 1) / TT) * ((N + BN - 1) / BN);
+  const int64_t tiles = ((M + TT - 1) / TT) * gemm_row_tiles<GATED>(N);
   const int slots = CPS * sms;
   const int grid = (int)(tiles < slots ? tiles : slots);
   cudaLaunchConfig_t cfg = {};
@@ -237,15 +264,15 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
 // when the layer has more 128-row tiles than SMs (every tile then runs at once instead of some SMs
 // taking two in turn); from 33 tokens: tiles of 256 tokens.  Both take 128 weight rows as the MMA's
 // M = 128 operand.
-template <int FMT, int BITS>
+template <int FMT, int BITS, bool GATED = false>
 ql_status launch_gemm(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, const void *bias,
-                      void *y, void *workspace, cudaStream_t st, int sms) {
+                      void *y, void *workspace, cudaStream_t st, int sms, const GatedArgs &ga = {}) {
   if (M <= gemm::TT_SMALL) {
-    if ((d->N + gemm::BN - 1) / gemm::BN > sms)
-      return launch_gemm_tt<FMT, BITS, gemm::TT_SMALL, 2>(d, w, x, M, bias, y, workspace, st, sms);
-    return launch_gemm_tt<FMT, BITS, gemm::TT_SMALL>(d, w, x, M, bias, y, workspace, st, sms);
+    if (gemm_row_tiles<GATED>(d->N) > sms)
+      return launch_gemm_tt<FMT, BITS, gemm::TT_SMALL, 2, GATED>(d, w, x, M, bias, y, workspace, st, sms, ga);
+    return launch_gemm_tt<FMT, BITS, gemm::TT_SMALL, 1, GATED>(d, w, x, M, bias, y, workspace, st, sms, ga);
   }
-  return launch_gemm_tt<FMT, BITS, gemm::BM>(d, w, x, M, bias, y, workspace, st, sms);
+  return launch_gemm_tt<FMT, BITS, gemm::BM, 1, GATED>(d, w, x, M, bias, y, workspace, st, sms, ga);
 }
 
 // Affine layers the tensor-core GEMVs serve: group 32 or 64, K a multiple of 256 (the integer
@@ -266,17 +293,14 @@ inline size_t gemv_call_workspace_bytes(const ql_desc *d, int64_t M) {
   return own > gemm ? own : gemm;
 }
 
-template <int FMT, int BITS>
-ql_status launch_gemm(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, const void *bias,
-                      void *y, void *workspace, cudaStream_t st, int sms);
-
 // Multi-token tensor-core GEMV (int4 at 2..8 tokens; 2-, 4- and 8-bit affine with group 32 or 64 at
 // 1..8 tokens): x preparation, then the streaming kernel as its programmatic dependent.
-template <int FMT, int BITS, int G>
+template <int FMT, int BITS, int G, bool GATED>
 ql_status launch_gemv_mt(const ql_desc *d, const ql_packed_const *w, const __nv_bfloat16 *xb, int64_t M,
-                         const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms) {
+                         const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms,
+                         int act) {
   using L = MtLayout<FMT, BITS, G>;
-  const int64_t N = d->N, K = d->K, NS = K / 256, TG = (N + 63) / 64;
+  const int64_t N = d->N, K = d->K, NS = K / 256, TG = gemv_row_groups<GATED>(N);
   const GemvWorkspace ws = gemv_workspace_carve(workspace, M, N, K);
   cudaLaunchAttribute pa[1];
   pa[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -305,17 +329,18 @@ ql_status launch_gemv_mt(const ql_desc *d, const ql_packed_const *w, const __nv_
   if (p.split.P + (p.split.extra > 0) > 1 && ctas > GEMV_MT_MAX_CTAS) return QL_ERR_RANGE;  // partial sums' room
   p.ws = ws;
   p.y = yb;
+  p.act = act;
   const uint64_t code_row = FMT == FMT_INT4 ? (uint64_t)K / 2 : (uint64_t)K * BITS / 8;
   const uint64_t meta_row = FMT == FMT_INT4 ? (uint64_t)K / 16 : (uint64_t)K / G * 4;
   CUtensorMap mc, mg;  // codes: boxes of 64 rows x CODE_BOX bytes, swizzled; group words: 64 rows x META_ROW
-  if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, code_row, (uint64_t)N, code_row, L::CODE_BOX, 64,
+  if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, code_row, (uint64_t)N, code_row, L::CODE_BOX, gemv_box_rows<GATED>(),
                  L::CODE_BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !encode_2d(&mg, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->gmeta, meta_row, (uint64_t)N, meta_row, L::META_ROW, 64,
+      !encode_2d(&mg, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->gmeta, meta_row, (uint64_t)N, meta_row, L::META_ROW, gemv_box_rows<GATED>(),
                  CU_TENSOR_MAP_SWIZZLE_NONE))
     return cuda_failed();
   auto kern = [] {
-    if constexpr (FMT == FMT_INT4) return gemv_mt_int4_kernel;
-    else return gemv_mt_affine_kernel<BITS, G>;
+    if constexpr (FMT == FMT_INT4) return gemv_mt_int4_kernel<GATED>;
+    else return gemv_mt_affine_kernel<BITS, G, GATED>;
   }();
   static thread_local int configured_dev = -1;  // per instantiation and thread
   int dev = 0;
@@ -337,11 +362,12 @@ ql_status launch_gemv_mt(const ql_desc *d, const ql_packed_const *w, const __nv_
 }
 
 // Tensor-core int6 GEMV at 1..TM tokens: x preparation, then the streaming kernel as its dependent.
-template <int TM, bool PLANAR>
+template <int TM, bool PLANAR, bool GATED>
 ql_status launch_gemv_int6(const ql_desc *d, const ql_packed_const *w, const __nv_bfloat16 *xb, int64_t M,
-                           const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms) {
+                           const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms,
+                           int act) {
   using L = Int6Layout<TM>;
-  const int64_t N = d->N, K = d->K, NS = K / 256, TG = (N + 63) / 64;
+  const int64_t N = d->N, K = d->K, NS = K / 256, TG = gemv_row_groups<GATED>(N);
   const GemvWorkspace ws = gemv_workspace_carve(workspace, M, N, K);
   // split K over the CTAs of a 64-row group so that the groups fill one wave of resident CTAs
   const SplitK split = split_k(TG, (int64_t)sms * GEMV6_CTAS_PER_SM, NS, true);
@@ -374,14 +400,16 @@ ql_status launch_gemv_int6(const ql_desc *d, const ql_packed_const *w, const __n
   p.split = split;
   p.ws = ws;
   p.y = yb;
+  p.act = act;
   const uint64_t code_row = (uint64_t)K * 3 / 4, sc_row = (uint64_t)K / 16;
   CUtensorMap mc, ms;  // codes: 64 rows x 208 bytes (a super-block and 16 bytes more); scale codes: 64 x 16 B
-  if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, code_row, (uint64_t)N, code_row, GEMV6_CODE_ROW, 64,
+  if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, code_row, (uint64_t)N, code_row, GEMV6_CODE_ROW,
+                 gemv_box_rows<GATED>(),
                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->gmeta, sc_row, (uint64_t)N, sc_row, 16, 64,
+      !encode_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->gmeta, sc_row, (uint64_t)N, sc_row, 16, gemv_box_rows<GATED>(),
                  CU_TENSOR_MAP_SWIZZLE_NONE))
     return cuda_failed();
-  auto kern = gemv_int6_kernel<TM, PLANAR>;
+  auto kern = gemv_int6_kernel<TM, PLANAR, GATED>;
   static thread_local int configured_dev = -1;  // per instantiation and thread
   int dev = 0;
   cudaGetDevice(&dev);
@@ -405,11 +433,12 @@ ql_status launch_gemv_int6(const ql_desc *d, const ql_packed_const *w, const __n
 // exponent per token, programmatic dependent of what precedes it), then the streaming kernel as its
 // dependent.  x16 and the token exponents sit at the start of the workspace (the GEMM's layout), the
 // partial sums and counters of a K split where the GEMV layout has them (past 7 M K bytes).
-template <int BITS, int G, int NT>
+template <int BITS, int G, int NT, bool GATED>
 ql_status launch_gemv_f16(const ql_desc *d, const ql_packed_const *w, const __nv_bfloat16 *xb, int64_t M,
-                          const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms) {
+                          const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms,
+                          int act) {
   using L = F16Layout<BITS, G, NT>;
-  const int64_t N = d->N, K = d->K, NS = K / 256, TG = (N + 63) / 64;
+  const int64_t N = d->N, K = d->K, NS = K / 256, TG = gemv_row_groups<GATED>(N);
   const GemmWorkspace gw = gemm_workspace_carve(workspace, M, N, K);
   const GemvWorkspace vw = gemv_workspace_carve(workspace, M, N, K);
   const SplitK split = split_k(TG, (int64_t)sms * L::CTAS, NS, false);
@@ -441,16 +470,17 @@ ql_status launch_gemv_f16(const ql_desc *d, const ql_packed_const *w, const __nv
   p.split = split;
   p.ws = vw;
   p.y = yb;
+  p.act = act;
   const uint64_t code_row = (uint64_t)K * BITS / 8, meta_row = (uint64_t)K / G * 4;
   CUtensorMap mc, mg, mx;  // codes: 64 rows x CODE_BOX bytes, swizzled; group words: 64 x META_ROW; x: 8 NT x 32 halves
-  if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, code_row, (uint64_t)N, code_row, L::CODE_BOX, 64,
+  if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, code_row, (uint64_t)N, code_row, L::CODE_BOX, gemv_box_rows<GATED>(),
                  L::CODE_BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !encode_2d(&mg, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->gmeta, meta_row, (uint64_t)N, meta_row, L::META_ROW, 64,
+      !encode_2d(&mg, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->gmeta, meta_row, (uint64_t)N, meta_row, L::META_ROW, gemv_box_rows<GATED>(),
                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, gw.x16, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, 32,
                  (uint32_t)L::XROWS, CU_TENSOR_MAP_SWIZZLE_64B))
     return cuda_failed();
-  auto kern = gemv_f16_kernel<BITS, G, NT>;
+  auto kern = gemv_f16_kernel<BITS, G, NT, GATED>;
   static thread_local int configured_dev = -1;  // per instantiation and thread
   int dev = 0;
   cudaGetDevice(&dev);
@@ -472,12 +502,13 @@ ql_status launch_gemv_f16(const ql_desc *d, const ql_packed_const *w, const __nv
 
 // M = 1 on the diagonal-x kernel (int4, or 4-bit affine with group 32 / 64): each CTA converts its part
 // of x, then streams four 16-row tiles over it (+ the kernel that adds the parts when K is split)
-template <int FMT, int G>
+template <int FMT, int G, bool GATED>
 ql_status launch_gemv_m1(const ql_desc *d, const ql_packed_const *w, const __nv_bfloat16 *xb,
-                         const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms) {
+                         const __nv_bfloat16 *bb, __nv_bfloat16 *yb, void *workspace, cudaStream_t st, int sms,
+                         int act) {
   using L = M1Layout<FMT, G>;
   const int64_t M = 1;
-  const int64_t NS = d->K / 256, n_tiles = (d->N + 15) / 16, groups = (n_tiles + GEMV_WARPS - 1) / GEMV_WARPS;
+  const int64_t NS = d->K / 256, groups = gemv_row_groups<GATED>(d->N);
   // split K so that the tile groups fill the resident CTA slots, and so that each part's x fits the
   // CTA's blocks; the parts' sums go through the workspace (16 floats a tile and part)
   int64_t P = std::max<int64_t>(1, std::min<int64_t>(NS, (int64_t)sms * GEMV_CTAS_PER_SM / groups));
@@ -495,6 +526,7 @@ ql_status launch_gemv_m1(const ql_desc *d, const ql_packed_const *w, const __nv_
   p.P = (int)P;
   p.partial = ws.partial;
   p.y = yb;
+  p.act = act;
   const uint64_t gm_row = (uint64_t)NS * L::GM_ROW;  // group-word bytes a row
   CUtensorMap mc, mg;  // codes as [N][K/2] bytes, boxes of 16 rows x 128 bytes, 128-byte swizzle;
                        // group words as [N][gm_row] bytes, boxes of 16 rows x GM_ROW bytes
@@ -503,7 +535,10 @@ ql_status launch_gemv_m1(const ql_desc *d, const ql_packed_const *w, const __nv_
       !encode_2d(&mg, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->gmeta, gm_row, (uint64_t)d->N, gm_row, L::GM_ROW, 16,
                  CU_TENSOR_MAP_SWIZZLE_NONE))
     return cuda_failed();
-  auto kern = FMT == FMT_INT4 ? gemv_int4_m1_tc_kernel : gemv_affine4_m1_tc_kernel<G>;
+  auto kern = [] {
+    if constexpr (FMT == FMT_INT4) return gemv_int4_m1_tc_kernel<GATED>;
+    else return gemv_affine4_m1_tc_kernel<G, GATED>;
+  }();
   static thread_local int configured_dev = -1;  // per instantiation and thread
   int dev = 0;
   cudaGetDevice(&dev);
@@ -530,52 +565,61 @@ ql_status launch_gemv_m1(const ql_desc *d, const ql_packed_const *w, const __nv_
     rc.stream = st;
     rc.attrs = attr;
     rc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&rc, gemv_m1_sum_parts, (const float *)ws.partial, (int)P, (int64_t)d->N, bb, yb) !=
-        cudaSuccess)
+    if constexpr (GATED) {
+      rc.gridDim = dim3((unsigned)((d->N / 2 + 255) / 256));
+      if (cudaLaunchKernelEx(&rc, gemv_m1_sum_parts_gated, (const float *)ws.partial, (int)P, (int64_t)(d->N / 2),
+                             act, yb) != cudaSuccess)
+        return cuda_failed();
+    } else if (cudaLaunchKernelEx(&rc, gemv_m1_sum_parts, (const float *)ws.partial, (int)P, (int64_t)d->N, bb, yb) !=
+               cudaSuccess) {
       return cuda_failed();
+    }
   }
   return launched();
 }
 
-template <int FMT, int BITS>
+template <int FMT, int BITS, bool GATED = false>
 ql_status launch_gemv(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, const void *bias,
-                      void *y, void *workspace, cudaStream_t st, int sms) {
+                      void *y, void *workspace, cudaStream_t st, int sms, int act = ACT_SILU) {
   const auto *xb = static_cast<const __nv_bfloat16 *>(x);
   auto *yb = static_cast<__nv_bfloat16 *>(y);
   const auto *bb = static_cast<const __nv_bfloat16 *>(bias);
-  if (gemv_runs_on_gemm(d, M)) return launch_gemm<FMT, BITS>(d, w, x, M, bias, y, workspace, st, sms);
+  if constexpr (!GATED) {
+    if (gemv_runs_on_gemm(d, M)) return launch_gemm<FMT, BITS>(d, w, x, M, bias, y, workspace, st, sms);
+  }
   if constexpr (FMT == FMT_INT4) {
-    if (M >= 2) return launch_gemv_mt<FMT_INT4, 4, 32>(d, w, xb, M, bb, yb, workspace, st, sms);
+    if (M >= 2) return launch_gemv_mt<FMT_INT4, 4, 32, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
   }
   if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {  // M <= 8; dense or planar code storage
     constexpr bool PL = FMT == FMT_INT6P;
-    if (M == 1) return launch_gemv_int6<1, PL>(d, w, xb, M, bb, yb, workspace, st, sms);
-    if (M == 2) return launch_gemv_int6<2, PL>(d, w, xb, M, bb, yb, workspace, st, sms);
-    if (M <= 4) return launch_gemv_int6<4, PL>(d, w, xb, M, bb, yb, workspace, st, sms);
-    return launch_gemv_int6<8, PL>(d, w, xb, M, bb, yb, workspace, st, sms);
+    if (M == 1) return launch_gemv_int6<1, PL, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
+    if (M == 2) return launch_gemv_int6<2, PL, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
+    if (M <= 4) return launch_gemv_int6<4, PL, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
+    return launch_gemv_int6<8, PL, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
   }
   if constexpr (FMT == FMT_AFFINE) {  // bits 2, 4, 8
     if constexpr (BITS == 4) {  // one token: the diagonal-x kernel of int4 (the same nibble layout)
       if (affine_tc(d) && M == 1)
-        return d->group == 64 ? launch_gemv_m1<FMT_AFFINE, 64>(d, w, xb, bb, yb, workspace, st, sms)
-                              : launch_gemv_m1<FMT_AFFINE, 32>(d, w, xb, bb, yb, workspace, st, sms);
+        return d->group == 64 ? launch_gemv_m1<FMT_AFFINE, 64, GATED>(d, w, xb, bb, yb, workspace, st, sms, act)
+                              : launch_gemv_m1<FMT_AFFINE, 32, GATED>(d, w, xb, bb, yb, workspace, st, sms, act);
     }
     if (affine_tc(d) && M <= 8) {
-      if (d->group == 64) return launch_gemv_mt<FMT_AFFINE, BITS, 64>(d, w, xb, M, bb, yb, workspace, st, sms);
-      return launch_gemv_mt<FMT_AFFINE, BITS, 32>(d, w, xb, M, bb, yb, workspace, st, sms);
+      if (d->group == 64)
+        return launch_gemv_mt<FMT_AFFINE, BITS, 64, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
+      return launch_gemv_mt<FMT_AFFINE, BITS, 32, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
     }
     if (affine_tc(d)) {  // 9..32 tokens
       if (d->group == 64)
-        return M <= 16 ? launch_gemv_f16<BITS, 64, 2>(d, w, xb, M, bb, yb, workspace, st, sms)
-                       : launch_gemv_f16<BITS, 64, 4>(d, w, xb, M, bb, yb, workspace, st, sms);
-      return M <= 16 ? launch_gemv_f16<BITS, 32, 2>(d, w, xb, M, bb, yb, workspace, st, sms)
-                     : launch_gemv_f16<BITS, 32, 4>(d, w, xb, M, bb, yb, workspace, st, sms);
+        return M <= 16 ? launch_gemv_f16<BITS, 64, 2, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act)
+                       : launch_gemv_f16<BITS, 64, 4, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
+      return M <= 16 ? launch_gemv_f16<BITS, 32, 2, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act)
+                     : launch_gemv_f16<BITS, 32, 4, GATED>(d, w, xb, M, bb, yb, workspace, st, sms, act);
     }
   }
   if constexpr (FMT == FMT_INT4) {
-    if (M == 1) return launch_gemv_m1<FMT_INT4, 32>(d, w, xb, bb, yb, workspace, st, sms);
+    if (M == 1) return launch_gemv_m1<FMT_INT4, 32, GATED>(d, w, xb, bb, yb, workspace, st, sms, act);
   }
-  if constexpr (FMT == FMT_AFFINE) {  // groups without the multi-token kernel, M < 8: CUDA cores
+  if constexpr (FMT == FMT_AFFINE && !GATED) {  // groups without the multi-token kernel, M < 8: CUDA cores
     const WeightPtrs p = make_ptrs(d, w);
     const int64_t rows_per_block = 8;
     int64_t g = (d->N + rows_per_block - 1) / rows_per_block;
@@ -591,8 +635,109 @@ ql_status launch_gemv(const ql_desc *d, const ql_packed_const *w, const void *x,
       gemv_simple_kernel<FMT, BITS, 8><<<(int)g, 256, 0, st>>>(p, d->N, xb, (int)M, bb, yb);
     return launched();
   } else {
-    return QL_ERR_UNSUPPORTED;  // int4 and int6 returned above for every M in range
+    return QL_ERR_UNSUPPORTED;  // int4 and int6 returned above for every M in range, gated affine does not come here
   }
+}
+
+// The gated block: decode-shaped calls on the GEMVs, the rest -- and every call that saves a checkpoint,
+// and affine layers without a tensor-core GEMV -- on the GEMM.
+inline bool gated_runs_on_gemv(const ql_desc *d, int64_t M, bool saves) {
+  return !saves && M <= (d->fmt == QL_AFFINE_U32 ? 32 : 8) && (d->fmt != QL_AFFINE_U32 || affine_tc(d));
+}
+
+// covers the call with and without a checkpoint
+inline size_t gated_workspace_bytes(const ql_desc *d, int64_t M) {
+  const size_t gemm = gemm_workspace_bytes(M, d->N, d->K);
+  const size_t gemv = gated_runs_on_gemv(d, M, false) ? gemv_workspace_bytes(M, d->N, d->K) : 0;
+  return gemv > gemm ? gemv : gemm;
+}
+
+template <int FMT, int BITS>
+ql_status launch_gated(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, void *h,
+                       void *workspace, cudaStream_t st, int sms, const GatedArgs &ga) {
+  if (gated_runs_on_gemv(d, M, ga.saved != nullptr))
+    return launch_gemv<FMT, BITS, true>(d, w, x, M, nullptr, h, workspace, st, sms, ga.act);
+  return launch_gemm<FMT, BITS, true>(d, w, x, M, nullptr, h, workspace, st, sms, ga);
+}
+
+}  // namespace
+
+// ---- the input gradient ------------------------------------------------------
+namespace {
+
+// The three passes after dy has been prepared by `prep` (pass 2, which reads pass 1's row exponents).
+template <int FMT, int BITS, int TT, class Prep>
+ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t M, void *dx_out, void *workspace,
+                            cudaStream_t st, int sms, const Prep &prep) {
+  using namespace ql::dx;
+  const int64_t N = d->N, K = d->K, np = padded_n(N);
+  const int gr = gran(FMT, d->group);
+  const Workspace ws = carve(workspace, M, N, K, gr);
+  w_prep_kernel<FMT, BITS><<<(unsigned)(np / WP_ROWS), 256, 0, st>>>(
+      static_cast<const uint8_t *>(w->gmeta), static_cast<const uint8_t *>(w->steps), N, K, d->group, np, ws);
+  prep(ws, np);
+  const uint64_t row_bytes = (uint64_t)K * gemm::code_bits(FMT, BITS) / 8;
+  CUtensorMap my, mc, mh, mm;
+  constexpr bool PLANAR = FMT == FMT_INT6P;
+  constexpr uint32_t box = PLANAR ? 64u : (uint32_t)code_row(FMT, BITS);
+  constexpr CUtensorMapSwizzle sw = box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+  if (!encode_2d(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.dy16, (uint64_t)np, (uint64_t)M, (uint64_t)np * 2, BN, TT,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes, box, BN, sw) ||
+      !encode_2d(&mm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws.meta, (uint64_t)np, (uint64_t)(K / gr), (uint64_t)np * 4, BN,
+                 gr >= BKT ? 1u : (uint32_t)(BKT / gr), CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cuda_failed();
+  mh = mc;
+  if (PLANAR && !encode_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes, 32, BN,
+                           CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cuda_failed();
+  Params p;
+  p.M = M; p.N = N; p.K = K; p.G = d->group;
+  p.deal = deal(M, N, K, TT, sms);
+  p.dexp = ws.dexp;
+  p.partial = ws.partial;
+  p.dx = static_cast<__nv_bfloat16 *>(dx_out);
+  constexpr int smem = smem_bytes(FMT, BITS, TT);
+  auto kern = gemm_dx_kernel<FMT, BITS, TT>;
+  static thread_local int configured_dev = -1;  // per instantiation and thread
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_dev != dev) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return cuda_failed();
+    configured_dev = dev;
+  }
+  kern<<<(unsigned)(p.deal.waves ? p.deal.ctas : p.deal.shares), num_threads(TT), smem, st>>>(my, mc, mh, mm, p);
+  if (p.deal.joins())
+    join_kernel<TT><<<dim3((unsigned)p.deal.rest, (unsigned)(M < TT ? M : TT)), BKT, 0, st>>>(p);
+  return launched();
+}
+
+template <int FMT, int BITS, class Prep>
+ql_status launch_gemm_dx(const ql_desc *d, const ql_packed_const *w, int64_t M, void *dx_out, void *workspace,
+                         cudaStream_t st, int sms, const Prep &prep) {
+  if (dx::token_tile(M) == dx::TT_SMALL)
+    return launch_gemm_dx_tt<FMT, BITS, dx::TT_SMALL>(d, w, M, dx_out, workspace, st, sms, prep);
+  return launch_gemm_dx_tt<FMT, BITS, dx::TT_LARGE>(d, w, M, dx_out, workspace, st, sms, prep);
+}
+
+template <class Prep>
+ql_status gemm_dx_call(const ql_desc *d, const ql_packed_const *w, int64_t M, void *dx_out, void *workspace,
+                       cudaStream_t s, int sms, const Prep &prep) {
+  switch (d->fmt) {
+    case QL_INT4_NSS: return launch_gemm_dx<FMT_INT4, 4>(d, w, M, dx_out, workspace, s, sms, prep);
+    case QL_INT6_SYM: return launch_gemm_dx<FMT_INT6, 6>(d, w, M, dx_out, workspace, s, sms, prep);
+    case QL_INT6_PLANAR: return launch_gemm_dx<FMT_INT6P, 6>(d, w, M, dx_out, workspace, s, sms, prep);
+    default:
+      if (d->bits == 2) return launch_gemm_dx<FMT_AFFINE, 2>(d, w, M, dx_out, workspace, s, sms, prep);
+      if (d->bits == 4) return launch_gemm_dx<FMT_AFFINE, 4>(d, w, M, dx_out, workspace, s, sms, prep);
+      return launch_gemm_dx<FMT_AFFINE, 8>(d, w, M, dx_out, workspace, s, sms, prep);
+  }
+}
+
+inline size_t gemm_dx_workspace(const ql_desc *d, int64_t M) {
+  return dx::workspace_bytes(M, d->N, d->K, d->fmt == QL_AFFINE_U32 ? d->group : 32);
 }
 
 }  // namespace
@@ -625,6 +770,37 @@ ql_status noalloc_scratch(void **out) {
   *out = g_noalloc_addr[dev];
   return QL_OK;
 }
+}  // namespace
+
+namespace {
+
+// A matrix to hold in 8 bits: at most 2^38 padded values, which one grid of 256-thread blocks covers.
+ql_status check_saved8(int64_t rows, int64_t cols) {
+  if (rows < 1 || cols < 1) return QL_ERR_SHAPE;
+  constexpr int64_t most = (int64_t)1 << 38;
+  if (cols > most || rows > most / save8_cols(cols)) return QL_ERR_RANGE;
+  return QL_OK;
+}
+
+// The layer of a gated block, its tokens and its activation.
+ql_status check_gated(const ql_desc *d, int64_t M, int32_t act) {
+  const ql_status st = check_desc(d);
+  if (st != QL_OK) return st;
+  if (d->N % 2 != 0 || d->K % gemm::BK != 0 || d->N > (int64_t)INT32_MAX) return QL_ERR_SHAPE;
+  if (act != QL_ACT_SILU && act != QL_ACT_GELU_TANH && act != QL_ACT_GELU) return QL_ERR_UNSUPPORTED;
+  if (M < 1 || M > (int64_t)INT32_MAX) return QL_ERR_RANGE;
+  return QL_OK;
+}
+
+// The layer and tokens of an input gradient.
+ql_status check_dx(const ql_desc *d, int64_t M) {
+  const ql_status st = check_desc(d);
+  if (st != QL_OK) return st;
+  if (d->N > (int64_t)INT32_MAX - 64 || d->K > (int64_t)INT32_MAX) return QL_ERR_SHAPE;
+  if (M < 1 || M > (int64_t)INT32_MAX) return QL_ERR_RANGE;
+  return QL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -943,6 +1119,143 @@ ql_status qlinear_quantize_meta(const ql_desc *d, const float *scale, const floa
   else
     quantize_meta_kernel<true, 16><<<dim3(blocks, 1), 256, 0, s>>>(scale, scale, N, G, c0, c0, s0, s0);
   return launched();
+}
+
+ql_status qlinear_saved8_bytes(int64_t rows, int64_t cols, size_t *codes_bytes, size_t *exps_bytes) {
+  if (!codes_bytes || !exps_bytes) return QL_ERR_NULL;
+  const ql_status st = check_saved8(rows, cols);
+  if (st != QL_OK) return st;
+  *codes_bytes = (size_t)rows * save8_cols(cols);
+  *exps_bytes = (size_t)rows * (save8_cols(cols) / 16);
+  return QL_OK;
+}
+
+ql_status qlinear_save8(const void *x, int64_t rows, int64_t cols, const ql_saved8 *out, ql_stream_t stream) {
+  ql_status st = check_saved8(rows, cols);
+  if (st != QL_OK) return st;
+  if (!x || !out || !out->codes || !out->exps) return QL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(out->codes) || !aligned16(out->exps)) return QL_ERR_ALIGN;
+  const auto *xb = static_cast<const __nv_bfloat16 *>(x);
+  auto *codes = static_cast<int8_t *>(out->codes);
+  auto *exps = static_cast<uint8_t *>(out->exps);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t groups = rows * (save8_cols(cols) / 16);
+  if (cols % 16 == 0) save8_kernel<<<(unsigned)((groups + 255) / 256), 256, 0, s>>>(xb, groups, codes, exps);
+  else save8_ragged_kernel<<<(unsigned)((groups * 16 + 255) / 256), 256, 0, s>>>(xb, rows, cols, codes, exps);
+  return launched();
+}
+
+ql_status qlinear_restore8(const ql_saved8_const *in, int64_t rows, int64_t cols, void *out, ql_stream_t stream) {
+  ql_status st = check_saved8(rows, cols);
+  if (st != QL_OK) return st;
+  if (!out || !in || !in->codes || !in->exps) return QL_ERR_NULL;
+  if (!aligned16(out) || !aligned16(in->codes) || !aligned16(in->exps)) return QL_ERR_ALIGN;
+  auto *ob = static_cast<__nv_bfloat16 *>(out);
+  const auto *codes = static_cast<const int8_t *>(in->codes);
+  const auto *exps = static_cast<const uint8_t *>(in->exps);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t groups = rows * (save8_cols(cols) / 16);
+  if (cols % 16 == 0) restore8_kernel<<<(unsigned)((groups + 255) / 256), 256, 0, s>>>(codes, exps, groups, ob);
+  else restore8_ragged_kernel<<<(unsigned)((groups * 16 + 255) / 256), 256, 0, s>>>(codes, exps, rows, cols, ob);
+  return launched();
+}
+
+ql_status qlinear_gated_workspace_bytes(const ql_desc *d, int64_t M, size_t *bytes) {
+  const ql_status st = check_gated(d, M, ACT_SILU);
+  if (st != QL_OK) return st;
+  if (!bytes) return QL_ERR_NULL;
+  *bytes = gated_workspace_bytes(d, M);
+  return QL_OK;
+}
+
+ql_status qlinear_gated(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, int32_t act, void *h,
+                        const ql_saved8 *saved, void *workspace, size_t workspace_bytes, ql_stream_t stream) {
+  ql_status st = check_gated(d, M, act);
+  if (st != QL_OK) return st;
+  if (!w || !x || !h || !workspace || (saved && (!saved->codes || !saved->exps))) return QL_ERR_NULL;
+  if ((st = check_packed(d, w->codes, w->gmeta, w->steps)) != QL_OK) return st;
+  if (!aligned16(x) || !aligned16(h) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return QL_ERR_ALIGN;
+  if (saved && (!aligned16(saved->codes) || !aligned16(saved->exps))) return QL_ERR_ALIGN;
+  if (workspace_bytes < gated_workspace_bytes(d, M)) return QL_ERR_SHAPE;
+  DeviceInfo *di;
+  if ((st = device_info(&di)) != QL_OK) return st;
+  if (di->major != 10) return QL_ERR_UNSUPPORTED;
+  GatedArgs ga;
+  ga.act = act;
+  if (saved) {
+    ga.saved = static_cast<int8_t *>(saved->codes);
+    ga.saved_exps = static_cast<uint8_t *>(saved->exps);
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (d->fmt) {
+    case QL_INT4_NSS: return launch_gated<FMT_INT4, 4>(d, w, x, M, h, workspace, s, di->sms, ga);
+    case QL_INT6_SYM: return launch_gated<FMT_INT6, 6>(d, w, x, M, h, workspace, s, di->sms, ga);
+    case QL_INT6_PLANAR: return launch_gated<FMT_INT6P, 6>(d, w, x, M, h, workspace, s, di->sms, ga);
+    default:
+      if (d->bits == 2) return launch_gated<FMT_AFFINE, 2>(d, w, x, M, h, workspace, s, di->sms, ga);
+      if (d->bits == 4) return launch_gated<FMT_AFFINE, 4>(d, w, x, M, h, workspace, s, di->sms, ga);
+      return launch_gated<FMT_AFFINE, 8>(d, w, x, M, h, workspace, s, di->sms, ga);
+  }
+}
+
+ql_status qlinear_gemm_dx_workspace_bytes(const ql_desc *d, int64_t M, size_t *bytes) {
+  const ql_status st = check_dx(d, M);
+  if (st != QL_OK) return st;
+  if (!bytes) return QL_ERR_NULL;
+  *bytes = gemm_dx_workspace(d, M);
+  return QL_OK;
+}
+
+ql_status qlinear_gemm_dx(const ql_desc *d, const ql_packed_const *w, const void *dy, int64_t M, void *dx_out,
+                          void *workspace, size_t workspace_bytes, ql_stream_t stream) {
+  ql_status st = check_dx(d, M);
+  if (st != QL_OK) return st;
+  if (!w || !dy || !dx_out || !workspace) return QL_ERR_NULL;
+  if ((st = check_packed(d, w->codes, w->gmeta, w->steps)) != QL_OK) return st;
+  if (!aligned16(dy) || !aligned16(dx_out) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return QL_ERR_ALIGN;
+  if (workspace_bytes < gemm_dx_workspace(d, M)) return QL_ERR_SHAPE;
+  DeviceInfo *di;
+  if ((st = device_info(&di)) != QL_OK) return st;
+  if (di->major != 10) return QL_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t N = d->N;
+  const auto *yb = static_cast<const __nv_bfloat16 *>(dy);
+  return gemm_dx_call(d, w, M, dx_out, workspace, s, di->sms, [=](const dx::Workspace &ws, int64_t np) {
+    if (N % 8 == 0) dx::dy_prep_kernel<true><<<(unsigned)M, dx::DY_THREADS, 0, s>>>(yb, N, np, ws);
+    else dx::dy_prep_kernel<false><<<(unsigned)M, dx::DY_THREADS, 0, s>>>(yb, N, np, ws);
+  });
+}
+
+ql_status qlinear_gated_backward(const ql_desc *d, const ql_packed_const *w, const ql_saved8_const *saved,
+                                 const void *dh, int64_t M, int32_t act, void *dgu, void *dx_out, void *workspace,
+                                 size_t workspace_bytes, ql_stream_t stream) {
+  ql_status st = check_dx(d, M);
+  if (st == QL_OK) st = check_gated(d, M, act);
+  if (st != QL_OK) return st;
+  if (!w || !saved || !saved->codes || !saved->exps || !dh || !dx_out || !workspace) return QL_ERR_NULL;
+  if ((st = check_packed(d, w->codes, w->gmeta, w->steps)) != QL_OK) return st;
+  if (!aligned16(saved->codes) || !aligned16(saved->exps) || !aligned16(dh) || !aligned16(dgu) ||
+      !aligned16(dx_out) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return QL_ERR_ALIGN;
+  if (workspace_bytes < gemm_dx_workspace(d, M)) return QL_ERR_SHAPE;
+  DeviceInfo *di;
+  if ((st = device_info(&di)) != QL_OK) return st;
+  if (di->major != 10) return QL_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  dx::GatedGrad g0;
+  g0.codes = static_cast<const int8_t *>(saved->codes);
+  g0.exps = static_cast<const uint8_t *>(saved->exps);
+  g0.dh = static_cast<const __nv_bfloat16 *>(dh);
+  g0.dgu = static_cast<__nv_bfloat16 *>(dgu);
+  g0.F = d->N / 2;
+  g0.act = act;
+  return gemm_dx_call(d, w, M, dx_out, workspace, s, di->sms, [=](const dx::Workspace &ws, int64_t np) {
+    dx::GatedGrad g = g0;
+    g.np = np;
+    if (g.F % 8 == 0) dx::dgu_prep_kernel<true><<<(unsigned)M, dx::DGU_THREADS, 0, s>>>(g, ws);
+    else dx::dgu_prep_kernel<false><<<(unsigned)M, dx::DGU_THREADS, 0, s>>>(g, ws);
+  });
 }
 
 ql_status qlinear_set_withhold_copies(int32_t on) {
