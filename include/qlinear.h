@@ -422,7 +422,9 @@ ql_status qlinear_restore8(const ql_saved8_const *in, int64_t rows, int64_t cols
 
 /* Bytes of caller-provided device workspace qlinear_gated needs, with or
  * without a checkpoint (host-only, no CUDA call): that of qlinear_gemm for the
- * layer, or of qlinear_gemv where the call runs on it and that is more.
+ * layer plus, when M > 32, 131072 * min(148, ceil(M/256) * ceil(F/64))
+ * (accumulators on their way out); or that of qlinear_gemv where the call runs
+ * on it and that is more.
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE (also: N odd or K % 64 != 0),
  * QL_ERR_RANGE, QL_ERR_UNSUPPORTED. */
 ql_status qlinear_gated_workspace_bytes(const ql_desc *desc, int64_t M, size_t *bytes);

@@ -23,8 +23,8 @@
 //
 // Workspace (256-byte aligned sections, Np = N rounded up to 64):
 //   dy16   fp16 [M][Np]      scaled dy, zeros past N
-//   dexp   s32  [M]          -a_m
-//   bexp   s8   [Np]         b_n
+//   dexp   s32  [M]          -(a_m + DY_BIAS)
+//   rowexp u8   [Np]         exponent byte of 2^(DY_BIAS - b_n)
 //   meta   u32  [K / gran][Np]  scaled metadata of a run of gran weights: int4 (S, Z S) fp16 pair, int6 the
 //                            scales of its two 16-groups, affine (s, b); zeros past N
 //   partial f32 [2 DX_CTAS][TT][128]
@@ -49,7 +49,7 @@ __host__ __device__ constexpr int gran(int fmt, int group) { return fmt == FMT_A
 struct Workspace {
   __half *dy16;
   int *dexp;
-  int8_t *bexp;
+  uint8_t *rowexp;
   uint32_t *meta;
   float *partial;
 };
@@ -68,7 +68,7 @@ inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
   p += align256((size_t)M * np * 2);
   w.dexp = reinterpret_cast<int *>(p);
   p += align256((size_t)M * 4);
-  w.bexp = reinterpret_cast<int8_t *>(p);
+  w.rowexp = p;
   p += align256(np);
   w.meta = reinterpret_cast<uint32_t *>(p);
   p += align256((size_t)(K / g) * np * 4);
@@ -77,38 +77,28 @@ inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
 }
 
 // ---- pass 1: row exponents and transposed metadata ------------------------------------------------
-// A CTA takes 32 rows: each warp bounds four of them (as the forward's w_scale_row), then the words of 32
-// rows x 32 runs at a time are turned through shared memory, read along the row and written along n.
-constexpr int WP_ROWS = 32;
+// A CTA takes 32 rows x WP_RUNS runs.  It bounds its rows' weights itself (each of the CTAs along a row
+// again: a pass of its own for the bounds cost more than their re-reading from L2), then turns the words
+// through shared memory, read along the row and written along n.  The bound need not be tight -- a looser one
+// only moves the fp16 weights down, and they have 2^29 of range below the top -- so int4 and int6 take it
+// from the steps alone: codes of 255 (int6: -128) times the step.
+constexpr int WP_ROWS = 32, WP_RUNS = 64, WP_THREADS = 256;
+// The row factor 2^(DY_BIAS - b_n) that multiplies dy is kept as its exponent byte; the bias brings the
+// factor of ordinary weights (b_n about 16) near 1, so that dy times it stays in range whenever dy does.
+constexpr int DY_BIAS = 16;
 
 template <int FMT, int BITS>
-QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t K, int G, int lane) {
-  float bound = 0.f;
+QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t i, int64_t K, int G) {
   if constexpr (FMT == FMT_INT4) {
-    const uint16_t *gm = reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32);
-    const uint32_t *st = reinterpret_cast<const uint32_t *>(steps) + n * (K / 256);
-    for (int64_t g = lane; g < K / 32; g += 32) {
-      const uint32_t s = __ldg(st + (g >> 3)), c = __ldg(gm + g);
-      const float S = (float)(c & 0xffu) * f16_bits_to_f32(s), Z = (float)(c >> 8) * f16_bits_to_f32(s >> 16);
-      bound = fmaxf(bound, fabsf(S) * fmaxf(fabsf(Z), fabsf(15.f - Z)));
-    }
+    const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + i);
+    return 255.f * fabsf(f16_bits_to_f32(s)) * fmaxf(15.f, 255.f * fabsf(f16_bits_to_f32(s >> 16)));
   } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
-    const int8_t *gm = reinterpret_cast<const int8_t *>(gmeta) + n * (K / 16);
-    const uint16_t *st = reinterpret_cast<const uint16_t *>(steps) + n * (K / 256);
-    for (int64_t g = lane; g < K / 16; g += 32)
-      bound = fmaxf(bound, 32.f * fabsf((float)__ldg(gm + g) * f16_bits_to_f32(__ldg(st + (g >> 4)))));
+    return 4096.f * fabsf(f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + i)));
   } else {
-    const uint32_t *gm = reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G);
-    const float qmax = (float)((1 << BITS) - 1);
-    for (int64_t g = lane; g < K / G; g += 32) {
-      const uint32_t c = __ldg(gm + g);
-      const float s = bf16_bits_to_f32(c), b = bf16_bits_to_f32(c >> 16);
-      bound = fmaxf(bound, fmaxf(fabsf(b), fabsf(fmaf(qmax, s, b))));
-    }
+    const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G) + i);
+    const float s = bf16_bits_to_f32(c), b = bf16_bits_to_f32(c >> 16);
+    return fmaxf(fabsf(b), fabsf(fmaf((float)((1 << BITS) - 1), s, b)));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bound = fmaxf(bound, __shfl_xor_sync(0xffffffffu, bound, o));
-  return bound;
 }
 
 // The metadata word of run r (of gran weights) of row n, times sc = 2^b_n.
@@ -131,153 +121,148 @@ QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t
 }
 
 template <int FMT, int BITS>
-__global__ void __launch_bounds__(256) w_prep_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N, int64_t K,
-                                                     int G, int64_t np, Workspace ws) {
-  __shared__ float scale[WP_ROWS];
-  __shared__ uint32_t turn[32][33];
+__global__ void __launch_bounds__(WP_THREADS) w_prep_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
+                                                            int64_t K, int G, int64_t np, Workspace ws) {
+  constexpr int RW = WP_ROWS / (WP_THREADS / 32);  // rows a warp
+  __shared__ uint32_t turn[WP_ROWS][WP_RUNS + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS;
-  for (int i = warp; i < WP_ROWS; i += 8) {
-    const int64_t n = n0 + i;
-    int b = 0;
-    if (n < N) b = scale_exponent(meta_bound<FMT, BITS>(gmeta, steps, n, K, G, lane), 14);
-    if (lane == 0) {
-      scale[i] = exp2i(b);
-      ws.bexp[n] = (int8_t)b;
-    }
+  const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS + RW * warp;
+  const int64_t bounds = FMT == FMT_AFFINE ? K / G : K / 256, runs = K / gran(FMT, G);
+  float top[RW];
+#pragma unroll
+  for (int j = 0; j < RW; ++j) top[j] = 0.f;
+  for (int64_t i = lane; i < bounds; i += 32)
+#pragma unroll
+    for (int j = 0; j < RW; ++j) top[j] = fmaxf(top[j], meta_bound<FMT, BITS>(gmeta, steps, min(n0 + j, N - 1), i, K, G));
+  float scale[RW];
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+    // at least -111, so that 127 + DY_BIAS - b is an exponent byte (a weight of 2^125 overflows fp16 then)
+    const int b = n0 + j < N ? max(scale_exponent(top[j], 14), -111) : DY_BIAS;
+    scale[j] = exp2i(b);
+    if (blockIdx.y == 0 && lane == 0) ws.rowexp[n0 + j] = (uint8_t)(127 + DY_BIAS - b);
   }
-  __syncthreads();
-  const int64_t runs = K / gran(FMT, G);
-  for (int64_t r0 = 0; r0 < runs; r0 += 32) {
-    for (int i = warp; i < WP_ROWS; i += 8) {
-      const int64_t n = n0 + i, r = r0 + lane;
-      turn[i][lane] = n < N && r < runs ? scaled_meta<FMT>(gmeta, steps, n, r, K, G, scale[i]) : 0u;
+  const int64_t r0 = (int64_t)blockIdx.y * WP_RUNS;
+#pragma unroll
+  for (int j = 0; j < RW; ++j)
+#pragma unroll
+    for (int i = 0; i < WP_RUNS / 32; ++i) {
+      const int64_t n = n0 + j, r = r0 + 32 * i + lane;
+      turn[RW * warp + j][32 * i + lane] =
+          n < N && r < runs ? scaled_meta<FMT>(gmeta, steps, n, r, K, G, scale[j]) : 0u;
     }
-    __syncthreads();
-    for (int i = warp; i < 32; i += 8)
-      if (r0 + i < runs) ws.meta[(r0 + i) * np + n0 + lane] = turn[lane][i];
-    __syncthreads();
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WP_RUNS / (WP_THREADS / 32); ++i) {
+    const int r = warp + (WP_THREADS / 32) * i;
+    if (r0 + r < runs) ws.meta[(r0 + r) * np + (int64_t)blockIdx.x * WP_ROWS + lane] = turn[lane][r];
   }
 }
 
 // ---- pass 2: dy (or (dg | du)) to scaled fp16 rows ----------------------------------------------------
-constexpr int NO_EXP = -100000;  // exponent of a zero
+// One CTA a token row; an element enters the product as v 2^(DY_BIAS - b_n) 2^a, the row's a from a bound on
+// its scaled magnitudes.
 
-// floor(log2 |v|) for a normal v; a subnormal counts as 2^-126, and values that are not finite do not count
-// (they stay what they are under any scale)
-QL_DEVI int value_exp(float v) {
-  const int e = (int)((__float_as_uint(v) >> 23) & 0xffu);
-  return v == 0.f || e == 255 ? NO_EXP : max(e, 1) - 127;
-}
+// The exponent bytes of four rows -> their factors, i = 0..3
+QL_DEVI float row_factor(uint32_t bytes, int i) { return __uint_as_float(__byte_perm(bytes, 0u, 0x0444 | (i << 12)) >> 1); }
 
-// a_m from the row's largest exponent of dy 2^-b
-QL_DEVI int row_scale_exp(int emax) { return emax == NO_EXP ? 0 : 14 - emax; }
+// Byte i of a word in the mantissa of 2^23
+QL_DEVI float byte_of(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | i)); }
 
-// v * 2^e for results below 2^15 (so e <= 164 for any v but zero) that go to fp16 (zero there for
-// e < -252): two exact steps, the second of which may end in a subnormal
-QL_DEVI float scale_by(float v, int e) {
-  const int e1 = max(-126, min(126, e)), e2 = max(-126, min(126, e - e1));
-  return v * exp2i(e1) * exp2i(e2);
-}
-
-// The largest value of every thread's e over the CTA.
+// The largest value of every thread's v over the CTA.
 template <int THREADS>
-QL_DEVI int block_max(int e, int *red) {
+QL_DEVI float block_max(float v, float *red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = e;
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  e = red[0];
+  v = red[0];
 #pragma unroll
-  for (int w = 1; w < THREADS / 32; ++w) e = max(e, red[w]);
-  return e;
+  for (int w = 1; w < THREADS / 32; ++w) v = fmaxf(v, red[w]);
+  return v;
 }
 
-// Eight values at element offset i of a bf16 row, the elements from `end` on as zeros.  VEC: the row's
-// elements are 16-byte aligned at every multiple of 8.
+// Eight bf16 of a row from element i on, those from `end` on as zeros.  VEC: the row's elements are 16-byte
+// aligned at every multiple of 8, and end is one.
 template <bool VEC>
-QL_DEVI void load8(const __nv_bfloat16 *row, int64_t i, int64_t end, float (&v)[8]) {
-  if (VEC) {  // end is a multiple of 8
-    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(row + i));
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_bits_to_f32(u[j]);
-      v[2 * j + 1] = bf16_bits_to_f32(u[j] >> 16);
-    }
+QL_DEVI uint4 load8(const __nv_bfloat16 *row, int64_t i, int64_t end) {
+  if constexpr (VEC) {
+    return __ldg(reinterpret_cast<const uint4 *>(row + i));
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = i + j < end ? __bfloat162float(row[i + j]) : 0.f;
-  }
-}
-
-// Eight row exponents b_n from n on; those from `end` on are not used.
-template <bool VEC>
-QL_DEVI void load_bexp(const int8_t *b, int64_t n, int64_t end, int (&e)[8]) {
-  if (VEC) {
-    const uint2 q = *reinterpret_cast<const uint2 *>(b + n);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      e[j] = (int)(int8_t)(q.x >> (8 * j));
-      e[4 + j] = (int)(int8_t)(q.y >> (8 * j));
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = n + j < end ? (int)b[n + j] : 0;
-  }
-}
-
-template <bool VEC>
-QL_DEVI void store8_f16(__half *row, int64_t n, int64_t end, const float (&v)[8], const int (&e)[8], int a) {
-  if (VEC) {
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pack_f16x2(scale_by(v[2 * j], a - e[2 * j]), scale_by(v[2 * j + 1], a - e[2 * j + 1]));
-    *reinterpret_cast<uint4 *>(row + n) = make_uint4(o[0], o[1], o[2], o[3]);
-  } else {
+    uint32_t u[4] = {0u, 0u, 0u, 0u};
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(row);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (n + j < end) row[n + j] = __float2half_rn(scale_by(v[j], a - e[j]));
+      if (i + j < end) u[j >> 1] |= (uint32_t)src[i + j] << (16 * (j & 1));
+    return make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
-
-QL_DEVI int max_exp8(const float (&v)[8], const int (&e)[8], int m) {
+QL_DEVI void unpack8(uint4 q, float (&v)[8]) {
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int x = value_exp(v[j]);
-    if (x != NO_EXP) m = max(m, x - e[j]);
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(u[j] << 16);
+    v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
   }
-  return m;
 }
 
-constexpr int DY_THREADS = 256;
+constexpr int DY_THREADS = 256, DY_REGS = 4;
 
-// One CTA a token row.
+// Rows of up to DY_REGS * DY_THREADS vectors of 8 are read once and kept; longer rows are read again.
 template <bool VEC>
 __global__ void __launch_bounds__(DY_THREADS) dy_prep_kernel(const __nv_bfloat16 *dy, int64_t N, int64_t np,
                                                              Workspace ws) {
-  __shared__ int red[DY_THREADS / 32];
-  const int64_t m = blockIdx.x;
+  __shared__ float red[DY_THREADS / 32];
+  const int64_t m = blockIdx.x, nv = (N + 7) / 8;
   const __nv_bfloat16 *row = dy + m * N;
-  __half *out = ws.dy16 + m * np;
-  int emax = NO_EXP;
-  for (int64_t i = 8 * threadIdx.x; i < N; i += 8 * DY_THREADS) {
+  const uint2 *fac = reinterpret_cast<const uint2 *>(ws.rowexp);
+  uint4 *out = reinterpret_cast<uint4 *>(ws.dy16 + m * np);
+  auto top8 = [](uint4 q, uint2 f, float t) {
     float v[8];
-    int e[8];
-    load8<VEC>(row, i, N, v);
-    load_bexp<true>(ws.bexp, i, N, e);
-    emax = max_exp8(v, e, emax);
+    unpack8(q, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaxf(t, fabsf(v[j] * row_factor(j < 4 ? f.x : f.y, j & 3)));
+    return t;
+  };
+  auto put8 = [](uint4 q, uint2 f, float sc) {
+    float v[8];
+    unpack8(q, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * row_factor(j < 4 ? f.x : f.y, j & 3) * sc;
+    return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+  };
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const bool kept = nv <= (int64_t)DY_REGS * DY_THREADS;
+  uint4 q[DY_REGS];
+  uint2 f[DY_REGS];
+  float top = 0.f;
+  if (kept) {
+#pragma unroll
+    for (int r = 0; r < DY_REGS; ++r) {
+      const int64_t i = threadIdx.x + r * DY_THREADS;
+      q[r] = i < nv ? load8<VEC>(row, 8 * i, N) : zero;
+      f[r] = i < nv ? fac[i] : make_uint2(0u, 0u);
+    }
+#pragma unroll
+    for (int r = 0; r < DY_REGS; ++r) top = top8(q[r], f[r], top);
+  } else {
+    for (int64_t i = threadIdx.x; i < nv; i += DY_THREADS) top = top8(load8<VEC>(row, 8 * i, N), fac[i], top);
   }
-  const int a = row_scale_exp(block_max<DY_THREADS>(emax, red));
-  for (int64_t i = 8 * threadIdx.x; i < np; i += 8 * DY_THREADS) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    int e[8];
-    if (i < N) load8<VEC>(row, i, N, v);
-    load_bexp<true>(ws.bexp, i, np, e);
-    store8_f16<true>(out, i, np, v, e, a);
+  const int a = scale_exponent(block_max<DY_THREADS>(top, red), 14);
+  const float sc = exp2i(a);
+  if (kept) {
+#pragma unroll
+    for (int r = 0; r < DY_REGS; ++r) {
+      const int64_t i = threadIdx.x + r * DY_THREADS;
+      if (i < nv) out[i] = put8(q[r], f[r], sc);
+    }
+  } else {
+    for (int64_t i = threadIdx.x; i < nv; i += DY_THREADS) out[i] = put8(load8<VEC>(row, 8 * i, N), fac[i], sc);
   }
-  if (threadIdx.x == 0) ws.dexp[m] = -a;
+  if (threadIdx.x < np / 8 - nv) out[nv + threadIdx.x] = zero;
+  if (threadIdx.x == 0) ws.dexp[m] = -(a + DY_BIAS);
 }
 
 struct GatedGrad {
@@ -286,67 +271,113 @@ struct GatedGrad {
   const __nv_bfloat16 *dh;  // [M][F]
   __nv_bfloat16 *dgu;       // [M][2F] or NULL
   int64_t F, np;
-  int act;
 };
 
-// dg and du of eight features from f on (f a multiple of 8, below F; those from F on are zeros).
+constexpr int DGU_THREADS = 256;
+constexpr float MAX_SLOPE = 1.13f;  // of the activations; |act(g)| <= |g|
+
+// 16 exponent bytes of rows n .. n + 15 (bytes from `end` on as zeros).  VEC: n is a multiple of 16.
 template <bool VEC>
-QL_DEVI void gated_grad8(const GatedGrad &p, int64_t m, int64_t f, float (&dg)[8], float (&du)[8]) {
-  const int64_t fp = save8_cols(p.F);
-  float dh[8];
-  load8<VEC>(p.dh + m * p.F, f, p.F, dh);
-  const int8_t *codes = p.codes + 2 * m * fp + f;
-  const uint8_t *exps = p.exps + 2 * m * (fp / 16) + (f >> 4);
-  const uint2 cg = __ldg(reinterpret_cast<const uint2 *>(codes)), cu = __ldg(reinterpret_cast<const uint2 *>(codes + fp));
-  const float sg = save8_scale(__ldg(exps)), su = save8_scale(__ldg(exps + fp / 16));
+QL_DEVI uint4 load_rowexp(const uint8_t *e, int64_t n, int64_t end) {
+  if constexpr (VEC) {
+    return *reinterpret_cast<const uint4 *>(e + n);
+  } else {
+    uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float g = (float)(int8_t)((j < 4 ? cg.x : cg.y) >> (8 * (j & 3))) * sg;
-    const float u = (float)(int8_t)((j < 4 ? cu.x : cu.y) >> (8 * (j & 3))) * su;
-    float a, d;
-    act_grad(p.act, g, a, d);
-    dg[j] = f + j < p.F ? dh[j] * u * d : 0.f;
-    du[j] = f + j < p.F ? dh[j] * a : 0.f;
+    for (int j = 0; j < 16; ++j)
+      if (n + j < end) u[j >> 2] |= (uint32_t)e[n + j] << (8 * (j & 3));
+    return make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
-constexpr int DGU_THREADS = 512;
+QL_DEVI uint32_t max_byte(uint4 v) {
+  uint32_t m = __vmaxu4(__vmaxu4(v.x, v.y), __vmaxu4(v.z, v.w));
+  m = __vmaxu4(m, m >> 16);
+  return max(m & 0xFFu, (m >> 8) & 0xFFu);
+}
 
+// Sixteen 16-bit values -> row elements n .. n + 15 (those below `end`).  VEC: 16-byte aligned, all of them.
 template <bool VEC>
-__global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Workspace ws) {
-  __shared__ int red[DGU_THREADS / 32];
-  const int64_t m = blockIdx.x, N = 2 * p.F;
-  int emax = NO_EXP;
-  for (int64_t f = 8 * threadIdx.x; f < p.F; f += 8 * DGU_THREADS) {
-    float dg[8], du[8];
-    int e[8];
-    gated_grad8<VEC>(p, m, f, dg, du);
-    load_bexp<true>(ws.bexp, f, N, e);
-    emax = max_exp8(dg, e, emax);
-    load_bexp<VEC>(ws.bexp, p.F + f, N, e);
-    emax = max_exp8(du, e, emax);
-  }
-  const int a = row_scale_exp(block_max<DGU_THREADS>(emax, red));
-  __half *out = ws.dy16 + m * p.np;
-  for (int64_t f = 8 * threadIdx.x; f < p.F; f += 8 * DGU_THREADS) {
-    float dg[8], du[8];
-    int e[8];
-    gated_grad8<VEC>(p, m, f, dg, du);
-    load_bexp<true>(ws.bexp, f, N, e);
-    store8_f16<VEC>(out, f, p.F, dg, e, a);
-    load_bexp<VEC>(ws.bexp, p.F + f, N, e);
-    store8_f16<VEC>(out + p.F, f, p.F, du, e, a);
-    if (p.dgu) {
+QL_DEVI void store16(void *row, int64_t n, int64_t end, const uint32_t (&o)[8]) {
+  uint16_t *dst = static_cast<uint16_t *>(row) + n;
+  if constexpr (VEC) {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (f + j < p.F) {
-          p.dgu[m * N + f + j] = __float2bfloat16_rn(dg[j]);
-          p.dgu[m * N + p.F + f + j] = __float2bfloat16_rn(du[j]);
-        }
+    for (int j = 0; j < 16; ++j)
+      if (n + j < end) dst[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+  }
+}
+
+// A thread takes one group of 16 features at a time.  The row's scale comes from a bound that needs no
+// activation -- the group's largest |dh| times 127 steps of u (slope at most 1.13) or of g -- so every
+// gradient is computed once; the bound's slack costs a few of the 29 powers of two that fp16 has below its
+// top.  Bound by instruction issue; the int8 codes become floats by a byte permute and one FMA.
+template <int ACT, bool VEC>
+__global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Workspace ws) {
+  __shared__ float red[DGU_THREADS / 32];
+  const int64_t m = blockIdx.x, N = 2 * p.F, fp = save8_cols(p.F);
+  const int groups = (int)(fp / 16);
+  const __nv_bfloat16 *dh = p.dh + m * p.F;
+  const uint4 *cg = reinterpret_cast<const uint4 *>(p.codes + 2 * m * fp), *cu = cg + groups;
+  const uint8_t *eg = p.exps + 2 * m * groups, *eu = eg + groups;
+  float top = 0.f;
+  for (int i = threadIdx.x; i < groups; i += DGU_THREADS) {
+    const int64_t f = 16 * (int64_t)i;
+    const uint4 d0 = load8<VEC>(dh, f, p.F), d1 = load8<VEC>(dh, f + 8, p.F);
+    const uint4 rg = load_rowexp<VEC>(ws.rowexp, f, p.F), ru = load_rowexp<VEC>(ws.rowexp + p.F, f, p.F);
+    const float sg = save8_scale(__ldg(eg + i)), su = save8_scale(__ldg(eu + i));
+    const float dm = chunk_amax(d1, chunk_amax(d0, 0.f)) * 127.f;
+    top = fmaxf(top, dm * su * (MAX_SLOPE * __uint_as_float(max_byte(rg) << 23)));
+    top = fmaxf(top, dm * sg * __uint_as_float(max_byte(ru) << 23));
+  }
+  const int a = scale_exponent(block_max<DGU_THREADS>(top, red), 14);
+  const float sc = exp2i(a);
+  __half *out = ws.dy16 + m * p.np;
+  for (int i = threadIdx.x; i < groups; i += DGU_THREADS) {
+    const int64_t f = 16 * (int64_t)i;
+    const uint4 d0 = load8<VEC>(dh, f, p.F), d1 = load8<VEC>(dh, f + 8, p.F);
+    const uint4 qg = __ldg(cg + i), qu = __ldg(cu + i);
+    const uint4 rg = load_rowexp<VEC>(ws.rowexp, f, p.F), ru = load_rowexp<VEC>(ws.rowexp + p.F, f, p.F);
+    const float sg = save8_scale(__ldg(eg + i)), su = save8_scale(__ldg(eu + i));
+    const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+    const uint32_t gw[4] = {qg.x, qg.y, qg.z, qg.w}, uw[4] = {qu.x, qu.y, qu.z, qu.w};
+    const uint32_t fg[4] = {rg.x, rg.y, rg.z, rg.w}, fu[4] = {ru.x, ru.y, ru.z, ru.w};
+    // code c as the byte c + 128 in the mantissa of 2^23: value = (2^23 + 128 + c) s - (2^23 + 128) s, exact
+    const float zg = -8388736.f * sg, zu = -8388736.f * su;
+    uint32_t og[8], ou[8], bg[8], bu[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float dgv[2], duv[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = 2 * j + h;
+        const float d = h ? __uint_as_float(dw[j] & 0xffff0000u) : __uint_as_float(dw[j] << 16);
+        const float g = fmaf(byte_of(gw[e >> 2] ^ 0x80808080u, e & 3), sg, zg);
+        const float u = fmaf(byte_of(uw[e >> 2] ^ 0x80808080u, e & 3), su, zu);
+        float av, ad;
+        act_grad(ACT, g, av, ad);
+        dgv[h] = d * u * ad;
+        duv[h] = d * av;
+      }
+      if (p.dgu) {
+        bg[j] = pack_bf16x2(dgv[0], dgv[1]);
+        bu[j] = pack_bf16x2(duv[0], duv[1]);
+      }
+      const int e = 2 * j;
+      og[j] = pack_f16x2(dgv[0] * row_factor(fg[e >> 2], e & 3) * sc, dgv[1] * row_factor(fg[e >> 2], (e & 3) + 1) * sc);
+      ou[j] = pack_f16x2(duv[0] * row_factor(fu[e >> 2], e & 3) * sc, duv[1] * row_factor(fu[e >> 2], (e & 3) + 1) * sc);
+    }
+    store16<VEC>(out, f, p.F, og);
+    store16<VEC>(out + p.F, f, p.F, ou);
+    if (p.dgu) {
+      store16<VEC>(p.dgu + m * N, f, p.F, bg);
+      store16<VEC>(p.dgu + m * N + p.F, f, p.F, bu);
     }
   }
-  for (int64_t n = N + threadIdx.x; n < p.np; n += DGU_THREADS) out[n] = __float2half_rn(0.f);
-  if (threadIdx.x == 0) ws.dexp[m] = -a;
+  if (threadIdx.x < p.np - N) out[N + threadIdx.x] = __float2half_rn(0.f);
+  if (threadIdx.x == 0) ws.dexp[m] = -(a + DY_BIAS);
 }
 
 // ---- pass 3: the GEMM ------------------------------------------------------------------------------
@@ -776,25 +807,47 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
 }
 
 // ---- pass 4: the sums of the split tiles' parts -------------------------------------------------------
-// One CTA of 128 threads a (tile, token): thread r adds row r's parts in the order of the shares.
+// A CTA takes 16 tokens of a tile, a thread 8 rows (eight consecutive k, see out_k) of one of them; the
+// parts are added in the order of the shares.
+constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 8);
+
 template <int TT>
-__global__ void __launch_bounds__(BKT) join_kernel(Params p) {
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
+  __shared__ int range[3];  // first share, its slot, end of the shares
   const Deal &d = p.deal;
   const int64_t rest_tile = blockIdx.x, tile = (int64_t)d.waves * d.ctas + rest_tile;
-  const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
-  const int64_t m = m_tile * TT + blockIdx.y, k = k_tile * BKT + out_k((int)threadIdx.x);
-  if (m >= p.M) return;
-  const int64_t lo = rest_tile * d.steps, hi = lo + d.steps, all = (int64_t)d.rest * d.steps;
-  int c = (int)(lo * d.shares / all);  // at or just before the share that holds stage lo
-  while (d.share_begin(c + 1) <= lo) ++c;
-  float sum = 0.f;
-  for (; c < d.shares && d.share_begin(c) < hi; ++c) {
-    const int64_t b = d.share_begin(c);
-    if (b == d.share_begin(c + 1)) continue;
-    const int slot = 2 * c + (b < lo ? 1 : 0);  // the share's second piece when it began in the tile before
-    sum += __ldcg(p.partial + ((int64_t)slot * TT + blockIdx.y) * BKT + threadIdx.x);
+  if (threadIdx.x == 0) {
+    const int64_t lo = rest_tile * d.steps, hi = lo + d.steps, all = (int64_t)d.rest * d.steps;
+    int c = (int)(lo * d.shares / all);  // at or just before the share that holds stage lo
+    while (d.share_begin(c + 1) <= lo) ++c;
+    range[0] = c;
+    range[1] = 2 * c + (d.share_begin(c) < lo ? 1 : 0);  // its second piece if it began in the tile before
+    int e = (int)(hi * d.shares / all);  // the last share that begins below hi, or one after
+    while (e < d.shares && d.share_begin(e) < hi) ++e;
+    while (d.share_begin(e - 1) >= hi) --e;
+    range[2] = e;
   }
-  if (k < p.K) p.dx[m * p.K + k] = __float2bfloat16_rn(mul_pow2(sum, __ldg(p.dexp + m)));
+  __syncthreads();
+  const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
+  const int t = blockIdx.y * JOIN_TOKENS + threadIdx.x / (BKT / 8), r = 8 * (threadIdx.x % (BKT / 8));
+  const int64_t m = m_tile * TT + t, k = k_tile * BKT + r;
+  if (t >= TT || m >= p.M || k >= p.K) return;
+  const int end = range[2];
+  int slot = range[1];
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int c = range[0]; c < end; ++c) {
+    const float4 *src = reinterpret_cast<const float4 *>(p.partial + ((int64_t)slot * TT + t) * BKT + r);
+    const float4 x = __ldcg(src), y = __ldcg(src + 1);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    slot = 2 * (c + 1);
+  }
+  const int e = __ldg(p.dexp + m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = mul_pow2(v[i], e);
+  // rows hold k 0,4,1,5,2,6,3,7
+  *reinterpret_cast<uint4 *>(p.dx + m * p.K + k) =
+      make_uint4(pack_bf16x2(v[0], v[2]), pack_bf16x2(v[4], v[6]), pack_bf16x2(v[1], v[3]), pack_bf16x2(v[5], v[7]));
 }
 
 }  // namespace dx

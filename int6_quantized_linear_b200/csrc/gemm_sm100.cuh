@@ -137,6 +137,7 @@ struct Params {
   int act;
   int8_t *saved;        // codes [M][2][save8_cols(N / 2)] of (g, u), or NULL
   uint8_t *saved_exps;  // [M][2][save8_cols(N / 2) / 16]
+  float4 *scratch;      // TT = 256: [CTA][TT / 4][BN]
 };
 
 // The gated form: the layer's rows are F = N / 2 gate rows, then F up rows, and a tile is 64 features:
@@ -367,6 +368,50 @@ QL_DEVI void gated_store(const Params &p, const uint32_t (&r)[16], int64_t f, in
             (uint8_t)save8_exponent((kw >> (8 * (l & 3))) & 0xffu);
     }
   }
+}
+
+// What a lane needs of its row of a gated tile: its feature, its scale exponent, and the tile's tokens.
+struct GatedRow {
+  int64_t f, m0;
+  int we, chunks;  // chunks of 16 tokens that hold any
+  QL_DEVI GatedRow(const Params &p, int64_t n_tile, int64_t m_tile, int tt, int e, int lane) {
+    const int64_t n = layer_row<true>(n_tile, box_row<true>(32 * e + lane), p.N);
+    we = n < p.N ? p.ws.wexp[n] : 0;
+    f = n_tile * GATED_F + 16 * e + (lane & 15);
+    m0 = m_tile * tt;
+    const int64_t left = p.M - m0;
+    chunks = (int)((left < tt ? left : tt) + 15) / 16;
+  }
+};
+
+// Chunk c (16 tokens) of a row's accumulator: undo the power-of-two scales (exponents added first, see
+// mul_pow2), then the gated epilogue.  The exponents of tokens past M are read (their section of the
+// workspace is padded) and not used.
+QL_DEVI void gated_chunk(const Params &p, const GatedRow &row, uint32_t (&r)[16], int c, int lane) {
+  const int64_t m0 = row.m0 + 16 * c;
+  const int4 *xe4 = reinterpret_cast<const int4 *>(p.ws.xexp + m0);
+  int xe[16];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int4 v = __ldg(xe4 + j);
+    xe[4 * j] = v.x; xe[4 * j + 1] = v.y; xe[4 * j + 2] = v.z; xe[4 * j + 3] = v.w;
+  }
+  int lo = xe[0], hi = xe[0];
+#pragma unroll
+  for (int t = 1; t < 16; ++t) {
+    lo = min(lo, xe[t]);
+    hi = max(hi, xe[t]);
+  }
+  if (__all_sync(0xffffffffu, lo + row.we >= -126 && hi + row.we <= 127)) {
+    const int w_bits = row.we * (1 << 23) + 0x3F800000;
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      r[t] = __float_as_uint(__fmul_rn(__uint_as_float(r[t]), __int_as_float(xe[t] * (1 << 23) + w_bits)));
+  } else {
+#pragma unroll
+    for (int t = 0; t < 16; ++t) r[t] = __float_as_uint(mul_pow2(__uint_as_float(r[t]), xe[t] + row.we));
+  }
+  gated_store(p, r, row.f, m0, lane);
 }
 
 template <int FMT, int BITS, int TT, int CPS = 1, bool GATED = false>
@@ -611,13 +656,70 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
     // lane = weight row n of the tile (TMEM lane 32 e + lane); its TT columns = the tile's tokens
     const int e = warp - WARP_EPI0;  // TMEM lane quarter
     int64_t tcount = 0;
-    for (int64_t tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
+    if constexpr (GATED) {
+      // Two accumulators (TT = 32): the next tile's MMAs run beside the epilogue.  One (TT = 256): they can
+      // only start once it has been read, and act and the rounding to 8 bits take longer than the reading,
+      // so a tile is first moved as it is to this CTA's scratch (in L2) and finished from there beside the
+      // next tile's MMAs; each thread reads back what it wrote itself.  Nothing follows the last tile, so it is
+      // finished from tensor memory, by the dequantisers too.
+      float4 *scratch = p.scratch + (int64_t)blockIdx.x * (BN * TT / 4) + 32 * e + lane;
+      for (int64_t tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
+        const int64_t n_tile = tile / m_tiles, m_tile = tile - n_tile * m_tiles;
+        const int a = (int)(tcount % NACC);
+        const bool moved = NACC == 1 && tile + gridDim.x < num_tiles;
+        const bool shared_out = NACC == 1 && !moved;
+        const GatedRow row(p, n_tile, m_tile, TT, e, lane);
+        if (!mbar_wait_bounded(bar_acc_full(a), (uint32_t)(tcount / NACC) & 1, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t t_acc = tmem_base + ((uint32_t)(32 * e) << 16) + (uint32_t)(a * TT);
+        if (moved) {
+#pragma unroll 1
+          for (int c = 0; c < row.chunks; c += 2) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_acc + 16 * c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              scratch[(4 * c + j) * BN] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                      __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_acc_empty(a));
+#pragma unroll 1
+          for (int c = 0; c < row.chunks; ++c) {
+            uint32_t r[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 v = scratch[(4 * c + j) * BN];
+              r[4 * j] = __float_as_uint(v.x);
+              r[4 * j + 1] = __float_as_uint(v.y);
+              r[4 * j + 2] = __float_as_uint(v.z);
+              r[4 * j + 3] = __float_as_uint(v.w);
+            }
+            gated_chunk(p, row, r, c, lane);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < row.chunks; c += shared_out ? 1 + NG : 1) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_acc + 16 * c, r);
+            tmem_ld_wait();
+            gated_chunk(p, row, r, c, lane);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_acc_empty(a));
+        }
+      }
+    }
+    for (int64_t tile = GATED ? num_tiles : blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
       const int64_t n_tile = tile / m_tiles, m_tile = tile - n_tile * m_tiles;
       const int a = (int)(tcount % NACC);
       const uint32_t ause = (uint32_t)(tcount / NACC);
       // the tile's scale exponents and bias, loaded while its MMAs run: lane l holds the exponents of
       // tokens l, l + 32, .. (a load per column chunk would put an L2 round trip between the chunks)
-      const int64_t n = layer_row<GATED>(n_tile, box_row<GATED>(32 * e + lane), p.N);
+      const int64_t n = n_tile * BN + 32 * e + lane;
       const int we = n < p.N ? p.ws.wexp[n] : 0;
       const float bn = (p.bias && n < p.N) ? __bfloat162float(p.bias[n]) : 0.f;
       // (each exponent lies in [-126, 126], so one signed byte holds it: a chunk's 16 are one broadcast
@@ -672,9 +774,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
             r[t] = __float_as_uint(mul_pow2(__uint_as_float(r[t]), xe + we) + bn);
           }
         }
-        if constexpr (GATED) {
-          gated_store(p, r, n_tile * GATED_F + 16 * e + (lane & 15), m0, lane);
-        } else if (n < p.N) {  // token t of row n: the warp's 32 rows are 64 contiguous bytes of y's row m0 + t
+        if (n < p.N) {  // token t of row n: the warp's 32 rows are 64 contiguous bytes of y's row m0 + t
           __nv_bfloat16 *dst = p.y + m0 * p.N + n;
           const int64_t rows_left = p.M - m0;
 #pragma unroll
@@ -795,6 +895,22 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       gm[1] = ngm[1];
       st[0] = nst[0];
       st[1] = nst[1];
+    }
+    if constexpr (GATED && NACC == 1) {
+      // the CTA's last tile: chunks 1 + g, 2 + NG + g, .. are this group's once every MMA has retired
+      if (my_tiles > 0 && !*abort_flag && __all_sync(0xffffffffu, mbar_wait_bounded(bar_final, 0, abort_flag))) {
+        tc_fence_after();
+        const int64_t tile = blockIdx.x + (my_tiles - 1) * gridDim.x, n_tile = tile / m_tiles;
+        const GatedRow row(p, n_tile, tile - n_tile * m_tiles, TT, wd & 3, lane);
+#pragma unroll 1
+        for (int c = 1 + g; c < row.chunks; c += 1 + NG) {
+          uint32_t r16[16];
+          tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * (wd & 3)) << 16) + 16 * c, r16);
+          tmem_ld_wait();
+          gated_chunk(p, row, r16, c, lane);
+        }
+        tc_fence_before();
+      }
     }
   }
 

@@ -183,6 +183,9 @@ inline int64_t gemv_row_groups(int64_t N) {
 template <bool GATED>
 constexpr uint32_t gemv_box_rows() { return GATED ? GATED_ROWS : 64; }
 
+// CTAs an SM's worth of the gated GEMM at most: the SMs of a B200 (its workspace is sized without a device)
+constexpr int GATED_CTAS = 148;
+
 // What the gated forms of the launches take besides the layer's arguments (y is then h [M][N / 2]).
 struct GatedArgs {
   int act = ACT_SILU;
@@ -236,6 +239,7 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
   p.act = ga.act;
   p.saved = ga.saved;
   p.saved_exps = ga.saved_exps;
+  p.scratch = reinterpret_cast<float4 *>(static_cast<uint8_t *>(workspace) + gemm_workspace_bytes(M, N, K));
   const int smem = smem_bytes(FMT, BITS, TT);
   auto kern = gemm_kernel<FMT, BITS, TT, CPS, GATED>;
   static thread_local int configured_dev = -1;  // per (kernel instantiation, thread)
@@ -247,7 +251,7 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
     configured_dev = dev;
   }
   const int64_t tiles = ((M + TT - 1) / TT) * gemm_row_tiles<GATED>(N);
-  const int slots = CPS * sms;
+  const int slots = GATED ? CPS * std::min(sms, GATED_CTAS) : CPS * sms;
   const int grid = (int)(tiles < slots ? tiles : slots);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -647,7 +651,10 @@ inline bool gated_runs_on_gemv(const ql_desc *d, int64_t M, bool saves) {
 
 // covers the call with and without a checkpoint
 inline size_t gated_workspace_bytes(const ql_desc *d, int64_t M) {
-  const size_t gemm = gemm_workspace_bytes(M, d->N, d->K);
+  size_t gemm = gemm_workspace_bytes(M, d->N, d->K);
+  if (M > gemm::TT_SMALL)  // a scratch tile a CTA
+    gemm += (size_t)std::min<int64_t>((M + gemm::BM - 1) / gemm::BM * gemm_row_tiles<true>(d->N), GATED_CTAS) *
+            gemm::BN * gemm::BM * 4;
   const size_t gemv = gated_runs_on_gemv(d, M, false) ? gemv_workspace_bytes(M, d->N, d->K) : 0;
   return gemv > gemm ? gemv : gemm;
 }
@@ -673,7 +680,8 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
   const int64_t N = d->N, K = d->K, np = padded_n(N);
   const int gr = gran(FMT, d->group);
   const Workspace ws = carve(workspace, M, N, K, gr);
-  w_prep_kernel<FMT, BITS><<<(unsigned)(np / WP_ROWS), 256, 0, st>>>(
+  const dim3 wp_grid((unsigned)(np / WP_ROWS), (unsigned)((K / gr + WP_RUNS - 1) / WP_RUNS));
+  w_prep_kernel<FMT, BITS><<<wp_grid, WP_THREADS, 0, st>>>(
       static_cast<const uint8_t *>(w->gmeta), static_cast<const uint8_t *>(w->steps), N, K, d->group, np, ws);
   prep(ws, np);
   const uint64_t row_bytes = (uint64_t)K * gemm::code_bits(FMT, BITS) / 8;
@@ -710,7 +718,8 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
   }
   kern<<<(unsigned)(p.deal.waves ? p.deal.ctas : p.deal.shares), num_threads(TT), smem, st>>>(my, mc, mh, mm, p);
   if (p.deal.joins())
-    join_kernel<TT><<<dim3((unsigned)p.deal.rest, (unsigned)(M < TT ? M : TT)), BKT, 0, st>>>(p);
+    join_kernel<TT><<<dim3((unsigned)p.deal.rest, (unsigned)(((M < TT ? M : TT) + JOIN_TOKENS - 1) / JOIN_TOKENS)),
+                      JOIN_THREADS, 0, st>>>(p);
   return launched();
 }
 
@@ -1249,12 +1258,15 @@ ql_status qlinear_gated_backward(const ql_desc *d, const ql_packed_const *w, con
   g0.dh = static_cast<const __nv_bfloat16 *>(dh);
   g0.dgu = static_cast<__nv_bfloat16 *>(dgu);
   g0.F = d->N / 2;
-  g0.act = act;
   return gemm_dx_call(d, w, M, dx_out, workspace, s, di->sms, [=](const dx::Workspace &ws, int64_t np) {
     dx::GatedGrad g = g0;
     g.np = np;
-    if (g.F % 8 == 0) dx::dgu_prep_kernel<true><<<(unsigned)M, dx::DGU_THREADS, 0, s>>>(g, ws);
-    else dx::dgu_prep_kernel<false><<<(unsigned)M, dx::DGU_THREADS, 0, s>>>(g, ws);
+    const bool vec = g.F % 16 == 0;
+    auto *kern = act == ACT_SILU        ? (vec ? dx::dgu_prep_kernel<ACT_SILU, true> : dx::dgu_prep_kernel<ACT_SILU, false>)
+                 : act == ACT_GELU_TANH ? (vec ? dx::dgu_prep_kernel<ACT_GELU_TANH, true>
+                                               : dx::dgu_prep_kernel<ACT_GELU_TANH, false>)
+                                        : (vec ? dx::dgu_prep_kernel<ACT_GELU, true> : dx::dgu_prep_kernel<ACT_GELU, false>);
+    kern<<<(unsigned)M, dx::DGU_THREADS, 0, s>>>(g, ws);
   });
 }
 
