@@ -311,98 +311,167 @@ QL_DEVI void chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], const uint
 // Epilogue of the gated form for 16 tokens (m0 ..) of one feature f: lanes 0-15 of the warp hold the 16
 // tokens' g in r, lanes 16-31 the same features' u.  Each lane sends half of its tokens to its partner
 // (lane ^ 16) and receives the other projection of the half it keeps: lanes 0-15 finish tokens 0-7, lanes
-// 16-31 tokens 8-15, and the 16 lanes' features are contiguous in h.  With a checkpoint, the 16 features
-// are also one group of its scales: a group's key is the maximum over the half-warp, taken for four
-// values at once in the bytes of a word.
+// 16-31 tokens 8-15, 16 contiguous features of each.  This warp runs beside the dequantisers, whose issue
+// slots it takes, so it is written for few instructions: values travel and are stored in pairs (h) and
+// fours (codes) after a transposition among neighbouring lanes, and a group's scale is reduced once, not in
+// every lane.
+
+// h of 8 tokens.  Words of two tokens become words of two features: the even lane of a pair keeps the
+// first token, the odd lane the second.
+QL_DEVI void gated_store_h(const Params &p, const float (&h)[8], int64_t F, int64_t f, int64_t m0, int64_t rows_left,
+                           int lane) {
+  if (F % 2 == 0) {
+    const bool odd = lane & 1;
+    __nv_bfloat16 *dst = p.y + (m0 + odd) * F + (f & ~(int64_t)1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t own = pack_bf16x2(h[2 * j], h[2 * j + 1]), other = __shfl_xor_sync(0xffffffffu, own, 1);
+      const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+      if (f < F && 2 * j + odd < rows_left) *reinterpret_cast<uint32_t *>(dst) = w;
+      dst += 2 * F;
+    }
+  } else {
+    __nv_bfloat16 *dst = p.y + m0 * F + f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      if (f < F && t < rows_left) *dst = __float2bfloat16_rn(h[t]);
+      dst += F;
+    }
+  }
+}
+
+// The checkpoint of 8 tokens' g and u.  The 16 lanes' features are one group of each token and projection.
+// A value's upper 16 bits plus one, without the sign, order like save8_key and hold it in their upper bits
+// (the sum is the key's carry); two values share a word.  Words 0-3 are the tokens' g, 4-7 their u.
+QL_DEVI void gated_save(const Params &p, const float (&g)[8], const float (&u)[8], int64_t F, int64_t f, int64_t m0,
+                        int64_t rows_left, int lane) {
+  const int l = lane & 15;
+  uint32_t k[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float v0 = j < 4 ? g[2 * j] : u[2 * j - 8], v1 = j < 4 ? g[2 * j + 1] : u[2 * j - 7];
+    k[j] = (__byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632) & 0x7FFF7FFFu) + 0x00010001u;
+  }
+  // halve the words and the lanes in turn: bit 3 of l picks g or u, bits 2 and 1 the word; then the last bit's
+  // lanes meet
+  uint32_t a4[4], a2[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, (l & 8) ? k[j] : k[j + 4], 8);
+    a4[j] = __vmaxu2((l & 8) ? k[j + 4] : k[j], got);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, (l & 4) ? a4[j] : a4[j + 2], 4);
+    a2[j] = __vmaxu2((l & 4) ? a4[j + 2] : a4[j], got);
+  }
+  uint32_t w = __vmaxu2((l & 2) ? a2[1] : a2[0], __shfl_xor_sync(0xffffffffu, (l & 2) ? a2[0] : a2[1], 2));
+  w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, 1));
+  // lane l now has the two keys of word l >> 1; exponents, and the exponents of the inverse scales
+  const uint32_t e0 = save8_exponent(min((w & 0xFFFFu) >> 7, 255u)), e1 = save8_exponent(min(w >> 23, 255u));
+  const uint32_t inv = (254u - min(e0, 254u)) | ((254u - min(e1, 254u)) << 16);  // 0 for E = 255
+  const int64_t fp = save8_cols(F);
+  const bool live = f < fp;  // the same for the half-warp
+  {
+    const int t = 2 * ((l >> 1) & 3) + (l & 1);  // token of the key this lane stores: g's in lanes 0-7, u's in 8-15
+    if (live && t < rows_left)
+      p.saved_exps[((m0 + t) * 2 + (l >> 3)) * (fp / 16) + (f >> 4)] = (uint8_t)((l & 1) ? e1 : e0);
+  }
+  // codes: v 2^(127 - E) + 1.5 2^23 holds rint(v 2^(127 - E)) in its low byte
+  uint32_t c[4] = {0u, 0u, 0u, 0u};  // bytes of tokens 0-3, 4-7 of g, then of u
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t iw = __shfl_sync(0xffffffffu, inv, (lane & 16) + 2 * j);
+    const float i0 = __uint_as_float(iw << 23), i1 = __uint_as_float((iw & 0xFFFF0000u) << 7);
+    const float v0 = j < 4 ? g[2 * j] : u[2 * j - 8], v1 = j < 4 ? g[2 * j + 1] : u[2 * j - 7];
+    uint32_t b0 = __float_as_uint(fmaf(v0, i0, 12582912.f)), b1 = __float_as_uint(fmaf(v1, i1, 12582912.f));
+    if (i0 == 0.f) b0 = 0u;  // a group that is not finite
+    if (i1 == 0.f) b1 = 0u;
+    c[j >> 1] |= (j & 1) ? __byte_perm(b0, b1, 0x4044) & 0xFFFF0000u : __byte_perm(b0, b1, 0x0040) & 0xFFFFu;
+  }
+  // 4 x 4 bytes turn among four lanes: lane q of a quad gets token q (or 4 + q) of the quad's features
+  const int q = lane & 3;
+  int8_t *dst = p.saved + 2 * (m0 + q) * fp + (f & ~(int64_t)3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t v = c[i], o = __shfl_xor_sync(0xffffffffu, v, 1);
+    v = (q & 1) ? __byte_perm(v, o, 0x3715) : __byte_perm(v, o, 0x6240);  // bytes (t, t of the neighbour) x 2 tokens
+    o = __shfl_xor_sync(0xffffffffu, v, 2);
+    v = (q & 2) ? __byte_perm(v, o, 0x3276) : __byte_perm(v, o, 0x5410);
+    if (live && 4 * (i & 1) + q < rows_left) *reinterpret_cast<uint32_t *>(dst + (i >> 1) * fp + 8 * (i & 1) * fp) = v;
+  }
+}
+
 QL_DEVI void gated_store(const Params &p, const uint32_t (&r)[16], int64_t f, int64_t m0, int lane) {
   const int64_t F = p.N / 2;
-  const bool up = lane >= 16, live = f < F;
-  float g[8], u[8];
+  const bool up = lane >= 16;
+  float g[8], u[8], h[8];
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
     const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, up ? r[t] : r[8 + t], 16));
     g[t] = up ? other : __uint_as_float(r[t]);
     u[t] = up ? __uint_as_float(r[8 + t]) : other;
   }
+  if (f >= F) {  // features past the last: zeros in the checkpoint's padding
+#pragma unroll
+    for (int t = 0; t < 8; ++t) g[t] = u[t] = 0.f;
+  }
   m0 += up ? 8 : 0;
   const int64_t rows_left = p.M - m0;
-  if (live) {
-    __nv_bfloat16 *dst = p.y + m0 * F + f;
+  if (p.act == ACT_SILU) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t < rows_left) *dst = __float2bfloat16_rn(act_value(p.act, g[t]) * u[t]);
-      dst += F;
-    }
+    for (int t = 0; t < 8; ++t) h[t] = act_value(ACT_SILU, g[t]) * u[t];
+  } else {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) h[t] = act_value(p.act, g[t]) * u[t];
   }
-  if (p.saved) {
-    uint32_t k[4] = {0u, 0u, 0u, 0u};  // keys of g (tokens 0-3, 4-7), then of u
-    if (live) {
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        k[t >> 2] |= save8_key(g[t]) << (8 * (t & 3));
-        k[2 + (t >> 2)] |= save8_key(u[t]) << (8 * (t & 3));
-      }
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = __vmaxu4(k[j], __shfl_xor_sync(0xffffffffu, k[j], o));
-    const int64_t fp = save8_cols(F);
-    if (f < fp) {  // columns F .. fp - 1 hold zeros
-      int8_t *dst = p.saved + 2 * m0 * fp + f;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t < rows_left) {
-          const float ig = save8_inverse(save8_exponent((k[t >> 2] >> (8 * (t & 3))) & 0xffu));
-          const float iu = save8_inverse(save8_exponent((k[2 + (t >> 2)] >> (8 * (t & 3))) & 0xffu));
-          dst[0] = (int8_t)(live ? save8_code(g[t], ig) : 0);
-          dst[fp] = (int8_t)(live ? save8_code(u[t], iu) : 0);
-        }
-        dst += 2 * fp;
-      }
-      // lane l of the half-warp stores the exponent of value l: g of tokens 0-7, then u
-      const int l = lane & 15, t = l & 7;
-      const uint32_t kw = l < 4 ? k[0] : l < 8 ? k[1] : l < 12 ? k[2] : k[3];
-      if (t < rows_left)
-        p.saved_exps[((m0 + t) * 2 + (l >> 3)) * (fp / 16) + (f >> 4)] =
-            (uint8_t)save8_exponent((kw >> (8 * (l & 3))) & 0xffu);
-    }
-  }
+  gated_store_h(p, h, F, f, m0, rows_left, lane);
+  if (p.saved) gated_save(p, g, u, F, f, m0, rows_left, lane);
 }
 
-// What a lane needs of its row of a gated tile: its feature, its scale exponent, and the tile's tokens.
+// What a lane needs of its row of a gated tile: its feature, its scale exponent, the tile's tokens, and
+// whether every exponent sum of the warp's rows and these tokens is that of a normal float (then D * 2^e is
+// one multiplication by 2^e built from its bits, the same single rounding as mul_pow2).
 struct GatedRow {
   int64_t f, m0;
   int we, chunks;  // chunks of 16 tokens that hold any
+  bool one_mul;
   QL_DEVI GatedRow(const Params &p, int64_t n_tile, int64_t m_tile, int tt, int e, int lane) {
     const int64_t n = layer_row<true>(n_tile, box_row<true>(32 * e + lane), p.N);
     we = n < p.N ? p.ws.wexp[n] : 0;
     f = n_tile * GATED_F + 16 * e + (lane & 15);
     m0 = m_tile * tt;
     const int64_t left = p.M - m0;
-    chunks = (int)((left < tt ? left : tt) + 15) / 16;
+    const int tokens = (int)(left < tt ? left : tt);
+    chunks = (tokens + 15) / 16;
+    int lo = 1 << 20, hi = -(1 << 20);
+    for (int t = lane; t < tokens; t += 32) {
+      const int xe = __ldg(p.ws.xexp + m0 + t);
+      lo = min(lo, xe);
+      hi = max(hi, xe);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    one_mul = __all_sync(0xffffffffu, lo + we >= -126 && hi + we <= 127);
   }
 };
 
-// Chunk c (16 tokens) of a row's accumulator: undo the power-of-two scales (exponents added first, see
-// mul_pow2), then the gated epilogue.  The exponents of tokens past M are read (their section of the
-// workspace is padded) and not used.
-QL_DEVI void gated_chunk(const Params &p, const GatedRow &row, uint32_t (&r)[16], int c, int lane) {
-  const int64_t m0 = row.m0 + 16 * c;
-  const int4 *xe4 = reinterpret_cast<const int4 *>(p.ws.xexp + m0);
-  int xe[16];
+// The token exponents of chunk c (those of tokens past M are read, their section of the workspace being
+// padded, and not used).
+struct ChunkExp {
+  int4 v[4];
+  QL_DEVI void load(const Params &p, const GatedRow &row, int c) {
+    const int4 *src = reinterpret_cast<const int4 *>(p.ws.xexp + row.m0 + 16 * c);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int4 v = __ldg(xe4 + j);
-    xe[4 * j] = v.x; xe[4 * j + 1] = v.y; xe[4 * j + 2] = v.z; xe[4 * j + 3] = v.w;
+    for (int j = 0; j < 4; ++j) v[j] = __ldg(src + j);
   }
-  int lo = xe[0], hi = xe[0];
-#pragma unroll
-  for (int t = 1; t < 16; ++t) {
-    lo = min(lo, xe[t]);
-    hi = max(hi, xe[t]);
-  }
-  if (__all_sync(0xffffffffu, lo + row.we >= -126 && hi + row.we <= 127)) {
+  QL_DEVI int operator[](int t) const { return (t & 3) == 0 ? v[t >> 2].x : (t & 3) == 1 ? v[t >> 2].y : (t & 3) == 2 ? v[t >> 2].z : v[t >> 2].w; }
+};
+
+// Chunk c of a row's accumulator: undo the power-of-two scales (exponents added first, see mul_pow2),
+// then the gated epilogue.
+QL_DEVI void gated_chunk(const Params &p, const GatedRow &row, uint32_t (&r)[16], const ChunkExp &xe, int c, int lane) {
+  if (row.one_mul) {
     const int w_bits = row.we * (1 << 23) + 0x3F800000;
 #pragma unroll
     for (int t = 0; t < 16; ++t)
@@ -411,7 +480,7 @@ QL_DEVI void gated_chunk(const Params &p, const GatedRow &row, uint32_t (&r)[16]
 #pragma unroll
     for (int t = 0; t < 16; ++t) r[t] = __float_as_uint(mul_pow2(__uint_as_float(r[t]), xe[t] + row.we));
   }
-  gated_store(p, r, row.f, m0, lane);
+  gated_store(p, r, row.f, row.m0 + 16 * c, lane);
 }
 
 template <int FMT, int BITS, int TT, int CPS = 1, bool GATED = false>
@@ -686,26 +755,38 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_acc_empty(a));
+          float4 next[4];  // the chunk after, on its way
+          ChunkExp xe;
+          xe.load(p, row, 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) next[j] = scratch[j * BN];
 #pragma unroll 1
           for (int c = 0; c < row.chunks; ++c) {
             uint32_t r[16];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float4 v = scratch[(4 * c + j) * BN];
-              r[4 * j] = __float_as_uint(v.x);
-              r[4 * j + 1] = __float_as_uint(v.y);
-              r[4 * j + 2] = __float_as_uint(v.z);
-              r[4 * j + 3] = __float_as_uint(v.w);
+              r[4 * j] = __float_as_uint(next[j].x);
+              r[4 * j + 1] = __float_as_uint(next[j].y);
+              r[4 * j + 2] = __float_as_uint(next[j].z);
+              r[4 * j + 3] = __float_as_uint(next[j].w);
             }
-            gated_chunk(p, row, r, c, lane);
+            const ChunkExp cur = xe;
+            if (c + 1 < row.chunks) {
+              xe.load(p, row, c + 1);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) next[j] = scratch[(4 * (c + 1) + j) * BN];
+            }
+            gated_chunk(p, row, r, cur, c, lane);
           }
         } else {
 #pragma unroll 1
           for (int c = 0; c < row.chunks; c += shared_out ? 1 + NG : 1) {
             uint32_t r[16];
             tmem_ld_32x32b_x16(t_acc + 16 * c, r);
+            ChunkExp xe;
+            xe.load(p, row, c);
             tmem_ld_wait();
-            gated_chunk(p, row, r, c, lane);
+            gated_chunk(p, row, r, xe, c, lane);
           }
           tc_fence_before();
           __syncwarp();
@@ -906,8 +987,10 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
         for (int c = 1 + g; c < row.chunks; c += 1 + NG) {
           uint32_t r16[16];
           tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * (wd & 3)) << 16) + 16 * c, r16);
+          ChunkExp xe;
+          xe.load(p, row, c);
           tmem_ld_wait();
-          gated_chunk(p, row, r16, c, lane);
+          gated_chunk(p, row, r16, xe, c, lane);
         }
         tc_fence_before();
       }
