@@ -12,8 +12,8 @@
 //     dx[m][k] = 2^-a_m sum_n (dy[m][n] 2^(a_m - b_n)) (w[n][k] 2^b_n),
 // with a_m chosen so that the row's largest scaled magnitude lies in [2^14, 2^15).
 //
-// Passes: (1) row exponents b_n and the scaled group metadata, transposed so that a stage's words are one
-// TMA box; (2) dy to scaled fp16 rows; (3) the GEMM; (4) the sum of the parts of split tiles.
+// Passes: (1) row exponents b_n; (2) dy to scaled fp16 rows; (3) the scaled group metadata, transposed so that a
+// stage's words are one TMA box; (4) the GEMM; (5) the sum of the parts of split tiles.
 //
 // A CTA an SM.  The tiles of whole waves (as many tiles as CTAs, again and again) are computed alone, all
 // CTAs moving along n together so that each code row and each dy column is fetched from memory about once
@@ -27,7 +27,7 @@
 //   rowexp u8   [Np]         exponent byte of 2^(DY_BIAS - b_n)
 //   meta   u32  [K / gran][Np]  scaled metadata of a run of gran weights: int4 (S, Z S) fp16 pair, int6 the
 //                            scales of its two 16-groups, affine (s, b); zeros past N
-//   partial f32 [2 DX_CTAS][TT][128]
+//   partial f32 [2 DX_CTAS][tokens a tile][128]
 #pragma once
 #include "gated.cuh"
 #include "gemm_sm100.cuh"
@@ -39,9 +39,15 @@ constexpr int BN = 64;    // weight rows a stage (the contraction)
 constexpr int BKT = 128;  // k a tile (the MMA's M)
 constexpr int DX_CTAS = 148;       // CTAs of a launch at most: the SMs of a B200
 constexpr int MIN_SHARE = 8;       // stages a share of a split tile has at least
-constexpr int TT_LARGE = 256, TT_SMALL = 32;
-
-inline int token_tile(int64_t M) { return M <= TT_SMALL ? TT_SMALL : TT_LARGE; }
+// Token tiles: the class (most tokens of a tile, which sizes the rings) and the tokens that a launch's tiles
+// have, a multiple of 16 (the MMA's N) that spreads M evenly.
+constexpr int TT_LARGE = 256, TT_MEDIUM = 128, TT_SMALL = 32;
+inline int tile_class(int64_t M) { return M <= TT_SMALL ? TT_SMALL : M <= TT_MEDIUM ? TT_MEDIUM : TT_LARGE; }
+inline int tile_tokens(int64_t M) {
+  const int c = tile_class(M);
+  const int64_t tiles = (M + c - 1) / c;
+  return (int)(((M + tiles - 1) / tiles + 15) / 16 * 16);
+}
 inline int64_t padded_n(int64_t N) { return (N + 63) / 64 * 64; }
 // weights a metadata word covers
 __host__ __device__ constexpr int gran(int fmt, int group) { return fmt == FMT_AFFINE ? group : 32; }
@@ -57,7 +63,7 @@ struct Workspace {
 inline size_t workspace_bytes(int64_t M, int64_t N, int64_t K, int g) {
   const size_t np = (size_t)padded_n(N);
   return align256((size_t)M * np * 2) + align256((size_t)M * 4) + align256(np) + align256((size_t)(K / g) * np * 4) +
-         (size_t)2 * DX_CTAS * token_tile(M) * BKT * 4;
+         (size_t)2 * DX_CTAS * tile_tokens(M) * BKT * 4;
 }
 
 inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
@@ -76,16 +82,20 @@ inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
   return w;
 }
 
-// ---- pass 1: row exponents and transposed metadata ------------------------------------------------
-// A CTA takes 32 rows x WP_RUNS runs.  It bounds its rows' weights itself (each of the CTAs along a row
-// again: a pass of its own for the bounds cost more than their re-reading from L2), then turns the words
-// through shared memory, read along the row and written along n.  The bound need not be tight -- a looser one
-// only moves the fp16 weights down, and they have 2^29 of range below the top -- so int4 and int6 take it
-// from the steps alone: codes of 255 (int6: -128) times the step.
-constexpr int WP_ROWS = 32, WP_RUNS = 64, WP_THREADS = 256;
+// The passes are a chain of programmatic dependents.  Pass 1 waits for what precedes the call before it
+// lets pass 2 start, and pass 2 for pass 1 before it lets pass 3 start, so passes 2 and 3 find the call's
+// inputs and the row exponents complete; pass 3 waits for pass 2 before it ends, and the GEMM for pass 3.
+// With few tokens pass 2 has few CTAs, and passes 2 and 3 run side by side.
+
+// ---- pass 1: row exponents ------------------------------------------------------------------------
+// One warp a row.  The bound on a row's weights need not be tight -- a looser one only moves the fp16 weights
+// down, and they have 2^29 of range below the top -- so int4 and int6 take it from the steps alone: codes of
+// 255 (int6: -128) times the step.
+//
 // The row factor 2^(DY_BIAS - b_n) that multiplies dy is kept as its exponent byte; the bias brings the
 // factor of ordinary weights (b_n about 16) near 1, so that dy times it stays in range whenever dy does.
-constexpr int DY_BIAS = 16;
+constexpr int DY_BIAS = 16, RE_WARPS = 8;
+constexpr int WP_ROWS = 32, WP_RUNS = 64, WP_THREADS = 256;
 
 template <int FMT, int BITS>
 QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t i, int64_t K, int G) {
@@ -101,64 +111,24 @@ QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, 
   }
 }
 
-// The metadata word of run r (of gran weights) of row n, times sc = 2^b_n.
-template <int FMT>
-QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t r, int64_t K, int G,
-                             float sc) {
-  if constexpr (FMT == FMT_INT4) {
-    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32) + r);
-    const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3));
-    const float S = __fmul_rn((float)(c & 0xffu), f16_bits_to_f32(s)) * sc;
-    return pack_f16x2(S, __fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
-  } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
-    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta + n * (K / 16)) + r);
-    const float st = f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3)));
-    return pack_f16x2(__fmul_rn((float)(int8_t)c, st) * sc, __fmul_rn((float)(int8_t)(c >> 8), st) * sc);
-  } else {
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G) + r);
-    return pack_f16x2(bf16_bits_to_f32(c) * sc, bf16_bits_to_f32(c >> 16) * sc);
-  }
-}
-
 template <int FMT, int BITS>
-__global__ void __launch_bounds__(WP_THREADS) w_prep_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
-                                                            int64_t K, int G, int64_t np, Workspace ws) {
-  constexpr int RW = WP_ROWS / (WP_THREADS / 32);  // rows a warp
-  __shared__ uint32_t turn[WP_ROWS][WP_RUNS + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS + RW * warp;
-  const int64_t bounds = FMT == FMT_AFFINE ? K / G : K / 256, runs = K / gran(FMT, G);
-  float top[RW];
-#pragma unroll
-  for (int j = 0; j < RW; ++j) top[j] = 0.f;
-  for (int64_t i = lane; i < bounds; i += 32)
-#pragma unroll
-    for (int j = 0; j < RW; ++j) top[j] = fmaxf(top[j], meta_bound<FMT, BITS>(gmeta, steps, min(n0 + j, N - 1), i, K, G));
-  float scale[RW];
-#pragma unroll
-  for (int j = 0; j < RW; ++j) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-    // at least -111, so that 127 + DY_BIAS - b is an exponent byte (a weight of 2^125 overflows fp16 then)
-    const int b = n0 + j < N ? max(scale_exponent(top[j], 14), -111) : DY_BIAS;
-    scale[j] = exp2i(b);
-    if (blockIdx.y == 0 && lane == 0) ws.rowexp[n0 + j] = (uint8_t)(127 + DY_BIAS - b);
+__global__ void __launch_bounds__(32 * RE_WARPS) row_exp_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
+                                                                int64_t K, int G, Workspace ws) {
+  const int lane = threadIdx.x & 31;
+  const int64_t n = (int64_t)blockIdx.x * RE_WARPS + (threadIdx.x >> 5);  // < Np
+  const int64_t words = FMT == FMT_AFFINE ? K / G : K / 256;
+  pdl_wait();
+  pdl_launch_dependents();
+  float top = 0.f;
+  if (n < N) {
+#pragma unroll 4
+    for (int64_t i = lane; i < words; i += 32) top = fmaxf(top, meta_bound<FMT, BITS>(gmeta, steps, n, i, K, G));
   }
-  const int64_t r0 = (int64_t)blockIdx.y * WP_RUNS;
 #pragma unroll
-  for (int j = 0; j < RW; ++j)
-#pragma unroll
-    for (int i = 0; i < WP_RUNS / 32; ++i) {
-      const int64_t n = n0 + j, r = r0 + 32 * i + lane;
-      turn[RW * warp + j][32 * i + lane] =
-          n < N && r < runs ? scaled_meta<FMT>(gmeta, steps, n, r, K, G, scale[j]) : 0u;
-    }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < WP_RUNS / (WP_THREADS / 32); ++i) {
-    const int r = warp + (WP_THREADS / 32) * i;
-    if (r0 + r < runs) ws.meta[(r0 + r) * np + (int64_t)blockIdx.x * WP_ROWS + lane] = turn[lane][r];
-  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // at least -111, so that 127 + DY_BIAS - b is an exponent byte (a weight of 2^125 overflows fp16 then)
+  const int b = n < N ? max(scale_exponent(top, 14), -111) : DY_BIAS;
+  if (lane == 0) ws.rowexp[n] = (uint8_t)(127 + DY_BIAS - b);
 }
 
 // ---- pass 2: dy (or (dg | du)) to scaled fp16 rows ----------------------------------------------------
@@ -243,6 +213,14 @@ __global__ void __launch_bounds__(DY_THREADS) dy_prep_kernel(const __nv_bfloat16
     for (int r = 0; r < DY_REGS; ++r) {
       const int64_t i = threadIdx.x + r * DY_THREADS;
       q[r] = i < nv ? load8<VEC>(row, 8 * i, N) : zero;
+    }
+  }
+  pdl_wait();  // the row exponents
+  pdl_launch_dependents();
+  if (kept) {
+#pragma unroll
+    for (int r = 0; r < DY_REGS; ++r) {
+      const int64_t i = threadIdx.x + r * DY_THREADS;
       f[r] = i < nv ? fac[i] : make_uint2(0u, 0u);
     }
 #pragma unroll
@@ -323,6 +301,8 @@ __global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Work
   const uint4 *cg = reinterpret_cast<const uint4 *>(p.codes + 2 * m * fp), *cu = cg + groups;
   const uint8_t *eg = p.exps + 2 * m * groups, *eu = eg + groups;
   float top = 0.f;
+  pdl_wait();  // the row exponents
+  pdl_launch_dependents();
   for (int i = threadIdx.x; i < groups; i += DGU_THREADS) {
     const int64_t f = 16 * (int64_t)i;
     const uint4 d0 = load8<VEC>(dh, f, p.F), d1 = load8<VEC>(dh, f + 8, p.F);
@@ -380,45 +360,101 @@ __global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Work
   if (threadIdx.x == 0) ws.dexp[m] = -(a + DY_BIAS);
 }
 
-// ---- pass 3: the GEMM ------------------------------------------------------------------------------
+// ---- pass 3: scaled metadata, transposed ------------------------------------------------------------
+// The metadata word of run r (of gran weights) of row n, times sc = 2^b_n.
+template <int FMT>
+QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t r, int64_t K, int G,
+                             float sc) {
+  if constexpr (FMT == FMT_INT4) {
+    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32) + r);
+    const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3));
+    const float S = __fmul_rn((float)(c & 0xffu), f16_bits_to_f32(s)) * sc;
+    return pack_f16x2(S, __fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
+  } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
+    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta + n * (K / 16)) + r);
+    const float st = f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3)));
+    return pack_f16x2(__fmul_rn((float)(int8_t)c, st) * sc, __fmul_rn((float)(int8_t)(c >> 8), st) * sc);
+  } else {
+    const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G) + r);
+    return pack_f16x2(bf16_bits_to_f32(c) * sc, bf16_bits_to_f32(c >> 16) * sc);
+  }
+}
+
+// A CTA turns the words of 32 rows x 64 runs through shared memory, read along the row and written along n.
+template <int FMT>
+__global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
+                                                          int64_t K, int G, int64_t np, Workspace ws) {
+  constexpr int RW = WP_ROWS / (WP_THREADS / 32);  // rows a warp
+  __shared__ uint32_t turn[WP_ROWS][WP_RUNS + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS, r0 = (int64_t)blockIdx.y * WP_RUNS, runs = K / gran(FMT, G);
+  pdl_launch_dependents();
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+    const int64_t n = n0 + RW * warp + j;
+    const float sc = exp2i(127 + DY_BIAS - (int)ws.rowexp[n]);
+#pragma unroll
+    for (int i = 0; i < WP_RUNS / 32; ++i) {
+      const int64_t r = r0 + 32 * i + lane;
+      turn[RW * warp + j][32 * i + lane] = n < N && r < runs ? scaled_meta<FMT>(gmeta, steps, n, r, K, G, sc) : 0u;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WP_RUNS / (WP_THREADS / 32); ++i) {
+    const int r = warp + (WP_THREADS / 32) * i;
+    if (r0 + r < runs) ws.meta[(r0 + r) * np + n0 + lane] = turn[lane][r];
+  }
+  pdl_wait();  // for pass 2
+}
+
+// ---- pass 4: the GEMM ------------------------------------------------------------------------------
 constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, WARP_DEQ0 = 8;
 __host__ __device__ constexpr int deq_groups(int tt) { return tt == TT_LARGE ? 2 : 4; }
 __host__ __device__ constexpr int num_threads(int tt) { return (WARP_DEQ0 + 4 * deq_groups(tt)) * 32; }
 
-// A stage: the transposed weight tile (A), the dy tile (B), the packed codes and the metadata words.
+// Two rings.  What TMA brings -- the dy tile (B), the packed codes and the metadata words -- waits in a ring as
+// deep as shared memory allows (up to 16), because for few tokens the stream of codes is what bounds the kernel
+// and needs bytes in flight; the transposed weight tiles (A, 16 KB each) only have to keep the tensor core
+// busy: up to four.
 __host__ __device__ constexpr int code_row(int fmt, int bits) { return BKT * gemm::code_bits(fmt, bits) / 8; }
 constexpr int A_BYTES = BN * BKT * 2;
 __host__ __device__ constexpr int b_bytes(int tt) { return tt * BN * 2; }
 __host__ __device__ constexpr int p_bytes(int fmt, int bits) { return BN * code_row(fmt, bits); }
 constexpr int META_BYTES = BN * 4 * 4;  // up to four runs of 32 k
 __host__ __device__ constexpr int stage_bytes(int fmt, int bits, int tt) {
-  return A_BYTES + b_bytes(tt) + p_bytes(fmt, bits) + META_BYTES;
+  return b_bytes(tt) + p_bytes(fmt, bits) + META_BYTES;
 }
-__host__ __device__ constexpr int smem_need(int fmt, int bits, int tt, int st) {
-  return st * stage_bytes(fmt, bits, tt) + (3 * st + 5) * 8 + 16 + 1024;
+__host__ __device__ constexpr int smem_need(int fmt, int bits, int tt, int st, int as) {
+  return st * stage_bytes(fmt, bits, tt) + as * A_BYTES + (2 * st + as + 5) * 8 + 16 + 1024;
+}
+__host__ __device__ constexpr int a_stages(int fmt, int bits, int tt) {
+  return smem_need(fmt, bits, tt, 4, 4) <= gemm::SMEM_LIMIT ? 4 : 3;
 }
 __host__ __device__ constexpr int stages(int fmt, int bits, int tt) {
-  return smem_need(fmt, bits, tt, 6) <= gemm::SMEM_LIMIT ? 6
-       : smem_need(fmt, bits, tt, 5) <= gemm::SMEM_LIMIT ? 5
-       : smem_need(fmt, bits, tt, 4) <= gemm::SMEM_LIMIT ? 4 : 3;
+  int st = 16;
+  while (smem_need(fmt, bits, tt, st, a_stages(fmt, bits, tt)) > gemm::SMEM_LIMIT) --st;
+  return st;
 }
 __host__ __device__ constexpr int smem_bytes(int fmt, int bits, int tt) {
-  return smem_need(fmt, bits, tt, stages(fmt, bits, tt));
+  return smem_need(fmt, bits, tt, stages(fmt, bits, tt), a_stages(fmt, bits, tt));
 }
 
 // How the tiles are dealt: `waves` whole waves of `ctas` tiles, then the `rest` tiles that are left, their
 // rest * steps stages cut into `shares` equal ranges, one a CTA.
 struct Deal {
   int64_t m_tiles, k_tiles;
-  int steps;  // stages a tile: Np / 64
+  int tokens;  // a tile
+  int steps;   // stages a tile: Np / 64
   int ctas, waves, rest, shares;
   __host__ __device__ bool joins() const { return shares != rest; }  // else a share is a whole tile
   __host__ __device__ int64_t share_begin(int c) const { return (int64_t)rest * steps * c / shares; }
 };
 
-inline Deal deal(int64_t M, int64_t N, int64_t K, int tt, int sms) {
+inline Deal deal(int64_t M, int64_t N, int64_t K, int sms) {
   Deal d;
-  d.m_tiles = (M + tt - 1) / tt;
+  d.tokens = tile_tokens(M);
+  d.m_tiles = (M + d.tokens - 1) / d.tokens;
   d.k_tiles = (K + BKT - 1) / BKT;
   d.steps = (int)(padded_n(N) / BN);
   d.ctas = sms < DX_CTAS ? sms : DX_CTAS;
@@ -548,30 +584,31 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
     gemm_dx_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_codes,
                    const __grid_constant__ CUtensorMap map_codes_hi, const __grid_constant__ CUtensorMap map_meta,
                    Params p) {
-  constexpr int STAGES = stages(FMT, BITS, TT), NG = deq_groups(TT);
+  constexpr int STAGES = stages(FMT, BITS, TT), AST = a_stages(FMT, BITS, TT), NG = deq_groups(TT);
   constexpr int PROW = code_row(FMT, BITS);
-  constexpr int OFF_B = A_BYTES, OFF_P = OFF_B + b_bytes(TT), OFF_M = OFF_P + p_bytes(FMT, BITS);
-  constexpr int STAGE = stage_bytes(FMT, BITS, TT);
+  constexpr int OFF_P = b_bytes(TT), OFF_M = OFF_P + p_bytes(FMT, BITS);  // in a stage, after the dy tile
+  constexpr int STAGE = stage_bytes(FMT, BITS, TT), OFF_A = STAGES * STAGE;
   static_assert(STAGE % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
+  static_assert(STAGES >= AST, "an A slot's previous MMAs are found by their stage");
   constexpr uint32_t TMEM_COLS = 2 * TT;
-  static_assert(NG < STAGES, "a group's step through the ring crosses its end at most once");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE);
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 3 * STAGES + 5);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_A + AST * A_BYTES);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + AST + 5);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
   auto bar_tma_full = [&](int s) { return smem_u32(bars + s); };
-  auto bar_a_full = [&](int s) { return smem_u32(bars + STAGES + s); };
-  auto bar_empty = [&](int s) { return smem_u32(bars + 2 * STAGES + s); };
-  auto bar_acc_full = [&](int a) { return smem_u32(bars + 3 * STAGES + a); };
-  auto bar_acc_empty = [&](int a) { return smem_u32(bars + 3 * STAGES + 2 + a); };
-  const uint32_t bar_final = smem_u32(bars + 3 * STAGES + 4);
+  auto bar_empty = [&](int s) { return smem_u32(bars + STAGES + s); };
+  auto bar_a_full = [&](int s) { return smem_u32(bars + 2 * STAGES + s); };
+  auto bar_acc_full = [&](int a) { return smem_u32(bars + 2 * STAGES + AST + a); };
+  auto bar_acc_empty = [&](int a) { return smem_u32(bars + 2 * STAGES + AST + 2 + a); };
+  const uint32_t bar_final = smem_u32(bars + 2 * STAGES + AST + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = (int)blockIdx.x;
   // runs of a tile and bytes of its metadata box
   const int runs = FMT == FMT_AFFINE ? (p.G >= BKT ? 1 : BKT / p.G) : 4;
-  const uint32_t stage_tx = (uint32_t)(b_bytes(TT) + p_bytes(FMT, BITS) + runs * BN * 4);
+  const int tokens = p.deal.tokens;
+  const uint32_t stage_tx = (uint32_t)(b_bytes(tokens) + p_bytes(FMT, BITS) + runs * BN * 4);
 
   auto step_ring = [](int &slot, uint32_t &phase, int by, int depth) {
     slot += by;
@@ -584,9 +621,9 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_tma_full(s), 1);
-      mbar_init(bar_a_full(s), 4);
       mbar_init(bar_empty(s), 1);
     }
+    for (int s = 0; s < AST; ++s) mbar_init(bar_a_full(s), 4);
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_acc_full(a), 1);
       mbar_init(bar_acc_empty(a), 4);
@@ -603,6 +640,8 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  pdl_launch_dependents();
+  pdl_wait();  // the preparation passes' results
 
   if (warp == WARP_TMA) {
     if (lane == 0) {
@@ -625,7 +664,7 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
           }
           const uint32_t b = bar_tma_full(s), dst = sbase + s * STAGE;
           mbar_arrive_expect_tx(b, stage_tx);
-          tma_load_2d(dst + OFF_B, &map_dy, b, st * BN, (int32_t)(m_tile * TT));
+          tma_load_2d(dst, &map_dy, b, st * BN, (int32_t)(m_tile * tokens));
           if constexpr (FMT == FMT_INT6P) {  // half a super-block: 64 low-plane bytes, 32 high-plane bytes
             const int32_t sb = (int32_t)(192 * (k_tile >> 1)), h = (int32_t)(k_tile & 1);
             tma_load_2d(dst + OFF_P, &map_codes, b, sb + 64 * h, st * BN);
@@ -648,9 +687,9 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
     }
   } else if (warp == WARP_MMA) {
     if (lane == 0) {
-      constexpr uint32_t idesc = umma_idesc_f16_f32(BKT, TT) | IDESC_A_M_MAJOR;
-      int s = 0, n = 0;
-      uint32_t ph = 0;
+      const uint32_t idesc = umma_idesc_f16_f32(BKT, tokens) | IDESC_A_M_MAJOR;
+      int s = 0, as = 0, n = 0;
+      uint32_t ph = 0, aph = 0;
       bool ok = true, issued = false;
       Piece pc;
       for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i, ++n) {
@@ -660,19 +699,20 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
         const uint32_t d_tmem = tmem_base + (uint32_t)(a * TT);
         for (int st = pc.step0; st < pc.step1; ++st) {
           // the dequantisers waited for this stage's copies, so the dy tile has landed too
-          if (!mbar_wait_bounded(bar_a_full(s), ph, abort_flag)) {
+          if (!mbar_wait_bounded(bar_a_full(as), aph, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = umma_desc_m_sw128(sbase + s * STAGE), bd = umma_desc_k_sw128(sbase + s * STAGE + OFF_B);
+          const uint64_t ad = umma_desc_m_sw128(sbase + OFF_A + as * A_BYTES), bd = umma_desc_k_sw128(sbase + s * STAGE);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)  // 16 rows n: 2048 bytes of A, 32 bytes along B's rows
             umma_f16_ss(d_tmem, ad + (uint64_t)(kk * (2048 >> 4)), bd + (uint64_t)(kk * (32 >> 4)), idesc,
                         st != pc.step0 || kk != 0);
-          umma_commit(bar_empty(s));
+          umma_commit(bar_empty(s));  // the stage, and the A slot
           issued = true;
           step_ring(s, ph, 1, STAGES);
+          step_ring(as, aph, 1, AST);
         }
         if (ok) umma_commit(bar_acc_full(a));
       }
@@ -690,35 +730,35 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
       const int a = i & 1;
       const int64_t k_tile = pc.tile / p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
       const int64_t k = k_tile * BKT + out_k(32 * e + lane);
-      const int tokens = (int)(p.M - m_tile * TT < TT ? p.M - m_tile * TT : TT);
+      const int64_t m0 = m_tile * tokens;
+      const int valid = (int)(p.M - m0 < tokens ? p.M - m0 : tokens);
       if (!mbar_wait_bounded(bar_acc_full(a), (i >> 1) & 1, abort_flag)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < TT / 16; ++c) {
+      for (int c = 0; c < tokens / 16; ++c) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * e) << 16) + (uint32_t)(a * TT + 16 * c), r);
         tmem_ld_wait();
-        if (c == TT / 16 - 1) {
+        if (c == tokens / 16 - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_acc_empty(a));
         }
         if (pc.slot < 0) {
           if (k < p.K) {
-            __nv_bfloat16 *dst = p.dx + (m_tile * TT + 16 * c) * p.K + k;
+            __nv_bfloat16 *dst = p.dx + (m0 + 16 * c) * p.K + k;
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
-              if (16 * c + t < tokens)
-                *dst = __float2bfloat16_rn(
-                    mul_pow2(__uint_as_float(r[t]), __ldg(p.dexp + m_tile * TT + 16 * c + t)));
+              if (16 * c + t < valid)
+                *dst = __float2bfloat16_rn(mul_pow2(__uint_as_float(r[t]), __ldg(p.dexp + m0 + 16 * c + t)));
               dst += p.K;
             }
           }
         } else {
-          float *dst = p.partial + ((int64_t)pc.slot * TT + 16 * c) * BKT + 32 * e + lane;
+          float *dst = p.partial + ((int64_t)pc.slot * tokens + 16 * c) * BKT + 32 * e + lane;
 #pragma unroll
           for (int t = 0; t < 16; ++t)
-            if (16 * c + t < tokens) dst[t * BKT] = __uint_as_float(r[t]);
+            if (16 * c + t < valid) dst[t * BKT] = __uint_as_float(r[t]);
         }
       }
     }
@@ -726,8 +766,10 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
     const int wd = warp - WARP_DEQ0, g = wd >> 2;
     const int tau = 32 * (wd & 3) + lane;
     const int n = tau & 63, half = tau >> 6;  // row of the stage, 64-k half of the tile
-    int s = 0, turn = 0;
+    int s = 0, as = 0, turn = 0;
     uint32_t ph = 0;
+    int es = STAGES - AST;  // stage of the step AST before this one, whose MMAs read this step's A slot
+    uint32_t eph = 1;       // and its phase (the first AST steps find their slots free: the phase before the first)
     bool ok = true;
     Piece pc;
     for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i) {
@@ -737,9 +779,13 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
             ok = false;
             break;
           }
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty(es), eph, abort_flag))) {
+            ok = false;
+            break;
+          }
           const uint8_t *stg = smem + s * STAGE;
           const uint32_t *meta = reinterpret_cast<const uint32_t *>(stg + OFF_M) + n;
-          uint8_t *arow = smem + s * STAGE + half * (BN * 128) + n * 128;
+          uint8_t *arow = smem + OFF_A + as * A_BYTES + half * (BN * 128) + n * 128;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // the half's 32-weight runs
             const int run = 2 * half + h;
@@ -791,10 +837,12 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_a_full(s));
+          if (lane == 0) mbar_arrive(bar_a_full(as));
         }
         if (++turn == NG) turn = 0;
         step_ring(s, ph, 1, STAGES);
+        step_ring(es, eph, 1, STAGES);
+        if (++as == AST) as = 0;
       }
     }
   }
@@ -806,12 +854,11 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
   }
 }
 
-// ---- pass 4: the sums of the split tiles' parts -------------------------------------------------------
+// ---- pass 5: the sums of the split tiles' parts -------------------------------------------------------
 // A CTA takes 16 tokens of a tile, a thread 8 rows (eight consecutive k, see out_k) of one of them; the
 // parts are added in the order of the shares.
 constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 8);
 
-template <int TT>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
   __shared__ int range[3];  // first share, its slot, end of the shares
   const Deal &d = p.deal;
@@ -827,16 +874,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
     while (d.share_begin(e - 1) >= hi) --e;
     range[2] = e;
   }
+  pdl_launch_dependents();
+  pdl_wait();  // the parts
   __syncthreads();
   const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
   const int t = blockIdx.y * JOIN_TOKENS + threadIdx.x / (BKT / 8), r = 8 * (threadIdx.x % (BKT / 8));
-  const int64_t m = m_tile * TT + t, k = k_tile * BKT + r;
-  if (t >= TT || m >= p.M || k >= p.K) return;
+  const int64_t m = m_tile * d.tokens + t, k = k_tile * BKT + r;
+  if (t >= d.tokens || m >= p.M || k >= p.K) return;
   const int end = range[2];
   int slot = range[1];
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int c = range[0]; c < end; ++c) {
-    const float4 *src = reinterpret_cast<const float4 *>(p.partial + ((int64_t)slot * TT + t) * BKT + r);
+    const float4 *src = reinterpret_cast<const float4 *>(p.partial + ((int64_t)slot * d.tokens + t) * BKT + r);
     const float4 x = __ldcg(src), y = __ldcg(src + 1);
     v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
     v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;

@@ -672,7 +672,23 @@ ql_status launch_gated(const ql_desc *d, const ql_packed_const *w, const void *x
 // ---- the input gradient ------------------------------------------------------
 namespace {
 
-// The three passes after dy has been prepared by `prep` (pass 2, which reads pass 1's row exponents).
+// A launch as a programmatic dependent of the kernel before it on the stream.
+template <class... Params, class... Args>
+bool launch_dependent(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = st;
+  c.attrs = pdl;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, Params(args)...) == cudaSuccess;
+}
+
+// The passes of gemm_dx.cuh; `prep` launches pass 2.
 template <int FMT, int BITS, int TT, class Prep>
 ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t M, void *dx_out, void *workspace,
                             cudaStream_t st, int sms, const Prep &prep) {
@@ -680,18 +696,21 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
   const int64_t N = d->N, K = d->K, np = padded_n(N);
   const int gr = gran(FMT, d->group);
   const Workspace ws = carve(workspace, M, N, K, gr);
-  const dim3 wp_grid((unsigned)(np / WP_ROWS), (unsigned)((K / gr + WP_RUNS - 1) / WP_RUNS));
-  w_prep_kernel<FMT, BITS><<<wp_grid, WP_THREADS, 0, st>>>(
-      static_cast<const uint8_t *>(w->gmeta), static_cast<const uint8_t *>(w->steps), N, K, d->group, np, ws);
-  prep(ws, np);
+  const auto *gmeta = static_cast<const uint8_t *>(w->gmeta), *steps = static_cast<const uint8_t *>(w->steps);
+  Params p;
+  p.M = M; p.N = N; p.K = K; p.G = d->group;
+  p.deal = deal(M, N, K, sms);
+  p.dexp = ws.dexp;
+  p.partial = ws.partial;
+  p.dx = static_cast<__nv_bfloat16 *>(dx_out);
   const uint64_t row_bytes = (uint64_t)K * gemm::code_bits(FMT, BITS) / 8;
   CUtensorMap my, mc, mh, mm;
   constexpr bool PLANAR = FMT == FMT_INT6P;
   constexpr uint32_t box = PLANAR ? 64u : (uint32_t)code_row(FMT, BITS);
   constexpr CUtensorMapSwizzle sw = box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                   : box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-  if (!encode_2d(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.dy16, (uint64_t)np, (uint64_t)M, (uint64_t)np * 2, BN, TT,
-                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!encode_2d(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.dy16, (uint64_t)np, (uint64_t)M, (uint64_t)np * 2, BN,
+                 (uint32_t)p.deal.tokens, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes, box, BN, sw) ||
       !encode_2d(&mm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws.meta, (uint64_t)np, (uint64_t)(K / gr), (uint64_t)np * 4, BN,
                  gr >= BKT ? 1u : (uint32_t)(BKT / gr), CU_TENSOR_MAP_SWIZZLE_NONE))
@@ -700,14 +719,8 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
   if (PLANAR && !encode_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes, 32, BN,
                            CU_TENSOR_MAP_SWIZZLE_NONE))
     return cuda_failed();
-  Params p;
-  p.M = M; p.N = N; p.K = K; p.G = d->group;
-  p.deal = deal(M, N, K, TT, sms);
-  p.dexp = ws.dexp;
-  p.partial = ws.partial;
-  p.dx = static_cast<__nv_bfloat16 *>(dx_out);
   constexpr int smem = smem_bytes(FMT, BITS, TT);
-  auto kern = gemm_dx_kernel<FMT, BITS, TT>;
+  auto *kern = gemm_dx_kernel<FMT, BITS, TT>;
   static thread_local int configured_dev = -1;  // per instantiation and thread
   int dev = 0;
   cudaGetDevice(&dev);
@@ -716,19 +729,30 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
       return cuda_failed();
     configured_dev = dev;
   }
-  kern<<<(unsigned)(p.deal.waves ? p.deal.ctas : p.deal.shares), num_threads(TT), smem, st>>>(my, mc, mh, mm, p);
-  if (p.deal.joins())
-    join_kernel<TT><<<dim3((unsigned)p.deal.rest, (unsigned)(((M < TT ? M : TT) + JOIN_TOKENS - 1) / JOIN_TOKENS)),
-                      JOIN_THREADS, 0, st>>>(p);
+  if (!launch_dependent(row_exp_kernel<FMT, BITS>, dim3((unsigned)(np / RE_WARPS)), 32 * RE_WARPS, 0, st, gmeta, steps,
+                        N, K, d->group, ws) ||
+      !prep(ws, np) ||
+      !launch_dependent(meta_kernel<FMT>, dim3((unsigned)(np / WP_ROWS), (unsigned)((K / gr + WP_RUNS - 1) / WP_RUNS)),
+                        WP_THREADS, 0, st, gmeta, steps, N, K, d->group, np, ws) ||
+      !launch_dependent(kern, dim3((unsigned)(p.deal.waves ? p.deal.ctas : p.deal.shares)), num_threads(TT), smem, st,
+                        my, mc, mh, mm, p))
+    return cuda_failed();
+  if (p.deal.joins() &&
+      !launch_dependent(join_kernel,
+                        dim3((unsigned)p.deal.rest, (unsigned)((std::min<int64_t>(M, p.deal.tokens) + JOIN_TOKENS - 1) / JOIN_TOKENS)),
+                        JOIN_THREADS, 0, st, p))
+    return cuda_failed();
   return launched();
 }
 
 template <int FMT, int BITS, class Prep>
 ql_status launch_gemm_dx(const ql_desc *d, const ql_packed_const *w, int64_t M, void *dx_out, void *workspace,
                          cudaStream_t st, int sms, const Prep &prep) {
-  if (dx::token_tile(M) == dx::TT_SMALL)
-    return launch_gemm_dx_tt<FMT, BITS, dx::TT_SMALL>(d, w, M, dx_out, workspace, st, sms, prep);
-  return launch_gemm_dx_tt<FMT, BITS, dx::TT_LARGE>(d, w, M, dx_out, workspace, st, sms, prep);
+  switch (dx::tile_class(M)) {
+    case dx::TT_SMALL: return launch_gemm_dx_tt<FMT, BITS, dx::TT_SMALL>(d, w, M, dx_out, workspace, st, sms, prep);
+    case dx::TT_MEDIUM: return launch_gemm_dx_tt<FMT, BITS, dx::TT_MEDIUM>(d, w, M, dx_out, workspace, st, sms, prep);
+    default: return launch_gemm_dx_tt<FMT, BITS, dx::TT_LARGE>(d, w, M, dx_out, workspace, st, sms, prep);
+  }
 }
 
 template <class Prep>
@@ -1231,8 +1255,8 @@ ql_status qlinear_gemm_dx(const ql_desc *d, const ql_packed_const *w, const void
   const int64_t N = d->N;
   const auto *yb = static_cast<const __nv_bfloat16 *>(dy);
   return gemm_dx_call(d, w, M, dx_out, workspace, s, di->sms, [=](const dx::Workspace &ws, int64_t np) {
-    if (N % 8 == 0) dx::dy_prep_kernel<true><<<(unsigned)M, dx::DY_THREADS, 0, s>>>(yb, N, np, ws);
-    else dx::dy_prep_kernel<false><<<(unsigned)M, dx::DY_THREADS, 0, s>>>(yb, N, np, ws);
+    return launch_dependent(N % 8 == 0 ? dx::dy_prep_kernel<true> : dx::dy_prep_kernel<false>, dim3((unsigned)M),
+                            dx::DY_THREADS, 0, s, yb, N, np, ws);
   });
 }
 
@@ -1266,7 +1290,7 @@ ql_status qlinear_gated_backward(const ql_desc *d, const ql_packed_const *w, con
                  : act == ACT_GELU_TANH ? (vec ? dx::dgu_prep_kernel<ACT_GELU_TANH, true>
                                                : dx::dgu_prep_kernel<ACT_GELU_TANH, false>)
                                         : (vec ? dx::dgu_prep_kernel<ACT_GELU, true> : dx::dgu_prep_kernel<ACT_GELU, false>);
-    kern<<<(unsigned)M, dx::DGU_THREADS, 0, s>>>(g, ws);
+    return launch_dependent(kern, dim3((unsigned)M), dx::DGU_THREADS, 0, s, g, ws);
   });
 }
 
