@@ -97,6 +97,30 @@ QL_DEVI bool mbar_wait_bounded(uint32_t bar, uint32_t parity, volatile int *abor
   }
 }
 
+// Wait for an mbarrier phase, letting the hardware suspend the thread (up to a hint, in ns) instead
+// of spinning; bounded like mbar_wait_bounded.
+QL_DEVI bool mbar_wait_suspend(uint32_t bar, uint32_t parity, volatile int *abort) {
+  const long long t0 = clock64();
+  const uint32_t hint = 1000000u;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(hint)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > QL_WAIT_LIMIT_CYCLES) {
+      atomicOr(&g_ql_status, QL_DEV_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // TMA (bulk tensor copy, global -> shared, completion counted on an mbarrier)
 // ---------------------------------------------------------------------------

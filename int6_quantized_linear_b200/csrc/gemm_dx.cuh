@@ -12,6 +12,11 @@
 //     dx[m][k] = 2^-a_m sum_n (dy[m][n] 2^(a_m - b_n)) (w[n][k] 2^b_n),
 // with a_m chosen so that the row's largest scaled magnitude lies in [2^14, 2^15).
 //
+// A code enters the arithmetic as it lies: masked into the low ten bits of a half it is the subnormal
+// q 2^-24, so one mask and one fused multiply-add (with 2^24 times the scale) make a weight, without the
+// detour through 1024 + q.  For 2^24 times the scale to be an fp16 number the scaled weights sit lower than in
+// the forward kernels, below 2^-5 (4-bit affine 2^-6, 2-bit 2^-9); fp16 has 2^15 and more of range below that.
+//
 // Passes: (1) row exponents b_n; (2) dy to scaled fp16 rows; (3) the scaled group metadata, transposed so that a
 // stage's words are one TMA box; (4) the GEMM; (5) the sum of the parts of split tiles.
 //
@@ -93,8 +98,13 @@ inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
 // 255 (int6: -128) times the step.
 //
 // The row factor 2^(DY_BIAS - b_n) that multiplies dy is kept as its exponent byte; the bias brings the
-// factor of ordinary weights (b_n about 16) near 1, so that dy times it stays in range whenever dy does.
-constexpr int DY_BIAS = 16, RE_WARPS = 8;
+// factor of ordinary weights (b_n about -4) near 1, so that dy times it stays in range whenever dy does.
+constexpr int DY_BIAS = -4, RE_WARPS = 8;
+// the exponent that a row's bound gets: the largest scale, at most bound / 15 (int4), bound / 32 (int6) or
+// 2 bound / (2^bits - 1) (affine), times 2^24 has to stay below 65504
+__host__ __device__ constexpr int w_top(int fmt, int bits) {
+  return fmt != FMT_AFFINE || bits == 8 ? -6 : bits == 4 ? -7 : -10;
+}
 constexpr int WP_ROWS = 32, WP_RUNS = 64, WP_THREADS = 256;
 
 template <int FMT, int BITS>
@@ -126,8 +136,8 @@ __global__ void __launch_bounds__(32 * RE_WARPS) row_exp_kernel(const uint8_t *g
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  // at least -111, so that 127 + DY_BIAS - b is an exponent byte (a weight of 2^125 overflows fp16 then)
-  const int b = n < N ? max(scale_exponent(top, 14), -111) : DY_BIAS;
+  // at most 120, so that 127 + DY_BIAS - b is an exponent byte (weights below 2^-126 lose bits then)
+  const int b = n < N ? min(scale_exponent(top, w_top(FMT, BITS)), 120) : DY_BIAS;
   if (lane == 0) ws.rowexp[n] = (uint8_t)(127 + DY_BIAS - b);
 }
 
@@ -361,7 +371,8 @@ __global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Work
 }
 
 // ---- pass 3: scaled metadata, transposed ------------------------------------------------------------
-// The metadata word of run r (of gran weights) of row n, times sc = 2^b_n.
+// The metadata word of run r (of gran weights) of row n: the scales times 2^24 sc, Z S and b times sc = 2^b_n.
+constexpr float SUB = 16777216.f;  // 2^24
 template <int FMT>
 QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t r, int64_t K, int G,
                              float sc) {
@@ -369,14 +380,14 @@ QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t
     const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32) + r);
     const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3));
     const float S = __fmul_rn((float)(c & 0xffu), f16_bits_to_f32(s)) * sc;
-    return pack_f16x2(S, __fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
+    return pack_f16x2(S * SUB, __fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
   } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
     const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta + n * (K / 16)) + r);
     const float st = f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3)));
-    return pack_f16x2(__fmul_rn((float)(int8_t)c, st) * sc, __fmul_rn((float)(int8_t)(c >> 8), st) * sc);
+    return pack_f16x2(__fmul_rn((float)(int8_t)c, st) * sc * SUB, __fmul_rn((float)(int8_t)(c >> 8), st) * sc * SUB);
   } else {
     const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G) + r);
-    return pack_f16x2(bf16_bits_to_f32(c) * sc, bf16_bits_to_f32(c >> 16) * sc);
+    return pack_f16x2(bf16_bits_to_f32(c) * sc * SUB, bf16_bits_to_f32(c >> 16) * sc);
   }
 }
 
@@ -409,8 +420,11 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
 }
 
 // ---- pass 4: the GEMM ------------------------------------------------------------------------------
-constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, WARP_DEQ0 = 8;
-__host__ __device__ constexpr int deq_groups(int tt) { return tt == TT_LARGE ? 2 : 4; }
+constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, WARP_DEQ0 = 8, NPROD = 3;
+#ifndef NG_TRY
+#define NG_TRY 4
+#endif
+__host__ __device__ constexpr int deq_groups(int tt) { return tt == TT_LARGE ? 2 : NG_TRY; }
 __host__ __device__ constexpr int num_threads(int tt) { return (WARP_DEQ0 + 4 * deq_groups(tt)) * 32; }
 
 // Two rings.  What TMA brings -- the dy tile (B), the packed codes and the metadata words -- waits in a ring as
@@ -428,8 +442,13 @@ __host__ __device__ constexpr int stage_bytes(int fmt, int bits, int tt) {
 __host__ __device__ constexpr int smem_need(int fmt, int bits, int tt, int st, int as) {
   return st * stage_bytes(fmt, bits, tt) + as * A_BYTES + (2 * st + as + 5) * 8 + 16 + 1024;
 }
+#ifndef AST_TRY
+#define AST_TRY 8
+#endif
 __host__ __device__ constexpr int a_stages(int fmt, int bits, int tt) {
-  return smem_need(fmt, bits, tt, 4, 4) <= gemm::SMEM_LIMIT ? 4 : 3;
+  int as = tt == TT_LARGE ? 4 : AST_TRY;
+  while (smem_need(fmt, bits, tt, as < 4 ? 4 : as, as) > gemm::SMEM_LIMIT) --as;  // at least as many stages
+  return as;
 }
 __host__ __device__ constexpr int stages(int fmt, int bits, int tt) {
   int st = 16;
@@ -504,53 +523,103 @@ struct Params {
   __nv_bfloat16 *dx;
 };
 
-// Eight weights of a run -> four words of fp16 pairs (k, k + 4), k = 0..3, scaled: the order in which one
-// bit operation takes pairs out of a code word.  The k order inside 8 is free here (it is the order of
-// the tile's output rows), see out_k.
+// The order in which a row's weights leave the code words in pairs, which is that of the tile's output rows
+// (any order would do): 0, 4, 1, 5, 2, 6, 3, 7 of 8 weights; bytes 0, 2, 1, 3 of 4; 2-bit fields 0, 8, 1, 9, .. of 16.
+// k of row r of the tile:
 template <int FMT, int BITS>
-QL_DEVI void codes8_to_pairs(const uint32_t (&c)[3], uint32_t (&pr)[4]) {  // -> 1024 + q (+ 32 for int6)
-  if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) pr[e] = ((c[0] >> (4 * e)) & 0x000F000Fu) | 0x64006400u;
-  } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {
-    const uint32_t t0 = __byte_perm(c[0], c[1], 0x5140), t1 = __byte_perm(c[0], c[1], 0x7362);
-    pr[0] = __byte_perm(t0, 0x64646464u, 0x4140);
-    pr[1] = __byte_perm(t0, 0x64646464u, 0x4342);
-    pr[2] = __byte_perm(t1, 0x64646464u, 0x4140);
-    pr[3] = __byte_perm(t1, 0x64646464u, 0x4342);
-  } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: 16 bits of codes
-    const uint32_t u = __byte_perm(c[0], 0u, 0x4140);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) pr[e] = ((u >> (2 * e)) & 0x00030003u) | 0x64006400u;
-  } else if constexpr (FMT == FMT_INT6P) {  // nibbles, then 16 bits of high fields
-    const uint32_t u = __byte_perm(c[1], 0u, 0x4140);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t f = ((c[0] >> (4 * e)) & 0x000F000Fu) | (((u >> (2 * e)) & 0x00030003u) << 4);
-      pr[e] = (f ^ 0x00200020u) | 0x64006400u;
-    }
-  } else {  // int6: two 24-bit units
-    const uint32_t u0 = c[0] & 0xFFFFFFu, u1 = c[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t f = ((u0 >> (6 * e)) & 0x3Fu) | (((u1 >> (6 * e)) & 0x3Fu) << 16);
-      pr[e] = (f ^ 0x00200020u) | 0x64006400u;
-    }
-  }
+QL_DEVI int out_k(int r) {
+  if (FMT == FMT_AFFINE && BITS == 8) return (r & ~3) | ((r & 3) >> 1) | ((r & 1) << 1);
+  if (FMT == FMT_AFFINE && BITS == 2) return (r & ~15) | ((r & 15) >> 1) | ((r & 1) << 3);
+  return (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);
 }
 
-// (1024 + q) pairs -> scaled weights: int4 q S - Z S and affine q s + b, one rounding each; int6 q S
-template <int FMT>
-QL_DEVI uint32_t scale_pair(uint32_t pr, __half2 s, __half2 o) {
-  const __half2 v = *reinterpret_cast<const __half2 *>(&pr);
-  __half2 w;
-  if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) w = __hmul2(__hsub2(v, __float2half2_rn(1056.f)), s);
-  else w = __hfma2(__hsub2(v, __float2half2_rn(1024.f)), s, o);
+QL_DEVI uint32_t fma_h2(uint32_t q, __half2 s, __half2 o) {
+  const __half2 w = __hfma2(*reinterpret_cast<const __half2 *>(&q), s, o);
   return *reinterpret_cast<const uint32_t *>(&w);
 }
 
-// k of row r of the tile: within 8 rows the pairs' order 0,4,1,5,2,6,3,7
-QL_DEVI int out_k(int r) { return (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2); }
+// The 32 weights of a run of row n: its codes in a stage's code tile at `stg` (the row's swizzle: chunk ^ bits
+// of n), its metadata word mw -> 16 words of scaled fp16 pairs in the order above.  A mask leaves codes in bits
+// 0-3 or 4-7 of the halves (2-bit: 0-1 to 6-7): s[i] is the scale for codes 4 i (2 i) bits up.
+template <int FMT, int BITS>
+QL_DEVI void decode_run(const uint8_t *stg, int n, int run, uint32_t mw, uint32_t (&o)[16]) {
+  const __half2 mv = *reinterpret_cast<const __half2 *>(&mw);
+  constexpr int PROW = code_row(FMT, BITS);
+  if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {  // 64-byte swizzle
+    const uint4 v = *reinterpret_cast<const uint4 *>(stg + n * 64 + ((run ^ ((n >> 1) & 3)) << 4));
+    const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+    const __half2 s0 = __low2half2(mv), s1 = __hmul2(s0, __float2half2_rn(0.0625f));
+    const __half2 z = FMT == FMT_INT4 ? __hneg2(__high2half2(mv)) : __high2half2(mv);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t c8 = c[q] >> 8;
+      o[4 * q] = fma_h2(c[q] & 0x000F000Fu, s0, z);
+      o[4 * q + 1] = fma_h2(c[q] & 0x00F000F0u, s1, z);
+      o[4 * q + 2] = fma_h2(c8 & 0x000F000Fu, s0, z);
+      o[4 * q + 3] = fma_h2(c8 & 0x00F000F0u, s1, z);
+    }
+  } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {  // 128-byte swizzle
+    const uint4 v = *reinterpret_cast<const uint4 *>(stg + n * 128 + (((2 * run) ^ (n & 7)) << 4));
+    const uint4 u = *reinterpret_cast<const uint4 *>(stg + n * 128 + (((2 * run + 1) ^ (n & 7)) << 4));
+    const uint32_t c[8] = {v.x, v.y, v.z, v.w, u.x, u.y, u.z, u.w};
+    const __half2 s = __low2half2(mv), z = __high2half2(mv);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      o[2 * q] = fma_h2(c[q] & 0x00FF00FFu, s, z);
+      o[2 * q + 1] = fma_h2(__byte_perm(c[q], 0u, 0x4341), s, z);
+    }
+  } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: 8 bytes, no swizzle
+    const uint2 v = *reinterpret_cast<const uint2 *>(stg + n * PROW + 8 * run);
+    const uint32_t c[2] = {v.x, v.y};
+    __half2 s[4];
+    s[0] = __low2half2(mv);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s[i] = __hmul2(s[i - 1], __float2half2_rn(0.25f));
+    const __half2 z = __high2half2(mv);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t c8 = c[q] >> 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[8 * q + i] = fma_h2(c[q] & (0x00030003u << (2 * i)), s[i], z);
+        o[8 * q + 4 + i] = fma_h2(c8 & (0x00030003u << (2 * i)), s[i], z);
+      }
+    }
+  } else {  // int6: fields f = q & 63, q = (f ^ 32) - 32; the scale changes after 16 weights
+    const __half2 m32 = __float2half2_rn(-32.f / SUB);
+    const __half2 s[2] = {__low2half2(mv), __high2half2(mv)};
+    const __half2 z[2] = {__hmul2(s[0], m32), __hmul2(s[1], m32)};
+    if constexpr (FMT == FMT_INT6P) {  // low plane with 64-byte swizzle, then the high plane, 32 bytes a row
+      const uint4 v = *reinterpret_cast<const uint4 *>(stg + n * 64 + ((run ^ ((n >> 1) & 3)) << 4));
+      const uint2 w = *reinterpret_cast<const uint2 *>(stg + BN * 64 + n * 32 + 8 * run);
+      const uint32_t c[4] = {v.x, v.y, v.z, v.w}, hi[4] = {w.x, w.x >> 16, w.y, w.y >> 16};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t h = __byte_perm(hi[q], 0u, 0x4140);  // high fields of weights 0-3 and 4-7
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = (c[q] >> (4 * e)) & 0x000F000Fu;
+          const uint32_t up = (e < 2 ? h << (4 - 2 * e) : h >> (2 * e - 4)) & 0x00300030u;
+          o[4 * q + e] = fma_h2((lo | up) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
+        }
+      }
+    } else {  // 24 bytes: eight 24-bit units of 4 weights; words of the low (a) and high (b) two of 2 x 4 weights
+      const uint2 *src = reinterpret_cast<const uint2 *>(stg + n * PROW + 24 * run);
+      const uint2 x = src[0], y = src[1], w = src[2];
+      const uint32_t u[8] = {x.x, __funnelshift_r(x.x, x.y, 24), __funnelshift_r(x.y, y.x, 16), y.x >> 8,
+                             y.y, __funnelshift_r(y.y, w.x, 24), __funnelshift_r(w.x, w.y, 16), w.y >> 8};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a = __byte_perm(u[2 * q], u[2 * q + 1], 0x5410);
+        const uint32_t b = __byte_perm(u[2 * q] >> 12, u[2 * q + 1] >> 12, 0x5410);
+        o[4 * q] = fma_h2((a & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
+        o[4 * q + 1] = fma_h2(((a >> 6) & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
+        o[4 * q + 2] = fma_h2((b & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
+        o[4 * q + 3] = fma_h2(((b >> 6) & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
+      }
+    }
+  }
+}
 
 // Shared-memory matrix descriptor of an M-major operand in the 128-byte-swizzled layout: for each
 // contraction index a row of 128 bytes (64 fp16 along M), 16-byte chunks XOR-ed with (row % 8); the next 8
@@ -566,18 +635,37 @@ QL_DEVI uint64_t umma_desc_m_sw128(uint32_t smem_addr) {
 }
 constexpr uint32_t IDESC_A_M_MAJOR = 1u << 15;
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16
-QL_DEVI void umma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The MMAs of a stage, D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16, four slices of 16 rows n (2048
+// bytes of A, 32 bytes along B's rows: 128 and 2 descriptor units), and the barrier that receives an arrival
+// when they are done.  The whole warp comes here and one elected lane issues, by predicate: under a branch
+// that one lane takes, the descriptors are not warp-uniform values and every MMA waits for its operands to
+// move into uniform registers (measured: 400 cycles a stage, the kernel's pace).
+QL_DEVI void umma_stage(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 a, %1, 128;\n\tadd.u64 b, %2, 2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 256;\n\tadd.u64 b, %2, 4;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 384;\n\tadd.u64 b, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(bar)
+      : "memory");
+}
+// umma_commit by the lane that umma_stage elects
+QL_DEVI void umma_commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 
-// Warp roles as in the forward GEMM: 0 TMA producer, 1 tensor memory and MMA issue, 4-7 epilogue (one k a
-// lane), 8.. dequantisers in groups of four warps that take the stages in turn.  A thread of a group
+// Warp roles: 0, 2 and 3 TMA producers, 1 tensor memory and MMA issue, 4-7 epilogue (one k a lane), 8..
+// dequantisers in groups of four warps that take the stages in turn.  A thread of a group
 // decodes 64 weights of one row n: 128 bytes of A.
 template <int FMT, int BITS, int TT>
 __global__ void __launch_bounds__(num_threads(TT), 1)
@@ -589,7 +677,7 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
   constexpr int OFF_P = b_bytes(TT), OFF_M = OFF_P + p_bytes(FMT, BITS);  // in a stage, after the dy tile
   constexpr int STAGE = stage_bytes(FMT, BITS, TT), OFF_A = STAGES * STAGE;
   static_assert(STAGE % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
-  static_assert(STAGES >= AST, "an A slot's previous MMAs are found by their stage");
+  static_assert(STAGES >= AST && NG <= STAGES && NPROD <= STAGES, "an A slot's previous MMAs are found by their stage");
   constexpr uint32_t TMEM_COLS = 2 * TT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -643,41 +731,47 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
   pdl_launch_dependents();
   pdl_wait();  // the preparation passes' results
 
-  if (warp == WARP_TMA) {
+  // Warps 0, 2 and 3 bring the stages in turn: a thread needs 120 ns and more to wait for a stage and start its
+  // copies (measured: 64 x 64-byte boxes, 123 ns a stage from one thread, 41 ns from four), whatever their size.
+  if (warp != WARP_MMA && warp < WARP_EPI0) {
     if (lane == 0) {
       tma_prefetch_desc(&map_dy);
       tma_prefetch_desc(&map_codes);
       tma_prefetch_desc(&map_meta);
       if constexpr (FMT == FMT_INT6P) tma_prefetch_desc(&map_codes_hi);
-      int s = 0;
+      const int first = warp == WARP_TMA ? 0 : warp - 1;
+      int s = first;
       uint32_t ph = 0;
-      int64_t it = 0;
+      int64_t it = first;
       bool ok = true;
       const bool start = !copies_withheld();
+      int st = first;  // this producer's next stage, counted from the piece's first
       Piece pc;
       for (int i = 0; ok && start && get_piece(p.deal, cta, i, pc); ++i) {
-        const int64_t k_tile = pc.tile / p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
-        for (int st = pc.step0; st < pc.step1; ++st, ++it) {
+        const int64_t k_tile = pc.tile / p.deal.m_tiles;
+        const int32_t m0 = (int32_t)((pc.tile - k_tile * p.deal.m_tiles) * tokens);
+        const int32_t x = FMT == FMT_INT6P ? (int32_t)(192 * (k_tile >> 1) + 64 * (k_tile & 1)) : (int32_t)(k_tile * PROW);
+        const int32_t xh = (int32_t)(192 * (k_tile >> 1) + 128 + 32 * (k_tile & 1));
+        const int32_t run0 = (int32_t)(k_tile * BKT / gran(FMT, p.G));
+        const int steps = pc.step1 - pc.step0;
+        for (; st < steps; st += NPROD, it += NPROD) {
           if (!mbar_wait_bounded(bar_empty(s), ph ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
           const uint32_t b = bar_tma_full(s), dst = sbase + s * STAGE;
+          const int32_t n = (pc.step0 + st) * BN;
           mbar_arrive_expect_tx(b, stage_tx);
-          tma_load_2d(dst, &map_dy, b, st * BN, (int32_t)(m_tile * tokens));
-          if constexpr (FMT == FMT_INT6P) {  // half a super-block: 64 low-plane bytes, 32 high-plane bytes
-            const int32_t sb = (int32_t)(192 * (k_tile >> 1)), h = (int32_t)(k_tile & 1);
-            tma_load_2d(dst + OFF_P, &map_codes, b, sb + 64 * h, st * BN);
-            tma_load_2d(dst + OFF_P + BN * 64, &map_codes_hi, b, sb + 128 + 32 * h, st * BN);
-          } else {
-            tma_load_2d(dst + OFF_P, &map_codes, b, (int32_t)(k_tile * PROW), st * BN);
-          }
-          tma_load_2d(dst + OFF_M, &map_meta, b, st * BN, (int32_t)(k_tile * BKT / gran(FMT, p.G)));
-          step_ring(s, ph, 1, STAGES);
+          tma_load_2d(dst + OFF_P, &map_codes, b, x, n);
+          if constexpr (FMT == FMT_INT6P) tma_load_2d(dst + OFF_P + BN * 64, &map_codes_hi, b, xh, n);
+          tma_load_2d(dst + OFF_M, &map_meta, b, n, run0);
+          tma_load_2d(dst, &map_dy, b, n, m0);
+          step_ring(s, ph, NPROD, STAGES);
         }
+        st -= steps;
       }
       if (!ok) {  // let copies already issued land before the CTA can exit
-        for (int64_t j = it - 1; j >= 0 && j >= it - STAGES; --j) {
+        for (int64_t j = it - NPROD; j >= 0 && j >= it - STAGES; j -= NPROD) {
           const long long t0 = clock64();
           while (!mbar_try_wait(bar_tma_full((int)(j % STAGES)), (uint32_t)((j / STAGES) & 1)) &&
                  clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
@@ -686,41 +780,37 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
       }
     }
   } else if (warp == WARP_MMA) {
-    if (lane == 0) {
-      const uint32_t idesc = umma_idesc_f16_f32(BKT, tokens) | IDESC_A_M_MAJOR;
-      int s = 0, as = 0, n = 0;
-      uint32_t ph = 0, aph = 0;
-      bool ok = true, issued = false;
-      Piece pc;
-      for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i, ++n) {
-        const int a = n & 1;
-        if (!mbar_wait_bounded(bar_acc_empty(a), ((n >> 1) & 1) ^ 1, abort_flag)) break;
+    const uint32_t idesc = umma_idesc_f16_f32(BKT, tokens) | IDESC_A_M_MAJOR;
+    const uint64_t ad0 = umma_desc_m_sw128(sbase + OFF_A), bd0 = umma_desc_k_sw128(sbase);
+    int s = 0, as = 0;
+    uint32_t ph = 0, aph = 0;
+    bool ok = true, issued = false;
+    Piece pc;
+    for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i) {
+      const int a = i & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_acc_empty(a), ((i >> 1) & 1) ^ 1, abort_flag))) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(a * TT);
+      for (int st = pc.step0; st < pc.step1; ++st) {
+        // the dequantisers waited for this stage's copies, so the dy tile has landed too
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_a_full(as), aph, abort_flag))) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(a * TT);
-        for (int st = pc.step0; st < pc.step1; ++st) {
-          // the dequantisers waited for this stage's copies, so the dy tile has landed too
-          if (!mbar_wait_bounded(bar_a_full(as), aph, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = umma_desc_m_sw128(sbase + OFF_A + as * A_BYTES), bd = umma_desc_k_sw128(sbase + s * STAGE);
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)  // 16 rows n: 2048 bytes of A, 32 bytes along B's rows
-            umma_f16_ss(d_tmem, ad + (uint64_t)(kk * (2048 >> 4)), bd + (uint64_t)(kk * (32 >> 4)), idesc,
-                        st != pc.step0 || kk != 0);
-          umma_commit(bar_empty(s));  // the stage, and the A slot
-          issued = true;
-          step_ring(s, ph, 1, STAGES);
-          step_ring(as, aph, 1, AST);
-        }
-        if (ok) umma_commit(bar_acc_full(a));
+        // done: the stage and the A slot are free
+        umma_stage(d_tmem, ad0 + (uint64_t)(as * (A_BYTES >> 4)), bd0 + (uint64_t)(s * (STAGE >> 4)), idesc,
+                   st != pc.step0, bar_empty(s));
+        issued = true;
+        step_ring(s, ph, 1, STAGES);
+        step_ring(as, aph, 1, AST);
       }
-      if (issued) {  // all MMAs retired before teardown
-        umma_commit(bar_final);
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar_final, 0) && clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
-        }
+      if (ok) umma_commit_elected(bar_acc_full(a));
+    }
+    if (issued) {  // all MMAs retired before teardown
+      umma_commit_elected(bar_final);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bar_final, 0) && clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
       }
     }
   } else if (warp >= WARP_EPI0 && warp < WARP_EPI0 + 4) {
@@ -729,10 +819,10 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
     for (int i = 0; get_piece(p.deal, cta, i, pc); ++i) {
       const int a = i & 1;
       const int64_t k_tile = pc.tile / p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
-      const int64_t k = k_tile * BKT + out_k(32 * e + lane);
+      const int64_t k = k_tile * BKT + out_k<FMT, BITS>(32 * e + lane);
       const int64_t m0 = m_tile * tokens;
       const int valid = (int)(p.M - m0 < tokens ? p.M - m0 : tokens);
-      if (!mbar_wait_bounded(bar_acc_full(a), (i >> 1) & 1, abort_flag)) break;
+      if (!mbar_wait_suspend(bar_acc_full(a), (i >> 1) & 1, abort_flag)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < tokens / 16; ++c) {
@@ -766,84 +856,47 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
     const int wd = warp - WARP_DEQ0, g = wd >> 2;
     const int tau = 32 * (wd & 3) + lane;
     const int n = tau & 63, half = tau >> 6;  // row of the stage, 64-k half of the tile
-    int s = 0, as = 0, turn = 0;
-    uint32_t ph = 0;
-    int es = STAGES - AST;  // stage of the step AST before this one, whose MMAs read this step's A slot
-    uint32_t eph = 1;       // and its phase (the first AST steps find their slots free: the phase before the first)
-    bool ok = true;
+    // the half's two runs: their words in a stage's metadata
+    const int run_shift = FMT != FMT_AFFINE || p.G == 32 ? 0 : p.G == 64 ? 1 : 2;
+    const int meta0 = OFF_M + 4 * (((2 * half) >> run_shift) * BN + n), meta1 = OFF_M + 4 * (((2 * half + 1) >> run_shift) * BN + n);
+    uint8_t *const arow0 = smem + OFF_A + half * (BN * 128) + n * 128;
+    int64_t total = 0;  // this CTA's stages
     Piece pc;
-    for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i) {
-      for (int st = pc.step0; st < pc.step1; ++st) {
-        if (turn == g) {
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tma_full(s), ph, abort_flag))) {
-            ok = false;
-            break;
-          }
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty(es), eph, abort_flag))) {
-            ok = false;
-            break;
-          }
-          const uint8_t *stg = smem + s * STAGE;
-          const uint32_t *meta = reinterpret_cast<const uint32_t *>(stg + OFF_M) + n;
-          uint8_t *arow = smem + OFF_A + as * A_BYTES + half * (BN * 128) + n * 128;
+    for (int i = 0; get_piece(p.deal, cta, i, pc); ++i) total += pc.step1 - pc.step0;
+    int s = g, as = g % AST;
+    uint32_t ph = 0;
+    // the stage of the step AST before, whose MMAs read this step's A slot, and its phase (the first AST steps
+    // find their slots free: the phase before the first)
+    int es = g + STAGES - AST;
+    uint32_t eph = 1;
+    if (es >= STAGES) {
+      es -= STAGES;
+      eph = 0;
+    }
+    for (int64_t it = g; it < total; it += NG) {
+      // In this order: copies may land out of turn and other groups be behind, and a wait by parity is only
+      // right while its barrier is at that phase or just past it.  The A slot's wait says that the MMAs of step
+      // it - AST, and so of every step before, are done; the previous use of stage s (it - STAGES) is one of them.
+      if (!__all_sync(0xffffffffu, mbar_wait_suspend(bar_empty(es), eph, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_suspend(bar_tma_full(s), ph, abort_flag))) break;
+      const uint8_t *stg = smem + s * STAGE;
+      uint8_t *arow = arow0 + as * A_BYTES;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // the half's 32-weight runs
-            const int run = 2 * half + h;
-            const uint32_t mw = meta[(FMT == FMT_AFFINE ? 32 * run / p.G : run) * BN];
-            const __half2 mv = *reinterpret_cast<const __half2 *>(&mw);
-            // 32 codes: words of 8 codes each (8-bit: two words each)
-            uint32_t cw[4][3];
-            const uint8_t *prow = stg + OFF_P + n * PROW;
-            if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {  // 64-byte swizzle
-              const uint4 v = *reinterpret_cast<const uint4 *>(prow + ((run ^ ((n >> 1) & 3)) << 4));
-              cw[0][0] = v.x; cw[1][0] = v.y; cw[2][0] = v.z; cw[3][0] = v.w;
-            } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {  // 128-byte swizzle
-              const uint4 v = *reinterpret_cast<const uint4 *>(prow + (((2 * run) ^ (n & 7)) << 4));
-              const uint4 u = *reinterpret_cast<const uint4 *>(prow + (((2 * run + 1) ^ (n & 7)) << 4));
-              cw[0][0] = v.x; cw[0][1] = v.y; cw[1][0] = v.z; cw[1][1] = v.w;
-              cw[2][0] = u.x; cw[2][1] = u.y; cw[3][0] = u.z; cw[3][1] = u.w;
-            } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: 8 bytes, no swizzle
-              const uint2 v = *reinterpret_cast<const uint2 *>(prow + 8 * run);
-              cw[0][0] = v.x; cw[1][0] = v.x >> 16; cw[2][0] = v.y; cw[3][0] = v.y >> 16;
-            } else if constexpr (FMT == FMT_INT6P) {  // low plane 64-byte swizzle, high plane 32 bytes a row
-              const uint4 v = *reinterpret_cast<const uint4 *>(stg + OFF_P + n * 64 + ((run ^ ((n >> 1) & 3)) << 4));
-              const uint2 u = *reinterpret_cast<const uint2 *>(stg + OFF_P + BN * 64 + n * 32 + 8 * run);
-              cw[0][0] = v.x; cw[1][0] = v.y; cw[2][0] = v.z; cw[3][0] = v.w;
-              cw[0][1] = u.x; cw[1][1] = u.x >> 16; cw[2][1] = u.y; cw[3][1] = u.y >> 16;
-            } else {  // int6: 24 bytes = eight 24-bit units, two a word group
-              const uint2 *src = reinterpret_cast<const uint2 *>(prow + 24 * run);
-              const uint2 a = src[0], b = src[1], c = src[2];
-              cw[0][0] = a.x; cw[0][1] = __funnelshift_r(a.x, a.y, 24);
-              cw[1][0] = __funnelshift_r(a.y, b.x, 16); cw[1][1] = b.x >> 8;
-              cw[2][0] = b.y; cw[2][1] = __funnelshift_r(b.y, c.x, 24);
-              cw[3][0] = __funnelshift_r(c.x, c.y, 16); cw[3][1] = c.y >> 8;
-            }
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[16];
+        decode_run<FMT, BITS>(stg + OFF_P, n, 2 * half + h, *reinterpret_cast<const uint32_t *>(stg + (h ? meta1 : meta0)), o);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t pr[4];
-              codes8_to_pairs<FMT, BITS>(cw[q], pr);
-              __half2 sv, ov;
-              if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {  // 16-weight groups
-                sv = q < 2 ? __low2half2(mv) : __high2half2(mv);
-                ov = sv;
-              } else {
-                sv = __low2half2(mv);
-                ov = FMT == FMT_INT4 ? __hneg2(__high2half2(mv)) : __high2half2(mv);
-              }
-              const uint4 o = make_uint4(scale_pair<FMT>(pr[0], sv, ov), scale_pair<FMT>(pr[1], sv, ov),
-                                         scale_pair<FMT>(pr[2], sv, ov), scale_pair<FMT>(pr[3], sv, ov));
-              *reinterpret_cast<uint4 *>(arow + (((4 * h + q) ^ (n & 7)) << 4)) = o;
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_a_full(as));
-        }
-        if (++turn == NG) turn = 0;
-        step_ring(s, ph, 1, STAGES);
-        step_ring(es, eph, 1, STAGES);
-        if (++as == AST) as = 0;
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4 *>(arow + (((4 * h + q) ^ (n & 7)) << 4)) =
+              make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_a_full(as));
+      step_ring(s, ph, NG, STAGES);
+      step_ring(es, eph, NG, STAGES);
+      as += NG;
+      if (as >= AST) as %= AST;
     }
   }
 
@@ -855,10 +908,11 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
 }
 
 // ---- pass 5: the sums of the split tiles' parts -------------------------------------------------------
-// A CTA takes 16 tokens of a tile, a thread 8 rows (eight consecutive k, see out_k) of one of them; the
+// A CTA takes 32 tokens of a tile, a thread 16 rows (sixteen consecutive k, see out_k) of one of them; the
 // parts are added in the order of the shares.
-constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 8);
+constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 16);
 
+template <int FMT, int BITS>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
   __shared__ int range[3];  // first share, its slot, end of the shares
   const Deal &d = p.deal;
@@ -878,25 +932,29 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
   pdl_wait();  // the parts
   __syncthreads();
   const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
-  const int t = blockIdx.y * JOIN_TOKENS + threadIdx.x / (BKT / 8), r = 8 * (threadIdx.x % (BKT / 8));
+  const int t = blockIdx.y * JOIN_TOKENS + threadIdx.x / (BKT / 16), r = 16 * (threadIdx.x % (BKT / 16));
   const int64_t m = m_tile * d.tokens + t, k = k_tile * BKT + r;
   if (t >= d.tokens || m >= p.M || k >= p.K) return;
   const int end = range[2];
   int slot = range[1];
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float v[16] = {};
   for (int c = range[0]; c < end; ++c) {
     const float4 *src = reinterpret_cast<const float4 *>(p.partial + ((int64_t)slot * d.tokens + t) * BKT + r);
-    const float4 x = __ldcg(src), y = __ldcg(src + 1);
-    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = __ldcg(src + j);
+      v[4 * j] += x.x; v[4 * j + 1] += x.y; v[4 * j + 2] += x.z; v[4 * j + 3] += x.w;
+    }
     slot = 2 * (c + 1);
   }
   const int e = __ldg(p.dexp + m);
+  float o[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = mul_pow2(v[i], e);
-  // rows hold k 0,4,1,5,2,6,3,7
-  *reinterpret_cast<uint4 *>(p.dx + m * p.K + k) =
-      make_uint4(pack_bf16x2(v[0], v[2]), pack_bf16x2(v[4], v[6]), pack_bf16x2(v[1], v[3]), pack_bf16x2(v[5], v[7]));
+  for (int i = 0; i < 16; ++i) o[out_k<FMT, BITS>(i)] = mul_pow2(v[i], e);
+  uint4 *dst = reinterpret_cast<uint4 *>(p.dx + m * p.K + k);
+  dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+  dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]),
+                      pack_bf16x2(o[14], o[15]));
 }
 
 }  // namespace dx

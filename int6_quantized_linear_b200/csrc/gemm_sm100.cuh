@@ -926,7 +926,10 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
         }
       }
       // the codes have landed, and the MMAs that last read this A stage have completed (they
-      // released the stage before TMA refilled it)
+      // released the stage before TMA refilled it).  Their wait comes first: this group did not see the stage's
+      // previous use (another group's), copies may land out of turn, and the wait for the codes is only right
+      // once that use's phase is over.
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty(s), ph ^ 1u, abort_flag))) break;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tma_full(s), ph, abort_flag))) break;
       tc_fence_after();
       const uint8_t *prow = smem + off_p(FMT, BITS, TT, s) + br * PROW;

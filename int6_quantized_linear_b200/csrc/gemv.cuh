@@ -375,30 +375,6 @@ QL_DEVI uint32_t lds32(uint32_t a) {
   return v;
 }
 
-// Wait for an mbarrier phase, letting the hardware suspend the thread (up to a hint, in ns) instead
-// of spinning; bounded like mbar_wait_bounded.
-QL_DEVI bool mbar_wait_suspend(uint32_t bar, uint32_t parity, volatile int *abort) {
-  const long long t0 = clock64();
-  const uint32_t hint = 1000000u;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(hint)
-        : "memory");
-    if (ok) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > QL_WAIT_LIMIT_CYCLES) {
-      atomicOr(&g_ql_status, QL_DEV_TIMEOUT);
-      *abort = 1;
-      return false;
-    }
-  }
-}
-
 // ACC = C + A * B (first MMA of a chain) and ACC += A * B, with A = u8 codes x 16 and B = the
 // high (signed) or low (unsigned) x bytes
 #define QL_IMMA0(TB, ACC, C, A0, A1, A2, A3, B0, B1)                                                  \
