@@ -189,23 +189,37 @@ QL_DEVI void tmem_dealloc(uint32_t taddr, uint32_t ncols) {  // whole warp
 QL_DEVI void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 QL_DEVI void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16: A is M = 128 TMEM lanes (one row each) with
-// its K values packed two 16-bit halves per 32-bit column, the lower k in the low half.
-QL_DEVI void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                             uint32_t accumulate) {
+// The MMAs of one 64-deep stage, D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16: A is M = 128 TMEM lanes
+// (one row each) with its K values packed two 16-bit halves per 32-bit column, the lower k in the low half;
+// four slices of 16 (8 columns of A, 32 bytes = 2 descriptor units of B).  `bar` receives one arrival when they,
+// and everything that lane issued before, are done.  A whole warp comes here and one elected lane issues, by
+// predicate: under a branch that a single lane takes, the operands are not warp-uniform values, and every MMA
+// waits until they have moved into uniform registers (measured: about 400 cycles a stage).
+QL_DEVI void umma_stage_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                               uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 4;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(bar)
       : "memory");
 }
 
-// Arrive (once) on an mbarrier when all tcgen05 operations issued so far by
-// this thread have completed.
-QL_DEVI void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+// Arrive (once) on an mbarrier when all tcgen05 operations that the elected lane issued so far have
+// completed.
+QL_DEVI void umma_commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // Each thread of the warp reads 32 consecutive 32-bit columns of its TMEM lane.

@@ -637,9 +637,7 @@ constexpr uint32_t IDESC_A_M_MAJOR = 1u << 15;
 
 // The MMAs of a stage, D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16, four slices of 16 rows n (2048
 // bytes of A, 32 bytes along B's rows: 128 and 2 descriptor units), and the barrier that receives an arrival
-// when they are done.  The whole warp comes here and one elected lane issues, by predicate: under a branch
-// that one lane takes, the descriptors are not warp-uniform values and every MMA waits for its operands to
-// move into uniform registers (measured: 400 cycles a stage, the kernel's pace).
+// when they are done; issued like umma_stage_tmem_a.
 QL_DEVI void umma_stage(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t"
@@ -656,14 +654,6 @@ QL_DEVI void umma_stage(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(bar)
       : "memory");
 }
-// umma_commit by the lane that umma_stage elects
-QL_DEVI void umma_commit_elected(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
 // Warp roles: 0, 2 and 3 TMA producers, 1 tensor memory and MMA issue, 4-7 epilogue (one k a lane), 8..
 // dequantisers in groups of four warps that take the stages in turn.  A thread of a group
 // decodes 64 weights of one row n: 128 bytes of A.

@@ -636,63 +636,57 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       }
     }
   } else if (warp == WARP_MMA) {
-    if (lane == 0) {
-      // D[weight row][token] += W tile (A, M = 128) x x tile (B, N = TT).  This one thread sets the
-      // kernel's pace, so its loop is unrolled over the ring's slots: slot j's x-tile descriptor
-      // and A columns are compile-time offsets from slot 0's, and the phase flips once a ring cycle.
-      constexpr uint32_t idesc = umma_idesc_f16_f32(BN, TT);
-      constexpr uint32_t XDESC_STEP = (uint32_t)(a_bytes(TT) >> 4);  // descriptor address units
-      const uint64_t xdesc0 = umma_desc_k_sw128(sbase + off_a(TT, 0));
-      const uint32_t a_tmem0 = tmem_base + A_COL0;
-      int64_t tcount = 0, tile = blockIdx.x;
-      int kb = 0;  // stage within the current tile
-      uint32_t ph = 0, d_tmem = tmem_base;
-      bool ok = true, issued = false;
-      // start a tile: its accumulator must have been drained (bounded wait)
-      auto begin_tile = [&]() {
-        const int a = (int)(tcount % NACC);
-        const uint32_t ause = (uint32_t)(tcount / NACC);
-        if (!mbar_wait_bounded(bar_acc_empty(a), (ause & 1) ^ 1, abort_flag)) return false;
+    // D[weight row][token] += W tile (A, M = 128) x x tile (B, N = TT).  This warp sets the kernel's pace, so
+    // its loop is unrolled over the ring's slots (slot j's x-tile descriptor and A columns are compile-time
+    // offsets from slot 0's, and the phase flips once a ring cycle), and all of it runs the loop, one elected
+    // lane issuing (see umma_stage_tmem_a).
+    constexpr uint32_t idesc = umma_idesc_f16_f32(BN, TT);
+    constexpr uint32_t XDESC_STEP = (uint32_t)(a_bytes(TT) >> 4);  // descriptor address units
+    const uint64_t xdesc0 = umma_desc_k_sw128(sbase + off_a(TT, 0));
+    const uint32_t a_tmem0 = tmem_base + A_COL0;
+    int64_t tcount = 0, tile = blockIdx.x;
+    int kb = 0;  // stage within the current tile
+    uint32_t ph = 0, d_tmem = tmem_base;
+    bool ok = true, issued = false;
+    // start a tile: its accumulator must have been drained (bounded wait)
+    auto begin_tile = [&]() {
+      const int a = (int)(tcount % NACC);
+      const uint32_t ause = (uint32_t)(tcount / NACC);
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_acc_empty(a), (ause & 1) ^ 1, abort_flag))) return false;
+      tc_fence_after();
+      d_tmem = tmem_base + (uint32_t)(a * TT);  // accumulator a: columns a * TT ..
+      return true;
+    };
+    if (tile < num_tiles) ok = begin_tile();
+    while (ok && tile < num_tiles) {
+#pragma unroll
+      for (int j = 0; j < STAGES; ++j) {
+        if (!ok || tile >= num_tiles) break;
+        // b_full alone: its arrivals come from dequantisers that waited for this stage's tma_full,
+        // so the x tile has landed before the MMAs read it (and a copy that never lands ends their
+        // wait, and so this one, by the abort flag)
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_b_full(j), ph, abort_flag))) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        d_tmem = tmem_base + (uint32_t)(a * TT);  // accumulator a: columns a * TT ..
-        return true;
-      };
-      if (tile < num_tiles) ok = begin_tile();
-      while (ok && tile < num_tiles) {
-#pragma unroll
-        for (int j = 0; j < STAGES; ++j) {
-          if (!ok || tile >= num_tiles) break;
-          // b_full alone: its arrivals come from dequantisers that waited for this stage's tma_full,
-          // so the x tile has landed before the MMAs read it (and a copy that never lands ends their
-          // wait, and so this one, by the abort flag)
-          if (!mbar_wait_bounded(bar_b_full(j), ph, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t xdesc = xdesc0 + (uint64_t)(j * XDESC_STEP);
-          const uint32_t a_tmem = a_tmem0 + (uint32_t)(j * TA_ACOLS);  // lanes 0..127
-          // 16 fp16 = 8 TMEM columns; 32 bytes = 2 descriptor units
-          umma_f16_tmem_a(d_tmem, a_tmem, xdesc, idesc, kb != 0);
-#pragma unroll
-          for (int kk = 1; kk < BK / 16; ++kk) umma_f16_tmem_a(d_tmem, a_tmem + 8 * kk, xdesc + 2 * kk, idesc, 1u);
-          umma_commit(bar_empty(j));
-          issued = true;
-          if (++kb == num_kb) {  // the tile's last stage
-            kb = 0;
-            umma_commit(bar_acc_full((int)(tcount % NACC)));
-            tile += gridDim.x;
-            ++tcount;
-            if (tile < num_tiles) ok = begin_tile();
-          }
+        umma_stage_tmem_a(d_tmem, a_tmem0 + (uint32_t)(j * TA_ACOLS), xdesc0 + (uint64_t)(j * XDESC_STEP), idesc,
+                          kb != 0, bar_empty(j));
+        issued = true;
+        if (++kb == num_kb) {  // the tile's last stage
+          kb = 0;
+          umma_commit_elected(bar_acc_full((int)(tcount % NACC)));
+          tile += gridDim.x;
+          ++tcount;
+          if (tile < num_tiles) ok = begin_tile();
         }
-        ph ^= 1u;
       }
-      if (issued) {  // all MMAs retired before teardown
-        umma_commit(bar_final);
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar_final, 0) && clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
-        }
+      ph ^= 1u;
+    }
+    if (issued) {  // all MMAs retired before teardown
+      umma_commit_elected(bar_final);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bar_final, 0) && clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
       }
     }
   } else if (warp >= WARP_META0 && warp < WARP_META0 + NUM_META_WARPS) {
@@ -926,11 +920,20 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
         }
       }
       // the codes have landed, and the MMAs that last read this A stage have completed (they
-      // released the stage before TMA refilled it).  Their wait comes first: this group did not see the stage's
-      // previous use (another group's), copies may land out of turn, and the wait for the codes is only right
-      // once that use's phase is over.
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty(s), ph ^ 1u, abort_flag))) break;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tma_full(s), ph, abort_flag))) break;
+      // released the stage before TMA refilled it).  Where the ring is not a whole number of group turns, the
+      // stage's previous use was another group's: this group did not see it land, copies may land out of turn,
+      // and a wait by parity is only right once that phase is over, so the release is tested first (both
+      // tests are on their way together: one after the other cost 1-5 % of the kernel).
+      bool landed;
+      if constexpr (STAGES % NG != 0) {
+        const bool released = mbar_try_wait(bar_empty(s), ph ^ 1u);
+        landed = mbar_try_wait(bar_tma_full(s), ph);
+        if (!(released && landed))
+          landed = mbar_wait_bounded(bar_empty(s), ph ^ 1u, abort_flag) && mbar_wait_bounded(bar_tma_full(s), ph, abort_flag);
+      } else {
+        landed = mbar_wait_bounded(bar_tma_full(s), ph, abort_flag);
+      }
+      if (!__all_sync(0xffffffffu, landed)) break;
       tc_fence_after();
       const uint8_t *prow = smem + off_p(FMT, BITS, TT, s) + br * PROW;
       uint32_t o[32];
