@@ -3,9 +3,14 @@
 //   dx[M][K] = dy[M][N] . W[N][K],  dy bf16 (or the gated block's (dg | du)), W quantized, dx bf16
 //
 // The contraction runs over the weight rows n, along which the packed codes are strided, so the weight
-// tile is wanted transposed: D[128 k][TT tokens] += W^T[128 k][64 n] x dy^T.  The dequantisers decode whole
-// 32-weight runs of a row as in the forward kernels and store them as rows of an M-major (transposed) A
-// operand in shared memory; the tensor core does the transposition.
+// tile is wanted transposed: D[128 k][tokens] += W^T[128 k][64 n] x dy^T, W^T the MMA's A operand in tensor memory
+// (lane = k, two n a column) and dy, as it lies, its B operand in shared memory.  The transposition costs
+// nothing: a matrix load with transposition (ldmatrix .trans on 16-bit elements) of eight rows' packed codes
+// gives each thread 16 bits of codes of two neighbouring rows n, n + 1 side by side -- four nibbles, two bytes or
+// eight 2-bit fields of consecutive k -- and each mask of that word is a pair (n, n + 1) of one k: a TMEM word.
+// (A first form decoded along the rows and let the tensor core transpose an M-major A tile in shared memory.  Its
+// stores, the tensor core's reads of it and dy's went through shared memory at 832 of 821 measured cycles a
+// stage against the MMAs' 512; without the tile it is 576.)
 //
 // Operands are fp16 with exact power-of-two scales, as in the forward GEMM (gemm_prep.cuh).  A weight row's
 // scale 2^b_n cannot be undone after a sum over rows, so its inverse goes into the other operand:
@@ -30,8 +35,9 @@
 //   dy16   fp16 [M][Np]      scaled dy, zeros past N
 //   dexp   s32  [M]          -(a_m + DY_BIAS)
 //   rowexp u8   [Np]         exponent byte of 2^(DY_BIAS - b_n)
-//   meta   u32  [K / gran][Np]  scaled metadata of a run of gran weights: int4 (S, Z S) fp16 pair, int6 the
-//                            scales of its two 16-groups, affine (s, b); zeros past N
+//   meta   u32  [K / gran][Np]  scaled metadata of a run of gran weights, two words for each two rows n, n + 1
+//                            of fp16 pairs: their scales, then their offsets (int4 -Z S, affine b; int6 the scales
+//                            of the run's two 16-groups); zeros past N
 //   partial f32 [2 DX_CTAS][tokens a tile][128]
 #pragma once
 #include "gated.cuh"
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Work
 }
 
 // ---- pass 3: scaled metadata, transposed ------------------------------------------------------------
-// The metadata word of run r (of gran weights) of row n: the scales times 2^24 sc, Z S and b times sc = 2^b_n.
+// The metadata of run r (of gran weights) of row n: the scales times 2^24 sc, -Z S and b times sc = 2^b_n.
 constexpr float SUB = 16777216.f;  // 2^24
 template <int FMT>
 QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t r, int64_t K, int G,
@@ -380,7 +386,7 @@ QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t
     const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32) + r);
     const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3));
     const float S = __fmul_rn((float)(c & 0xffu), f16_bits_to_f32(s)) * sc;
-    return pack_f16x2(S * SUB, __fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
+    return pack_f16x2(S * SUB, -__fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
   } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
     const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta + n * (K / 16)) + r);
     const float st = f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3)));
@@ -414,49 +420,45 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
 #pragma unroll
   for (int i = 0; i < WP_RUNS / (WP_THREADS / 32); ++i) {
     const int r = warp + (WP_THREADS / 32) * i;
-    if (r0 + r < runs) ws.meta[(r0 + r) * np + n0 + lane] = turn[lane][r];
+    if (r0 + r < runs) {  // rows n, n + 1: their low halves, then their high halves
+      const uint32_t own = turn[lane][r], other = turn[lane ^ 1][r];
+      ws.meta[(r0 + r) * np + n0 + lane] = (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+    }
   }
   pdl_wait();  // for pass 2
 }
 
 // ---- pass 4: the GEMM ------------------------------------------------------------------------------
 constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, WARP_DEQ0 = 8, NPROD = 3;
-#ifndef NG_TRY
-#define NG_TRY 4
-#endif
-__host__ __device__ constexpr int deq_groups(int tt) { return tt == TT_LARGE ? 2 : NG_TRY; }
+__host__ __device__ constexpr int deq_groups(int tt) { return tt == TT_LARGE ? 2 : 4; }
 __host__ __device__ constexpr int num_threads(int tt) { return (WARP_DEQ0 + 4 * deq_groups(tt)) * 32; }
 
-// Two rings.  What TMA brings -- the dy tile (B), the packed codes and the metadata words -- waits in a ring as
-// deep as shared memory allows (up to 16), because for few tokens the stream of codes is what bounds the kernel
-// and needs bytes in flight; the transposed weight tiles (A, 16 KB each) only have to keep the tensor core
-// busy: up to four.
+// What TMA brings -- the dy tile (B), the packed codes and the metadata words -- waits in a ring as deep as shared
+// memory allows (up to 16): for few tokens the stream of codes bounds the kernel and needs bytes in flight.  The
+// weight tiles (A, 32 columns each) have a ring of up to eight beside the accumulators in tensor memory: two
+// accumulators (an epilogue beside the next tile's MMAs), or one of 256 columns.
 __host__ __device__ constexpr int code_row(int fmt, int bits) { return BKT * gemm::code_bits(fmt, bits) / 8; }
-constexpr int A_BYTES = BN * BKT * 2;
 __host__ __device__ constexpr int b_bytes(int tt) { return tt * BN * 2; }
 __host__ __device__ constexpr int p_bytes(int fmt, int bits) { return BN * code_row(fmt, bits); }
 constexpr int META_BYTES = BN * 4 * 4;  // up to four runs of 32 k
+constexpr uint32_t TMEM_COLS = 512, A_COLS = BN / 2;
+__host__ __device__ constexpr int num_acc(int tt) { return tt == TT_LARGE ? 1 : 2; }
 __host__ __device__ constexpr int stage_bytes(int fmt, int bits, int tt) {
   return b_bytes(tt) + p_bytes(fmt, bits) + META_BYTES;
 }
-__host__ __device__ constexpr int smem_need(int fmt, int bits, int tt, int st, int as) {
-  return st * stage_bytes(fmt, bits, tt) + as * A_BYTES + (2 * st + as + 5) * 8 + 16 + 1024;
-}
-#ifndef AST_TRY
-#define AST_TRY 8
-#endif
-__host__ __device__ constexpr int a_stages(int fmt, int bits, int tt) {
-  int as = tt == TT_LARGE ? 4 : AST_TRY;
-  while (smem_need(fmt, bits, tt, as < 4 ? 4 : as, as) > gemm::SMEM_LIMIT) --as;  // at least as many stages
-  return as;
+__host__ __device__ constexpr int smem_need(int fmt, int bits, int tt, int st) {
+  return st * stage_bytes(fmt, bits, tt) + (3 * st + 5) * 8 + 16 + 1024;
 }
 __host__ __device__ constexpr int stages(int fmt, int bits, int tt) {
   int st = 16;
-  while (smem_need(fmt, bits, tt, st, a_stages(fmt, bits, tt)) > gemm::SMEM_LIMIT) --st;
+  while (smem_need(fmt, bits, tt, st) > gemm::SMEM_LIMIT) --st;
   return st;
 }
+__host__ __device__ constexpr int a_stages(int fmt, int bits, int tt) {
+  return stages(fmt, bits, tt) < 8 ? stages(fmt, bits, tt) : 8;
+}
 __host__ __device__ constexpr int smem_bytes(int fmt, int bits, int tt) {
-  return smem_need(fmt, bits, tt, stages(fmt, bits, tt), a_stages(fmt, bits, tt));
+  return smem_need(fmt, bits, tt, stages(fmt, bits, tt));
 }
 
 // How the tiles are dealt: `waves` whole waves of `ctas` tiles, then the `rest` tiles that are left, their
@@ -523,156 +525,179 @@ struct Params {
   __nv_bfloat16 *dx;
 };
 
-// The order in which a row's weights leave the code words in pairs, which is that of the tile's output rows
-// (any order would do): 0, 4, 1, 5, 2, 6, 3, 7 of 8 weights; bytes 0, 2, 1, 3 of 4; 2-bit fields 0, 8, 1, 9, .. of 16.
-// k of row r of the tile:
+// k of TMEM lane r of a tile, as the matrix loads deal them out (thread t of a warp holds codes of column t / 4):
+// nibbles 4 (t / 4) + i in lane 8 i + t / 4 of the warp's 32, bytes 2 (t / 4) + i of its two 16-k halves, 2-bit
+// fields 8 (t / 4) + i of 64 k, of which the warp takes four (i = 0..3 or 4..7); dense int6: see decode_stage.
 template <int FMT, int BITS>
 QL_DEVI int out_k(int r) {
-  if (FMT == FMT_AFFINE && BITS == 8) return (r & ~3) | ((r & 3) >> 1) | ((r & 1) << 1);
-  if (FMT == FMT_AFFINE && BITS == 2) return (r & ~15) | ((r & 15) >> 1) | ((r & 1) << 3);
-  return (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);
+  if (FMT == FMT_INT6) return (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);
+  if (FMT == FMT_AFFINE && BITS == 8) return (r & ~15) | ((r & 7) << 1) | ((r >> 3) & 1);
+  if (FMT == FMT_AFFINE && BITS == 2) return (r & 64) | ((r & 7) << 3) | ((r >> 3) & 7);
+  return (r & ~31) | ((r & 7) << 2) | ((r >> 3) & 3);
 }
 
 QL_DEVI uint32_t fma_h2(uint32_t q, __half2 s, __half2 o) {
   const __half2 w = __hfma2(*reinterpret_cast<const __half2 *>(&q), s, o);
   return *reinterpret_cast<const uint32_t *>(&w);
 }
+QL_DEVI __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); }
+// Four 8 x 8 matrices of 16-bit elements, transposed; lane l gives the address of row l (16 bytes).
+QL_DEVI void ldmatrix_x4_trans(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+QL_DEVI uint32_t movmatrix_trans(uint32_t v) {
+  uint32_t o;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(v));
+  return o;
+}
+QL_DEVI uint2 lds_u2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+QL_DEVI uint32_t lds_u1(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+// 16 lanes x 32 columns: thread t's words 2 j and 2 j + 1 go to lanes t / 4 and t / 4 + 8, column 4 j + t % 4.
+QL_DEVI void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 
-// The 32 weights of a run of row n: its codes in a stage's code tile at `stg` (the row's swizzle: chunk ^ bits
-// of n), its metadata word mw -> 16 words of scaled fp16 pairs in the order above.  A mask leaves codes in bits
-// 0-3 or 4-7 of the halves (2-bit: 0-1 to 6-7): s[i] is the scale for codes 4 i (2 i) bits up.
+// A warp's 32 k (quarter wq of the tile's 128) of a stage's 64 rows: its code tile at shared address `codes`, its
+// metadata words at `meta` + the thread's offset -> the words of lanes 0-15 (lo) and 16-31 (hi) of the quarter.
+// A mask leaves codes in bits 0-3 or 4-7 of the halves (2-bit: 0-1 to 6-7), which the scale makes up for.
 template <int FMT, int BITS>
-QL_DEVI void decode_run(const uint8_t *stg, int n, int run, uint32_t mw, uint32_t (&o)[16]) {
-  const __half2 mv = *reinterpret_cast<const __half2 *>(&mw);
-  constexpr int PROW = code_row(FMT, BITS);
-  if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {  // 64-byte swizzle
-    const uint4 v = *reinterpret_cast<const uint4 *>(stg + n * 64 + ((run ^ ((n >> 1) & 3)) << 4));
-    const uint32_t c[4] = {v.x, v.y, v.z, v.w};
-    const __half2 s0 = __low2half2(mv), s1 = __hmul2(s0, __float2half2_rn(0.0625f));
-    const __half2 z = FMT == FMT_INT4 ? __hneg2(__high2half2(mv)) : __high2half2(mv);
+QL_DEVI void decode_stage(uint32_t codes, uint32_t meta, int wq, int lane, uint32_t (&lo)[16], uint32_t (&hi)[16]) {
+  if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {  // rows of 64 bytes, 64-byte swizzle
+    uint32_t c[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t c8 = c[q] >> 8;
-      o[4 * q] = fma_h2(c[q] & 0x000F000Fu, s0, z);
-      o[4 * q + 1] = fma_h2(c[q] & 0x00F000F0u, s1, z);
-      o[4 * q + 2] = fma_h2(c8 & 0x000F000Fu, s0, z);
-      o[4 * q + 3] = fma_h2(c8 & 0x00F000F0u, s1, z);
+    for (int x = 0; x < 2; ++x) {
+      const int n = 32 * x + lane;
+      ldmatrix_x4_trans(codes + n * 64 + ((wq ^ ((n >> 1) & 3)) << 4), c + 4 * x);
     }
-  } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {  // 128-byte swizzle
-    const uint4 v = *reinterpret_cast<const uint4 *>(stg + n * 128 + (((2 * run) ^ (n & 7)) << 4));
-    const uint4 u = *reinterpret_cast<const uint4 *>(stg + n * 128 + (((2 * run + 1) ^ (n & 7)) << 4));
-    const uint32_t c[8] = {v.x, v.y, v.z, v.w, u.x, u.y, u.z, u.w};
-    const __half2 s = __low2half2(mv), z = __high2half2(mv);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      o[2 * q] = fma_h2(c[q] & 0x00FF00FFu, s, z);
-      o[2 * q + 1] = fma_h2(__byte_perm(c[q], 0u, 0x4341), s, z);
+    for (int j = 0; j < 8; ++j) {
+      const uint2 m = lds_u2(meta + 32 * j);
+      const __half2 s0 = as_h2(m.x), s1 = __hmul2(s0, __float2half2_rn(0.0625f)), z = as_h2(m.y);
+      const uint32_t c8 = c[j] >> 8;
+      lo[2 * j] = fma_h2(c[j] & 0x000F000Fu, s0, z);
+      lo[2 * j + 1] = fma_h2(c[j] & 0x00F000F0u, s1, z);
+      hi[2 * j] = fma_h2(c8 & 0x000F000Fu, s0, z);
+      hi[2 * j + 1] = fma_h2(c8 & 0x00F000F0u, s1, z);
     }
-  } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: 8 bytes, no swizzle
-    const uint2 v = *reinterpret_cast<const uint2 *>(stg + n * PROW + 8 * run);
-    const uint32_t c[2] = {v.x, v.y};
-    __half2 s[4];
-    s[0] = __low2half2(mv);
+  } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {  // rows of 128 bytes, 128-byte swizzle
+    uint32_t c[2][8];
 #pragma unroll
-    for (int i = 1; i < 4; ++i) s[i] = __hmul2(s[i - 1], __float2half2_rn(0.25f));
-    const __half2 z = __high2half2(mv);
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t c8 = c[q] >> 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[8 * q + i] = fma_h2(c[q] & (0x00030003u << (2 * i)), s[i], z);
-        o[8 * q + 4 + i] = fma_h2(c8 & (0x00030003u << (2 * i)), s[i], z);
+      for (int x = 0; x < 2; ++x) {
+        const int n = 32 * x + lane;
+        ldmatrix_x4_trans(codes + n * 128 + (((2 * wq + b) ^ (n & 7)) << 4), c[b] + 4 * x);
       }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint2 m = lds_u2(meta + 32 * j);
+      const __half2 s = as_h2(m.x), z = as_h2(m.y);
+      lo[2 * j] = fma_h2(c[0][j] & 0x00FF00FFu, s, z);
+      lo[2 * j + 1] = fma_h2(__byte_perm(c[0][j], 0u, 0x4341), s, z);
+      hi[2 * j] = fma_h2(c[1][j] & 0x00FF00FFu, s, z);
+      hi[2 * j + 1] = fma_h2(__byte_perm(c[1][j], 0u, 0x4341), s, z);
     }
-  } else {  // int6: fields f = q & 63, q = (f ^ 32) - 32; the scale changes after 16 weights
+  } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: rows of 32 bytes, two 64-k halves
+    uint32_t c[8];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) ldmatrix_x4_trans(codes + (32 * x + lane) * 32 + 16 * (wq >> 1), c + 4 * x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint2 m = lds_u2(meta + 32 * j);
+      const __half2 quarter = __float2half2_rn(0.25f), z = as_h2(m.y);
+      const __half2 s0 = as_h2(m.x), s1 = __hmul2(s0, quarter), s2 = __hmul2(s1, quarter), s3 = __hmul2(s2, quarter);
+      const uint32_t v = c[j] >> (8 * (wq & 1));
+      lo[2 * j] = fma_h2(v & 0x00030003u, s0, z);
+      lo[2 * j + 1] = fma_h2(v & 0x000C000Cu, s1, z);
+      hi[2 * j] = fma_h2(v & 0x00300030u, s2, z);
+      hi[2 * j + 1] = fma_h2(v & 0x00C000C0u, s3, z);
+    }
+  } else {  // int6: fields f = q & 63, q = (f ^ 32) - 32
     const __half2 m32 = __float2half2_rn(-32.f / SUB);
-    const __half2 s[2] = {__low2half2(mv), __high2half2(mv)};
-    const __half2 z[2] = {__hmul2(s[0], m32), __hmul2(s[1], m32)};
-    if constexpr (FMT == FMT_INT6P) {  // low plane with 64-byte swizzle, then the high plane, 32 bytes a row
-      const uint4 v = *reinterpret_cast<const uint4 *>(stg + n * 64 + ((run ^ ((n >> 1) & 3)) << 4));
-      const uint2 w = *reinterpret_cast<const uint2 *>(stg + BN * 64 + n * 32 + 8 * run);
-      const uint32_t c[4] = {v.x, v.y, v.z, v.w}, hi[4] = {w.x, w.x >> 16, w.y, w.y >> 16};
+    if constexpr (FMT == FMT_INT6P) {  // nibbles as int4, then the high plane, rows of 32 bytes for 128 k
+      uint32_t c[8], h[8];
+      const int g = lane >> 2;
+      // thread t needs the high fields of nibble column t / 4: a byte of the high plane's column 4 (wq & 1) + t / 8
+      const int src = 4 * (4 * (wq & 1) + (g >> 1)) + (lane & 3);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t h = __byte_perm(hi[q], 0u, 0x4140);  // high fields of weights 0-3 and 4-7
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lo = (c[q] >> (4 * e)) & 0x000F000Fu;
-          const uint32_t up = (e < 2 ? h << (4 - 2 * e) : h >> (2 * e - 4)) & 0x00300030u;
-          o[4 * q + e] = fma_h2((lo | up) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
-        }
+      for (int x = 0; x < 2; ++x) {
+        const int n = 32 * x + lane;
+        ldmatrix_x4_trans(codes + n * 64 + ((wq ^ ((n >> 1) & 3)) << 4), c + 4 * x);
+        ldmatrix_x4_trans(codes + BN * 64 + n * 32 + 16 * (wq >> 1), h + 4 * x);
       }
-    } else {  // 24 bytes: eight 24-bit units of 4 weights; words of the low (a) and high (b) two of 2 x 4 weights
-      const uint2 *src = reinterpret_cast<const uint2 *>(stg + n * PROW + 24 * run);
-      const uint2 x = src[0], y = src[1], w = src[2];
-      const uint32_t u[8] = {x.x, __funnelshift_r(x.x, x.y, 24), __funnelshift_r(x.y, y.x, 16), y.x >> 8,
-                             y.y, __funnelshift_r(y.y, w.x, 24), __funnelshift_r(w.x, w.y, 16), w.y >> 8};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t a = __byte_perm(u[2 * q], u[2 * q + 1], 0x5410);
-        const uint32_t b = __byte_perm(u[2 * q] >> 12, u[2 * q + 1] >> 12, 0x5410);
-        o[4 * q] = fma_h2((a & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
-        o[4 * q + 1] = fma_h2(((a >> 6) & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
-        o[4 * q + 2] = fma_h2((b & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
-        o[4 * q + 3] = fma_h2(((b >> 6) & 0x003F003Fu) ^ 0x00200020u, s[q >> 1], z[q >> 1]);
+      for (int j = 0; j < 8; ++j) {
+        const __half2 s = as_h2(lds_u1(meta + 32 * j + (g & 4))), z = __hmul2(s, m32);  // 16-weight groups: g / 4
+        const uint32_t hv = __shfl_sync(0xffffffffu, h[j], src) >> (8 * (g & 1));
+        lo[2 * j] = fma_h2(((c[j] & 0x000F000Fu) | ((hv << 4) & 0x00300030u)) ^ 0x00200020u, s, z);
+        lo[2 * j + 1] = fma_h2((((c[j] >> 4) & 0x000F000Fu) | ((hv << 2) & 0x00300030u)) ^ 0x00200020u, s, z);
+        hi[2 * j] = fma_h2((((c[j] >> 8) & 0x000F000Fu) | (hv & 0x00300030u)) ^ 0x00200020u, s, z);
+        hi[2 * j + 1] = fma_h2((((c[j] >> 12) & 0x000F000Fu) | ((hv >> 2) & 0x00300030u)) ^ 0x00200020u, s, z);
+      }
+    } else {
+      // dense: thread t takes row t / 4 of eight and, of each 8 codes (two 24-bit units), codes t % 4 and 4 + t % 4 as
+      // the elements 2 (t % 4), + 1 of an 8 x 8 matrix, which movmatrix transposes: row p is k = p / 2 + 4 (p % 2)
+      const int g = lane >> 2, sh = 6 * (lane & 3);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t row = codes + (8 * j + g) * code_row(FMT, BITS) + 24 * wq;
+        const uint2 x = lds_u2(row), y = lds_u2(row + 8), w = lds_u2(row + 16);
+        const uint32_t u[8] = {x.x, __funnelshift_r(x.x, x.y, 24), __funnelshift_r(x.y, y.x, 16), y.x >> 8,
+                               y.y, __funnelshift_r(y.y, w.x, 24), __funnelshift_r(w.x, w.y, 16), w.y >> 8};
+        const uint2 m = lds_u2(meta + 32 * j);
+        const __half2 s[2] = {as_h2(m.x), as_h2(m.y)};
+        const __half2 z[2] = {__hmul2(s[0], m32), __hmul2(s[1], m32)};
+        uint32_t o[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t f = (__byte_perm(u[2 * b] >> sh, u[2 * b + 1] >> sh, 0x5410) & 0x003F003Fu) ^ 0x00200020u;
+          o[b] = fma_h2(movmatrix_trans(f), s[b >> 1], z[b >> 1]);
+        }
+        lo[2 * j] = o[0];
+        lo[2 * j + 1] = o[1];
+        hi[2 * j] = o[2];
+        hi[2 * j + 1] = o[3];
       }
     }
   }
 }
 
-// Shared-memory matrix descriptor of an M-major operand in the 128-byte-swizzled layout: for each
-// contraction index a row of 128 bytes (64 fp16 along M), 16-byte chunks XOR-ed with (row % 8); the next 8
-// contraction indices 1024 bytes on, the next 64 of M BN * 128 bytes on.
-QL_DEVI uint64_t umma_desc_m_sw128(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);
-  d |= (uint64_t)((BN * 128) >> 4) << 16;  // leading byte offset: next 64 of M
-  d |= (uint64_t)(1024 >> 4) << 32;        // stride byte offset: next 8 of the contraction
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-constexpr uint32_t IDESC_A_M_MAJOR = 1u << 15;
-
-// The MMAs of a stage, D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16, four slices of 16 rows n (2048
-// bytes of A, 32 bytes along B's rows: 128 and 2 descriptor units), and the barrier that receives an arrival
-// when they are done; issued like umma_stage_tmem_a.
-QL_DEVI void umma_stage(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "add.u64 a, %1, 128;\n\tadd.u64 b, %2, 2;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.u64 a, %1, 256;\n\tadd.u64 b, %2, 4;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.u64 a, %1, 384;\n\tadd.u64 b, %2, 6;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(bar)
-      : "memory");
-}
 // Warp roles: 0, 2 and 3 TMA producers, 1 tensor memory and MMA issue, 4-7 epilogue (one k a lane), 8..
-// dequantisers in groups of four warps that take the stages in turn.  A thread of a group
-// decodes 64 weights of one row n: 128 bytes of A.
+// dequantisers in groups of four warps (one a quarter of the TMEM lanes) that take the stages in turn.
 template <int FMT, int BITS, int TT>
 __global__ void __launch_bounds__(num_threads(TT), 1)
     gemm_dx_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_codes,
                    const __grid_constant__ CUtensorMap map_codes_hi, const __grid_constant__ CUtensorMap map_meta,
                    Params p) {
   constexpr int STAGES = stages(FMT, BITS, TT), AST = a_stages(FMT, BITS, TT), NG = deq_groups(TT);
+  constexpr int NACC = num_acc(TT);
   constexpr int PROW = code_row(FMT, BITS);
   constexpr int OFF_P = b_bytes(TT), OFF_M = OFF_P + p_bytes(FMT, BITS);  // in a stage, after the dy tile
-  constexpr int STAGE = stage_bytes(FMT, BITS, TT), OFF_A = STAGES * STAGE;
+  constexpr int STAGE = stage_bytes(FMT, BITS, TT);
+  constexpr uint32_t A_COL0 = NACC * TT;
   static_assert(STAGE % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
   static_assert(STAGES >= AST && NG <= STAGES && NPROD <= STAGES, "an A slot's previous MMAs are found by their stage");
-  constexpr uint32_t TMEM_COLS = 2 * TT;
+  static_assert(A_COL0 + AST * A_COLS <= TMEM_COLS, "A ring beside the accumulators");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_A + AST * A_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + AST + 5);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
   auto bar_tma_full = [&](int s) { return smem_u32(bars + s); };
@@ -770,15 +795,15 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
       }
     }
   } else if (warp == WARP_MMA) {
-    const uint32_t idesc = umma_idesc_f16_f32(BKT, tokens) | IDESC_A_M_MAJOR;
-    const uint64_t ad0 = umma_desc_m_sw128(sbase + OFF_A), bd0 = umma_desc_k_sw128(sbase);
+    const uint32_t idesc = umma_idesc_f16_f32(BKT, tokens);
+    const uint64_t bd0 = umma_desc_k_sw128(sbase);
     int s = 0, as = 0;
     uint32_t ph = 0, aph = 0;
     bool ok = true, issued = false;
     Piece pc;
     for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i) {
-      const int a = i & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_acc_empty(a), ((i >> 1) & 1) ^ 1, abort_flag))) break;
+      const int a = i % NACC;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_acc_empty(a), ((i / NACC) & 1) ^ 1, abort_flag))) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(a * TT);
       for (int st = pc.step0; st < pc.step1; ++st) {
@@ -789,8 +814,8 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
         }
         tc_fence_after();
         // done: the stage and the A slot are free
-        umma_stage(d_tmem, ad0 + (uint64_t)(as * (A_BYTES >> 4)), bd0 + (uint64_t)(s * (STAGE >> 4)), idesc,
-                   st != pc.step0, bar_empty(s));
+        umma_stage_tmem_a(d_tmem, tmem_base + A_COL0 + (uint32_t)as * A_COLS, bd0 + (uint64_t)(s * (STAGE >> 4)), idesc,
+                          st != pc.step0, bar_empty(s));
         issued = true;
         step_ring(s, ph, 1, STAGES);
         step_ring(as, aph, 1, AST);
@@ -807,12 +832,12 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
     const int e = warp - WARP_EPI0;  // TMEM lane quarter
     Piece pc;
     for (int i = 0; get_piece(p.deal, cta, i, pc); ++i) {
-      const int a = i & 1;
+      const int a = i % NACC;
       const int64_t k_tile = pc.tile / p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
       const int64_t k = k_tile * BKT + out_k<FMT, BITS>(32 * e + lane);
       const int64_t m0 = m_tile * tokens;
       const int valid = (int)(p.M - m0 < tokens ? p.M - m0 : tokens);
-      if (!mbar_wait_suspend(bar_acc_full(a), (i >> 1) & 1, abort_flag)) break;
+      if (!mbar_wait_suspend(bar_acc_full(a), (i / NACC) & 1, abort_flag)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < tokens / 16; ++c) {
@@ -835,7 +860,7 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
             }
           }
         } else {
-          float *dst = p.partial + ((int64_t)pc.slot * tokens + 16 * c) * BKT + 32 * e + lane;
+          float *dst = p.partial + ((int64_t)pc.slot * tokens + 16 * c) * BKT + out_k<FMT, BITS>(32 * e + lane);
 #pragma unroll
           for (int t = 0; t < 16; ++t)
             if (16 * c + t < valid) dst[t * BKT] = __uint_as_float(r[t]);
@@ -844,12 +869,12 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
     }
   } else if (warp >= WARP_DEQ0) {
     const int wd = warp - WARP_DEQ0, g = wd >> 2;
-    const int tau = 32 * (wd & 3) + lane;
-    const int n = tau & 63, half = tau >> 6;  // row of the stage, 64-k half of the tile
-    // the half's two runs: their words in a stage's metadata
+    const int wq = wd & 3;  // lane quarter
+    // the thread's place in a stage's metadata: the run of its 32 k (2-bit: of its 8 of 64), rows 2 (t % 4), + 1
+    const int run = BITS == 2 && FMT == FMT_AFFINE ? 2 * (wq >> 1) + (lane >> 4) : wq;
     const int run_shift = FMT != FMT_AFFINE || p.G == 32 ? 0 : p.G == 64 ? 1 : 2;
-    const int meta0 = OFF_M + 4 * (((2 * half) >> run_shift) * BN + n), meta1 = OFF_M + 4 * (((2 * half + 1) >> run_shift) * BN + n);
-    uint8_t *const arow0 = smem + OFF_A + half * (BN * 128) + n * 128;
+    const int meta0 = OFF_M + (run >> run_shift) * (BN * 4) + 8 * (lane & 3);
+    const uint32_t t_row = tmem_base + ((uint32_t)(32 * wq) << 16) + A_COL0;
     int64_t total = 0;  // this CTA's stages
     Piece pc;
     for (int i = 0; get_piece(p.deal, cta, i, pc); ++i) total += pc.step1 - pc.step0;
@@ -869,18 +894,13 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
       // it - AST, and so of every step before, are done; the previous use of stage s (it - STAGES) is one of them.
       if (!__all_sync(0xffffffffu, mbar_wait_suspend(bar_empty(es), eph, abort_flag))) break;
       if (!__all_sync(0xffffffffu, mbar_wait_suspend(bar_tma_full(s), ph, abort_flag))) break;
-      const uint8_t *stg = smem + s * STAGE;
-      uint8_t *arow = arow0 + as * A_BYTES;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t o[16];
-        decode_run<FMT, BITS>(stg + OFF_P, n, 2 * half + h, *reinterpret_cast<const uint32_t *>(stg + (h ? meta1 : meta0)), o);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4 *>(arow + (((4 * h + q) ^ (n & 7)) << 4)) =
-              make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-      }
-      fence_proxy_async_smem();
+      tc_fence_after();
+      uint32_t lo[16], hi[16];
+      decode_stage<FMT, BITS>(sbase + s * STAGE + OFF_P, sbase + s * STAGE + meta0, wq, lane, lo, hi);
+      tmem_st_16x128b_x8(t_row + (uint32_t)as * A_COLS, lo);
+      tmem_st_16x128b_x8(t_row + (uint32_t)as * A_COLS + (16u << 16), hi);
+      tmem_st_wait();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_a_full(as));
       step_ring(s, ph, NG, STAGES);
@@ -898,11 +918,9 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
 }
 
 // ---- pass 5: the sums of the split tiles' parts -------------------------------------------------------
-// A CTA takes 32 tokens of a tile, a thread 16 rows (sixteen consecutive k, see out_k) of one of them; the
-// parts are added in the order of the shares.
+// A CTA takes 32 tokens of a tile, a thread 16 k of one of them; the parts are added in the order of the shares.
 constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 16);
 
-template <int FMT, int BITS>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
   __shared__ int range[3];  // first share, its slot, end of the shares
   const Deal &d = p.deal;
@@ -938,13 +956,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
     slot = 2 * (c + 1);
   }
   const int e = __ldg(p.dexp + m);
-  float o[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[out_k<FMT, BITS>(i)] = mul_pow2(v[i], e);
+  for (int i = 0; i < 16; ++i) v[i] = mul_pow2(v[i], e);
   uint4 *dst = reinterpret_cast<uint4 *>(p.dx + m * p.K + k);
-  dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-  dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]),
-                      pack_bf16x2(o[14], o[15]));
+  dst[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  dst[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                      pack_bf16x2(v[14], v[15]));
 }
 
 }  // namespace dx

@@ -131,16 +131,15 @@ struct TmapKey {
   const void *base;
   uint64_t inner, outer, row_bytes;
   uint32_t box_inner, box_outer;
-  int dt, sw, l2;
+  int dt, sw;
   bool operator==(const TmapKey &o) const {
     return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes &&
-           box_inner == o.box_inner && box_outer == o.box_outer && dt == o.dt && sw == o.sw && l2 == o.l2;
+           box_inner == o.box_inner && box_outer == o.box_outer && dt == o.dt && sw == o.sw;
   }
 };
 
 bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
-               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw,
-               CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
   constexpr int kEntries = 32;
   struct Entry {
     TmapKey key;
@@ -149,7 +148,7 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint6
   };
   static thread_local Entry cache[kEntries] = {};
   static thread_local int next = 0;
-  const TmapKey key{base, inner, outer, row_bytes, box_inner, box_outer, (int)dt, (int)sw, (int)l2};
+  const TmapKey key{base, inner, outer, row_bytes, box_inner, box_outer, (int)dt, (int)sw};
   for (int i = 0; i < kEntries; ++i)
     if (cache[i].valid && cache[i].key == key) {
       *map = cache[i].map;
@@ -162,7 +161,7 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint6
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
   if (fn(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-         l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   cache[next] = Entry{key, *map, true};
   next = (next + 1) % kEntries;
@@ -689,9 +688,6 @@ bool launch_dependent(void (*kern)(Params...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&c, kern, Params(args)...) == cudaSuccess;
 }
 
-#ifndef CODES_L2
-#define CODES_L2 CU_TENSOR_MAP_L2_PROMOTION_NONE
-#endif
 // The passes of gemm_dx.cuh; `prep` launches pass 2.
 template <int FMT, int BITS, int TT, class Prep>
 ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t M, void *dx_out, void *workspace,
@@ -715,8 +711,7 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
                                   : box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
   if (!encode_2d(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws.dy16, (uint64_t)np, (uint64_t)M, (uint64_t)np * 2, BN,
                  (uint32_t)p.deal.tokens, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes, box, BN, sw,
-                 CODES_L2) ||
+      !encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes, box, BN, sw) ||
       !encode_2d(&mm, CU_TENSOR_MAP_DATA_TYPE_UINT32, ws.meta, (uint64_t)np, (uint64_t)(K / gr), (uint64_t)np * 4, BN,
                  gr >= BKT ? 1u : (uint32_t)(BKT / gr), CU_TENSOR_MAP_SWIZZLE_NONE))
     return cuda_failed();
@@ -743,7 +738,7 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
                         my, mc, mh, mm, p))
     return cuda_failed();
   if (p.deal.joins() &&
-      !launch_dependent(join_kernel<FMT, BITS>,
+      !launch_dependent(join_kernel,
                         dim3((unsigned)p.deal.rest, (unsigned)((std::min<int64_t>(M, p.deal.tokens) + JOIN_TOKENS - 1) / JOIN_TOKENS)),
                         JOIN_THREADS, 0, st, p))
     return cuda_failed();
