@@ -132,6 +132,30 @@ QL_DEVI void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int
       : "memory");
 }
 
+// The same, and the arrival that announces its bytes, for a whole warp that stays together: an elected lane issues
+// by predicate (as umma_stage_tmem_a: a single-lane branch costs moves into uniform registers per operand).
+QL_DEVI void mbar_expect_tx_elected(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b64 st;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+QL_DEVI void tma_load_2d_elected(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+QL_DEVI void tma_load_3d_elected(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // Untiled bulk copy global -> shared completing on an mbarrier: both addresses 16-byte aligned,
 // size a multiple of 16.
 QL_DEVI void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {

@@ -141,7 +141,7 @@ struct Params {
 };
 
 // The gated form: the layer's rows are F = N / 2 gate rows, then F up rows, and a tile is 64 features:
-// their 64 gate rows and 64 up rows (two code boxes of 64 rows).  Which of the tile's rows goes to which
+// their 64 gate rows and 64 up rows (one code box of 2 x 64 rows of the layer as [2][F] rows).  Which of the tile's rows goes to which
 // TMEM lane is the dequantisers' choice, and they give each lane quarter 16 features, gate rows in its
 // lanes 0-15 and up rows in lanes 16-31: g and u of a feature then meet in one epilogue warp by a
 // shuffle, without shared memory.  Box row (and metadata slot row) of lane r of the tile:
@@ -150,8 +150,8 @@ template <bool GATED>
 QL_DEVI int box_row(int r) {
   return GATED ? ((r & 16) ? GATED_F : 0) + 16 * (r >> 5) + (r & 15) : r;
 }
-// Layer row of box row br.  A tile's last features may be past F: their gate rows are then up rows (or,
-// like their up rows, past N) whose results are not stored.
+// Layer row of box row br.  A tile's last features may be past F: their codes are zeros, their metadata that of
+// other rows (or, past N, zeros), and their results are not stored.
 template <bool GATED>
 QL_DEVI int64_t layer_row(int64_t n_tile, int br, int64_t N) {
   return GATED ? (br < GATED_F ? n_tile * GATED_F + br : N / 2 + n_tile * GATED_F + br - GATED_F) : n_tile * BN + br;
@@ -429,6 +429,100 @@ QL_DEVI void gated_store(const Params &p, const uint32_t (&r)[16], int64_t f, in
   if (p.saved) gated_save(p, g, u, F, f, m0, rows_left, lane);
 }
 
+// chunk_to_f16 of the gated form: the codes enter as the fp16 subnormals q 2^-24 that a mask leaves in the low bits
+// of a half (up to bit 9), and 2^24 goes into the scale, so a pair of weights is a mask and a fused multiply-add.
+// For that scale to be an fp16 number the weights are 2^-GATED_DOWN lower than the row scales of the prep pass put
+// them (int4: S <= 2^15 / 7.5, affine: s <= 2^16 / (2^bits - 1)); int6 rounds its scale and its product.
+template <int FMT, int BITS>
+__host__ __device__ constexpr int gated_down() { return FMT == FMT_AFFINE && BITS == 2 ? 24 : 21; }
+
+template <int FMT, int BITS>
+QL_DEVI void gated_chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], const uint8_t *src, const uint8_t *src_hi,
+                                uint32_t gm, uint32_t st, float sc, uint32_t (&o)[16]) {
+  constexpr float UP = (float)(1 << (24 - gated_down<FMT, BITS>()));  // 2^24 times 2^-GATED_DOWN
+  auto fma2 = [](uint32_t q, __half2 s, __half2 z) {
+    const __half2 w = __hfma2(*reinterpret_cast<const __half2 *>(&q), s, z);
+    return *reinterpret_cast<const uint32_t *>(&w);
+  };
+  constexpr float DOWN = 1.f / (float)(1 << gated_down<FMT, BITS>());
+  if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {
+    float S, z;
+    if constexpr (FMT == FMT_INT4) {
+      const float scf = __uint_as_float(0x4B000000u | (gm & 0xffu)) - 8388608.f;
+      const float zcf = __uint_as_float(0x4B000000u | ((gm >> 8) & 0xffu)) - 8388608.f;
+      S = scf * f16_bits_to_f32(st) * sc;
+      z = -(zcf * f16_bits_to_f32(st >> 16)) * S * DOWN;
+    } else {
+      S = bf16_bits_to_f32(gm) * sc;
+      z = bf16_bits_to_f32(gm >> 16) * sc * DOWN;
+    }
+    const __half2 s0 = __float2half2_rn(S * UP), s1 = __hmul2(s0, __float2half2_rn(0.0625f)), z2 = __float2half2_rn(z);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t w8 = cw[q] >> 8;
+      o[4 * q] = fma2(cw[q] & 0x000F000Fu, s0, z2);
+      o[4 * q + 1] = fma2(cw[q] & 0x00F000F0u, s1, z2);
+      o[4 * q + 2] = fma2(w8 & 0x000F000Fu, s0, z2);
+      o[4 * q + 3] = fma2(w8 & 0x00F000F0u, s1, z2);
+    }
+  } else if constexpr (FMT == FMT_AFFINE) {
+    const __half2 z2 = __float2half2_rn(bf16_bits_to_f32(gm >> 16) * sc * DOWN);
+    __half2 s[4];
+    s[0] = __float2half2_rn(bf16_bits_to_f32(gm) * sc * UP);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) s[e] = BITS == 2 ? __hmul2(s[e - 1], __float2half2_rn(0.25f)) : s[0];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (BITS == 8) {
+        const uint32_t w0 = cw[2 * q], w1 = cw[2 * q + 1];
+        const uint32_t t0 = __byte_perm(w0, w1, 0x5140), t1 = __byte_perm(w0, w1, 0x7362);  // (0 4 1 5) (2 6 3 7)
+        o[4 * q] = fma2(__byte_perm(t0, 0u, 0x4140), s[0], z2);
+        o[4 * q + 1] = fma2(__byte_perm(t0, 0u, 0x4342), s[0], z2);
+        o[4 * q + 2] = fma2(__byte_perm(t1, 0u, 0x4140), s[0], z2);
+        o[4 * q + 3] = fma2(__byte_perm(t1, 0u, 0x4342), s[0], z2);
+      } else {
+        const uint32_t u = __byte_perm(cw[q >> 1] >> (16 * (q & 1)), 0u, 0x4140);  // codes 0-3 in byte 0, 4-7 in byte 2
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[4 * q + e] = fma2(u & (0x00030003u << (2 * e)), s[e], z2);
+      }
+    }
+  } else {  // int6: fields f = q & 63, q = (f ^ 32) - 32; two 16-weight groups
+    const float step = f16_bits_to_f32(st) * sc * UP;
+    const __half2 s[2] = {__float2half2_rn((float)(int8_t)gm * step), __float2half2_rn((float)(int8_t)(gm >> 8) * step)};
+    const __half2 m32 = __float2half2_rn(-32.f / 16777216.f);
+    const __half2 z[2] = {__hmul2(s[0], m32), __hmul2(s[1], m32)};
+    if constexpr (FMT == FMT_INT6P) {
+      const uint4 l = *reinterpret_cast<const uint4 *>(src);
+      const uint2 h = *reinterpret_cast<const uint2 *>(src_hi);
+      const uint32_t c[4] = {l.x, l.y, l.z, l.w}, hi[4] = {h.x, h.x >> 16, h.y, h.y >> 16};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t u = __byte_perm(hi[q], 0u, 0x4140);
+        const __half2 sq = s[q >> 1], zq = z[q >> 1];
+        o[4 * q] = fma2(((c[q] & 0x000F000Fu) | ((u << 4) & 0x00300030u)) ^ 0x00200020u, sq, zq);
+        o[4 * q + 1] = fma2((((c[q] >> 4) & 0x000F000Fu) | ((u << 2) & 0x00300030u)) ^ 0x00200020u, sq, zq);
+        o[4 * q + 2] = fma2((((c[q] >> 8) & 0x000F000Fu) | (u & 0x00300030u)) ^ 0x00200020u, sq, zq);
+        o[4 * q + 3] = fma2((((c[q] >> 12) & 0x000F000Fu) | ((u >> 2) & 0x00300030u)) ^ 0x00200020u, sq, zq);
+      }
+    } else {  // eight 24-bit units of four codes
+      const uint2 *s2 = reinterpret_cast<const uint2 *>(src);
+      const uint2 x = s2[0], y = s2[1], w = s2[2];
+      const uint32_t u[8] = {x.x, __funnelshift_r(x.x, x.y, 24), __funnelshift_r(x.y, y.x, 16), y.x >> 8,
+                             y.y, __funnelshift_r(y.y, w.x, 24), __funnelshift_r(w.x, w.y, 16), w.y >> 8};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a = __byte_perm(u[2 * q], u[2 * q + 1], 0x5410);
+        const uint32_t b = __byte_perm(u[2 * q] >> 12, u[2 * q + 1] >> 12, 0x5410);
+        const __half2 sq = s[q >> 1], zq = z[q >> 1];
+        o[4 * q] = fma2((a & 0x003F003Fu) ^ 0x00200020u, sq, zq);
+        o[4 * q + 1] = fma2(((a >> 6) & 0x003F003Fu) ^ 0x00200020u, sq, zq);
+        o[4 * q + 2] = fma2((b & 0x003F003Fu) ^ 0x00200020u, sq, zq);
+        o[4 * q + 3] = fma2(((b >> 6) & 0x003F003Fu) ^ 0x00200020u, sq, zq);
+      }
+    }
+  }
+}
+
 // What a lane needs of its row of a gated tile: its feature, its scale exponent, the tile's tokens, and
 // whether every exponent sum of the warp's rows and these tokens is that of a normal float (then D * 2^e is
 // one multiplication by 2^e built from its bits, the same single rounding as mul_pow2).
@@ -436,9 +530,9 @@ struct GatedRow {
   int64_t f, m0;
   int we, chunks;  // chunks of 16 tokens that hold any
   bool one_mul;
-  QL_DEVI GatedRow(const Params &p, int64_t n_tile, int64_t m_tile, int tt, int e, int lane) {
+  QL_DEVI GatedRow(const Params &p, int64_t n_tile, int64_t m_tile, int tt, int e, int lane, int down) {
     const int64_t n = layer_row<true>(n_tile, box_row<true>(32 * e + lane), p.N);
-    we = n < p.N ? p.ws.wexp[n] : 0;
+    we = (n < p.N ? p.ws.wexp[n] : 0) + down;  // the weights sit 2^-down below the row scales
     f = n_tile * GATED_F + 16 * e + (lane & 15);
     m0 = m_tile * tt;
     const int64_t left = p.M - m0;
@@ -589,49 +683,45 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
     if (lane == 0) {
       tma_prefetch_desc(&map_x);
       tma_prefetch_desc(&map_codes);
-      int64_t it = 0;
-      int s = 0;
-      uint32_t ph = 0;
-      Cursor cur = cursor0();
-      bool ok = true;
-      const int64_t n_it = copies_withheld() ? 0 : total_it;  // steps whose copies are started
-      for (; it < n_it; ++it) {
-        if (!mbar_wait_bounded(bar_empty(s), ph ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx(bar_tma_full(s), STAGE_TX);
-        tma_load_2d(sbase + off_a(TT, s), &map_x, bar_tma_full(s), cur.kb * BK, (int32_t)(cur.m_tile * TT));
-        // the tile's code rows, as one box (or, gated, as a gate box and an up box of 64 rows)
-        auto load_codes = [&](int box_bytes, int off, int32_t x) {
-          if constexpr (GATED) {
-            const uint32_t dst = sbase + off_p(FMT, BITS, TT, s) + off;
-            tma_load_2d(dst, &map_codes, bar_tma_full(s), x, (int32_t)(cur.n_tile * GATED_F));
-            tma_load_2d(dst + GATED_F * box_bytes, &map_codes, bar_tma_full(s), x,
-                        (int32_t)(p.N / 2 + cur.n_tile * GATED_F));
-          } else {
-            tma_load_2d(sbase + off_p(FMT, BITS, TT, s) + off, &map_codes, bar_tma_full(s), x,
-                        (int32_t)(cur.n_tile * BN));
-          }
-        };
-        if constexpr (FMT == FMT_INT6P) {  // k-step kb: low-plane bytes 32 (kb % 4) .. and high-plane
-                                           // bytes 128 + 16 (kb % 4) .. of super-block kb / 4, by 16-byte boxes
-          const int32_t x0 = 192 * (cur.kb >> 2) + 32 * (cur.kb & 3), xh = 192 * (cur.kb >> 2) + 128 + 16 * (cur.kb & 3);
-          load_codes(16, 0, x0);
-          load_codes(16, 16 * BN, x0 + 16);
-          load_codes(16, 32 * BN, xh);
-        } else {
-          load_codes(PROW, 0, cur.kb * PROW);
-        }
-        step_ring(s, ph, STAGES);
-        advance(cur);
+    }
+    __syncwarp();
+    int64_t it = 0;
+    int s = 0;
+    uint32_t ph = 0;
+    Cursor cur = cursor0();
+    bool ok = true;
+    const int64_t n_it = copies_withheld() ? 0 : total_it;  // steps whose copies are started
+    for (; it < n_it; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty(s), ph ^ 1u, abort_flag))) {
+        ok = false;
+        break;
       }
-      if (!ok) {  // let copies already issued land before the CTA can exit
-        for (int64_t j = it - 1; j >= 0 && j >= it - STAGES; --j) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(bar_tma_full((int)(j % STAGES)), (uint32_t)((j / STAGES) & 1)) &&
-                 clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
-          }
+      const uint32_t bar = bar_tma_full(s);
+      mbar_expect_tx_elected(bar, STAGE_TX);
+      // the tile's code rows: one box (gated: 64 gate rows and the 64 up rows of the same features)
+      auto load_codes = [&](int off, int32_t x) {
+        const uint32_t dst = sbase + off_p(FMT, BITS, TT, s) + off;
+        if constexpr (GATED) tma_load_3d_elected(dst, &map_codes, bar, x, (int32_t)(cur.n_tile * GATED_F), 0);
+        else tma_load_2d_elected(dst, &map_codes, bar, x, (int32_t)(cur.n_tile * BN));
+      };
+      if constexpr (FMT == FMT_INT6P) {  // k-step kb: low-plane bytes 32 (kb % 4) .. and high-plane
+                                         // bytes 128 + 16 (kb % 4) .. of super-block kb / 4, by 16-byte boxes
+        const int32_t x0 = 192 * (cur.kb >> 2) + 32 * (cur.kb & 3), xh = 192 * (cur.kb >> 2) + 128 + 16 * (cur.kb & 3);
+        load_codes(0, x0);
+        load_codes(16 * BN, x0 + 16);
+        load_codes(32 * BN, xh);
+      } else {
+        load_codes(0, cur.kb * PROW);
+      }
+      tma_load_2d_elected(sbase + off_a(TT, s), &map_x, bar, cur.kb * BK, (int32_t)(cur.m_tile * TT));
+      step_ring(s, ph, STAGES);
+      advance(cur);
+    }
+    if (!ok) {  // let copies already issued land before the CTA can exit
+      for (int64_t j = it - 1; j >= 0 && j >= it - STAGES; --j) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar_tma_full((int)(j % STAGES)), (uint32_t)((j / STAGES) & 1)) &&
+               clock64() - t0 < QL_WAIT_LIMIT_CYCLES) {
         }
       }
     }
@@ -731,20 +821,23 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
         const int a = (int)(tcount % NACC);
         const bool moved = NACC == 1 && tile + gridDim.x < num_tiles;
         const bool shared_out = NACC == 1 && !moved;
-        const GatedRow row(p, n_tile, m_tile, TT, e, lane);
-        if (!mbar_wait_bounded(bar_acc_full(a), (uint32_t)(tcount / NACC) & 1, abort_flag)) break;
+        const GatedRow row(p, n_tile, m_tile, TT, e, lane, gated_down<FMT, BITS>());
+        if (!mbar_wait_suspend(bar_acc_full(a), (uint32_t)(tcount / NACC) & 1, abort_flag)) break;
         tc_fence_after();
         const uint32_t t_acc = tmem_base + ((uint32_t)(32 * e) << 16) + (uint32_t)(a * TT);
         if (moved) {
 #pragma unroll 1
-          for (int c = 0; c < row.chunks; c += 2) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t_acc + 16 * c, r);
+          for (int c = 0; c < row.chunks; c += 4) {  // (columns past the tokens are moved too, within the tile)
+            uint32_t r[2][32];
+            tmem_ld_32x32b_x32(t_acc + 16 * c, r[0]);
+            tmem_ld_32x32b_x32(t_acc + 16 * c + 32, r[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              scratch[(4 * c + j) * BN] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                                      __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t *v = r[j >> 3] + 4 * (j & 7);
+              scratch[(4 * c + j) * BN] = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]),
+                                                      __uint_as_float(v[2]), __uint_as_float(v[3]));
+            }
           }
           tc_fence_before();
           __syncwarp();
@@ -937,6 +1030,11 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       tc_fence_after();
       const uint8_t *prow = smem + off_p(FMT, BITS, TT, s) + br * PROW;
       uint32_t o[32];
+      auto to_f16 = [&](const uint32_t(&cw)[code_bits(FMT, BITS)], const uint8_t *src, const uint8_t *src_hi,
+                        uint32_t g1, uint32_t s1, uint32_t(&out)[16]) {
+        if constexpr (GATED) gated_chunk_to_f16<FMT, BITS>(cw, src, src_hi, g1, s1, sc, out);
+        else chunk_to_f16<FMT, BITS>(cw, src, src_hi, g1, s1, sc, out);
+      };
       if constexpr (PROW == 32 && (FMT == FMT_INT4 || FMT == FMT_AFFINE)) {
         // the row's two 16-byte chunks, read in the order (h ^ bit 2 of the row) so that the 32 lanes'
         // first reads cover all 32 banks in four wavefronts (rows are 32 bytes apart)
@@ -946,8 +1044,8 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
         const uint4 c0 = sw ? vb : va, c1 = sw ? va : vb;
         const uint32_t cw0[4] = {c0.x, c0.y, c0.z, c0.w}, cw1[4] = {c1.x, c1.y, c1.z, c1.w};
         uint32_t o0[16], o1[16];
-        chunk_to_f16<FMT, BITS>(cw0, nullptr, nullptr, gm[0], st[0], sc, o0);
-        chunk_to_f16<FMT, BITS>(cw1, nullptr, nullptr, gm[1], st[1], sc, o1);
+        to_f16(cw0, nullptr, nullptr, gm[0], st[0], o0);
+        to_f16(cw1, nullptr, nullptr, gm[1], st[1], o1);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           o[i] = o0[i];
@@ -965,7 +1063,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
           uint32_t cw[code_bits(FMT, BITS)];
           if constexpr (FMT == FMT_INT4 || FMT == FMT_AFFINE) load_code_words<FMT, BITS>(src, cw);
           uint32_t oh[16];
-          chunk_to_f16<FMT, BITS>(cw, src, src_hi, gm[h], st[h], sc, oh);
+          to_f16(cw, src, src_hi, gm[h], st[h], oh);
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[16 * h + i] = oh[i];
         }
@@ -988,7 +1086,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       if (my_tiles > 0 && !*abort_flag && __all_sync(0xffffffffu, mbar_wait_bounded(bar_final, 0, abort_flag))) {
         tc_fence_after();
         const int64_t tile = blockIdx.x + (my_tiles - 1) * gridDim.x, n_tile = tile / m_tiles;
-        const GatedRow row(p, n_tile, tile - n_tile * m_tiles, TT, wd & 3, lane);
+        const GatedRow row(p, n_tile, tile - n_tile * m_tiles, TT, wd & 3, lane, gated_down<FMT, BITS>());
 #pragma unroll 1
         for (int c = 1 + g; c < row.chunks; c += 1 + NG) {
           uint32_t r16[16];

@@ -129,17 +129,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // encoding is host time on every call's critical path.
 struct TmapKey {
   const void *base;
-  uint64_t inner, outer, row_bytes;
+  uint64_t inner, outer, row_bytes, planes, plane_bytes;
   uint32_t box_inner, box_outer;
   int dt, sw;
   bool operator==(const TmapKey &o) const {
-    return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes &&
-           box_inner == o.box_inner && box_outer == o.box_outer && dt == o.dt && sw == o.sw;
+    return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes && planes == o.planes &&
+           plane_bytes == o.plane_bytes && box_inner == o.box_inner && box_outer == o.box_outer && dt == o.dt &&
+           sw == o.sw;
   }
 };
 
-bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
-               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+// planes = 0: rows of `inner` elements, boxes of box_outer rows.  Otherwise a third dimension of `planes` such
+// matrices plane_bytes apart, of which a box takes all.
+bool encode(CUtensorMap *map, const TmapKey &key) {
   constexpr int kEntries = 32;
   struct Entry {
     TmapKey key;
@@ -148,7 +150,6 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint6
   };
   static thread_local Entry cache[kEntries] = {};
   static thread_local int next = 0;
-  const TmapKey key{base, inner, outer, row_bytes, box_inner, box_outer, (int)dt, (int)sw};
   for (int i = 0; i < kEntries; ++i)
     if (cache[i].valid && cache[i].key == key) {
       *map = cache[i].map;
@@ -156,16 +157,22 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint6
     }
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  if (fn(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  cuuint64_t dims[3] = {key.inner, key.outer, key.planes};
+  cuuint64_t strides[2] = {key.row_bytes, key.plane_bytes};
+  cuuint32_t box[3] = {key.box_inner, key.box_outer, (cuuint32_t)key.planes};
+  cuuint32_t estr[3] = {1, 1, 1};
+  if (fn(map, (CUtensorMapDataType)key.dt, key.planes ? 3 : 2, const_cast<void *>(key.base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, (CUtensorMapSwizzle)key.sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   cache[next] = Entry{key, *map, true};
   next = (next + 1) % kEntries;
   return true;
+}
+
+bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
+               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+  return encode(map, TmapKey{base, inner, outer, row_bytes, 0, 0, box_inner, box_outer, (int)dt, (int)sw});
 }
 
 // Row tiles of the GEMM: 128 rows, or 64 features of the gated form (64 gate rows and 64 up rows).
@@ -224,11 +231,17 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cuda_failed();
   // int6 planar: a k-step's codes are three 16-byte pieces of its super-block (two of the low plane,
-  // one of the high plane), loaded as three boxes of 16 bytes x BN rows
-  if (!encode_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, row_bytes, (uint64_t)N, row_bytes,
-                 FMT == FMT_INT6P ? 16u : (uint32_t)p_row_bytes(FMT, BITS), GATED ? GATED_F : BN,
-                 CU_TENSOR_MAP_SWIZZLE_NONE))
-    return cuda_failed();
+  // one of the high plane), loaded as three boxes of 16 bytes x BN rows; gated: boxes of the gate rows and the
+  // up rows of 64 features, the layer's rows as two planes of F
+  TmapKey kc{w->codes, row_bytes, (uint64_t)N, row_bytes, 0, 0, FMT == FMT_INT6P ? 16u : (uint32_t)p_row_bytes(FMT, BITS),
+             BN, (int)CU_TENSOR_MAP_DATA_TYPE_UINT8, (int)CU_TENSOR_MAP_SWIZZLE_NONE};
+  if (GATED) {
+    kc.outer = (uint64_t)N / 2;
+    kc.planes = 2;
+    kc.plane_bytes = row_bytes * ((uint64_t)N / 2);
+    kc.box_outer = GATED_F;
+  }
+  if (!encode(&mc, kc)) return cuda_failed();
   Params p;
   p.M = M; p.N = N; p.K = K; p.G = d->group;
   p.bias = static_cast<const __nv_bfloat16 *>(bias);
