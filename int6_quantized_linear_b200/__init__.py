@@ -10,6 +10,7 @@ is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass
 
@@ -290,31 +291,47 @@ def qlinear_gemm_noalloc(desc: Desc, codes, gmeta, steps, x, M: int, y, stream=N
 # ---- gated feed-forward block, 8-bit checkpoints, input gradients ------------------------------------------
 # These calls check their tensors before the library sees a pointer: contiguous CUDA tensors of one device, of
 # the type and at least the size that the call reads or writes.  They run on that device (also when it is not
-# the current one), on its current stream or on `stream`.
+# the current one), on its current stream or on `stream`.  A decode step is a few microseconds of GPU time, so
+# what depends on the layer and M alone is worked out once.
 
-def _need(where: str, t, dtype, numel: int, dev=None):
-    """Check one tensor and return its device."""
-    if not t.is_cuda or (dev is not None and t.device != dev):
+def _refuse(where: str, t, dtype, numel: int):
+    if t is None:
+        raise QLinearError(QL_ERR_NULL, where)
+    if not t.is_cuda or (t.dtype == dtype and t.is_contiguous() and t.numel() >= numel):
         raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: tensors must be on one CUDA device")
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
-        raise QLinearError(QL_ERR_SHAPE, f"{where}: expected a contiguous {dtype} tensor of at least {numel} "
-                                         f"elements, got {t.dtype} of shape {tuple(t.shape)}")
-    return t.device
+    raise QLinearError(QL_ERR_SHAPE, f"{where}: expected a contiguous {dtype} tensor of at least {numel} elements, "
+                                     f"got {t.dtype} of shape {tuple(t.shape)}")
 
 
-def _need_bytes(where: str, t, nbytes: int, dev):
-    if not t.is_cuda or t.device != dev:
+def _ptr_of(where: str, t, dtype, numel: int, dev: int) -> int:
+    """The address of a contiguous CUDA tensor of the given type, size and device; anything else is refused."""
+    if t is None or t.dtype != dtype or t.numel() < numel or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(where, t, dtype, numel)
+    return t.data_ptr()
+
+
+def _device_of(where: str, t) -> int:
+    if t is None or not t.is_cuda:
+        raise QLinearError(QL_ERR_NULL if t is None else QL_ERR_UNSUPPORTED, f"{where}: tensors must be on one CUDA device")
+    return t.get_device()
+
+
+def _buffer_of(where: str, t, nbytes: int, dev: int) -> int:
+    """The address of a contiguous CUDA buffer of any type with at least nbytes bytes (0: an unused one)."""
+    if nbytes == 0:
+        return 0 if t is None else t.data_ptr()
+    if t is None:
+        raise QLinearError(QL_ERR_NULL, where)
+    if t.get_device() != dev:
         raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: tensors must be on one CUDA device")
-    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+    if t.nbytes < nbytes or not t.is_contiguous():
         raise QLinearError(QL_ERR_SHAPE, f"{where}: expected a contiguous buffer of at least {nbytes} bytes")
+    return t.data_ptr()
 
 
-def _need_packed(where: str, desc: Desc, packed, dev):
-    for t, n in zip(packed, qlinear_packed_bytes(desc)):
-        if n:
-            if t is None:
-                raise QLinearError(QL_ERR_NULL, where)
-            _need_bytes(where, t, n, dev)
+def _packed_of(where: str, sizes, codes, gmeta, steps, dev: int) -> ql_packed:
+    return ql_packed(_buffer_of(where, codes, sizes[0], dev), _buffer_of(where, gmeta, sizes[1], dev),
+                     _buffer_of(where, steps, sizes[2], dev))
 
 
 def _activation(where: str, act: str) -> int:
@@ -324,80 +341,91 @@ def _activation(where: str, act: str) -> int:
     return a
 
 
-def _workspace(workspace, nbytes: int, dev, stream, where: str):
-    """The caller's workspace, checked, or one from the pool that torch's allocator keeps for the call's stream (so
-    that it is handed on only to work behind this call's)."""
-    import torch
-    if workspace is not None:
-        _need_bytes(where, workspace, nbytes, dev)
-        return workspace
-    with torch.cuda.stream(stream):  # None: the current one
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-
-
-def _run(where: str, dev, stream, name: str, *args):
-    import torch
-    if stream is not None and stream.device != dev:
-        raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: the stream belongs to another device than the tensors")
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        _check(f(*args, C.c_void_p(s.cuda_stream)), where)
-    else:
-        with torch.cuda.device(dev):
-            _check(f(*args, C.c_void_p(s.cuda_stream)), where)
-
-
-def _bytes2(name: str, *args):
-    a, b = C.c_size_t(), C.c_size_t()
-    _check(getattr(lib(), name)(*args, C.byref(a), C.byref(b)), name)
-    return a.value, b.value
-
-
 def _bytes_for(name: str, desc: Desc, M: int) -> int:
     d, n = desc.c(), C.c_size_t()
     _check(getattr(lib(), name)(C.byref(d), M, C.byref(n)), name)
     return n.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _layer_plan(bytes_name: str, desc: Desc, M: int):
+    """(C descriptor, its reference, packed sizes, workspace bytes) of a layer at M tokens."""
+    need = _bytes_for(bytes_name, desc, M)
+    d = desc.c()
+    return d, C.byref(d), qlinear_packed_bytes(desc), need
+
+
+@functools.lru_cache(maxsize=4096)
+def _saved8_sizes(rows: int, cols: int):
+    c, e = C.c_size_t(), C.c_size_t()
+    _check(lib().qlinear_saved8_bytes(rows, cols, C.byref(c), C.byref(e)), "qlinear_saved8_bytes")
+    return c.value, e.value
+
+
+def _workspace_of(where: str, workspace, nbytes: int, dev: int, stream):
+    """(tensor, address) of the caller's workspace, checked, or of one from the pool that torch's allocator keeps for
+    the call's stream (so that it is handed on only to work behind this call's)."""
+    import torch
+    if workspace is None:
+        with torch.cuda.stream(stream):  # None: the current one
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    return workspace, _buffer_of(where, workspace, nbytes, dev)
+
+
+def _run(where: str, dev: int, stream, f, *args):
+    import torch
+    if stream is None:
+        s = torch.cuda.current_stream(dev)
+    elif stream.device.index == dev:
+        s = stream
+    else:
+        raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: the stream belongs to another device than the tensors")
+    if torch.cuda.current_device() == dev:
+        status = f(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, s.cuda_stream)
+    if status:
+        raise QLinearError(status, where)
+
+
 def qlinear_saved8_bytes(rows: int, cols: int):
     """Bytes of (codes, exps) of a [rows][cols] matrix in 8 bits."""
-    return _bytes2("qlinear_saved8_bytes", rows, cols)
+    return _saved8_sizes(rows, cols)
 
 
 def alloc_saved8(rows: int, cols: int, device="cuda"):
     """Allocate (uninitialised) buffers of a [rows][cols] matrix in 8 bits: codes int8 [rows][cols rounded up to
     16] and exps uint8 [rows][that / 16].  A gated block's checkpoint has rows = 2 M, cols = F."""
     import torch
-    c, e = qlinear_saved8_bytes(rows, cols)
+    c, e = _saved8_sizes(rows, cols)
     return (torch.empty((rows, c // rows), dtype=torch.int8, device=device),
             torch.empty((rows, e // rows), dtype=torch.uint8, device=device))
 
 
-def _need_saved8(where: str, saved, rows: int, cols: int, dev) -> ql_saved8:
+def _saved8_of(where: str, saved, rows: int, cols: int, dev: int) -> ql_saved8:
     import torch
-    c, e = qlinear_saved8_bytes(rows, cols)
-    _need(where, saved[0], torch.int8, c, dev)
-    _need(where, saved[1], torch.uint8, e, dev)
-    return ql_saved8(saved[0].data_ptr(), saved[1].data_ptr())
+    c, e = _saved8_sizes(rows, cols)
+    return ql_saved8(_ptr_of(where, saved[0], torch.int8, c, dev), _ptr_of(where, saved[1], torch.uint8, e, dev))
 
 
 def qlinear_save8(x, rows: int, cols: int, saved, stream=None):
     """bf16 [rows][cols] -> its 8-bit form in ``saved`` = (codes, exps) of alloc_saved8()."""
     import torch
     w = "qlinear_save8"
-    dev = _need(w, x, torch.bfloat16, rows * cols)
-    s = _need_saved8(w, saved, rows, cols, dev)
-    _run(w, dev, stream, w, _ptr(x), rows, cols, C.byref(s))
+    dev = _device_of(w, x)
+    s = _saved8_of(w, saved, rows, cols, dev)
+    _run(w, dev, stream, lib().qlinear_save8, _ptr_of(w, x, torch.bfloat16, rows * cols, dev), rows, cols, C.byref(s))
 
 
 def qlinear_restore8(saved, rows: int, cols: int, out, stream=None):
     """The 8-bit form -> bf16 [rows][cols]."""
     import torch
     w = "qlinear_restore8"
-    dev = _need(w, out, torch.bfloat16, rows * cols)
-    s = _need_saved8(w, saved, rows, cols, dev)
-    _run(w, dev, stream, w, C.byref(s), rows, cols, _ptr(out))
+    dev = _device_of(w, out)
+    s = _saved8_of(w, saved, rows, cols, dev)
+    _run(w, dev, stream, lib().qlinear_restore8, C.byref(s), rows, cols,
+         _ptr_of(w, out, torch.bfloat16, rows * cols, dev))
 
 
 def qlinear_gated_workspace_bytes(desc: Desc, M: int) -> int:
@@ -416,17 +444,14 @@ def qlinear_gated(desc: Desc, codes, gmeta, steps, x, M: int, act: str, h, saved
     qlinear_gated_workspace_bytes(desc, M) bytes; allocated here when omitted."""
     import torch
     w = "qlinear_gated"
-    need = qlinear_gated_workspace_bytes(desc, M)
-    a = _activation(w, act)
-    F = desc.N // 2
-    dev = _need(w, x, torch.bfloat16, M * desc.K)
-    _need(w, h, torch.bfloat16, M * F, dev)
-    _need_packed(w, desc, (codes, gmeta, steps), dev)
-    s = None if saved is None else C.byref(_need_saved8(w, saved, 2 * M, F, dev))
-    workspace = _workspace(workspace, need, dev, stream, w)
-    d, p = desc.c(), ql_packed(_ptr(codes), _ptr(gmeta), _ptr(steps))
-    _run(w, dev, stream, w, C.byref(d), C.byref(p), _ptr(x), M, a, _ptr(h), s, _ptr(workspace),
-         workspace.numel() * workspace.element_size())
+    _, d, sizes, need = _layer_plan("qlinear_gated_workspace_bytes", desc, M)
+    a, F, bf16 = _activation(w, act), desc.N // 2, torch.bfloat16
+    dev = _device_of(w, x)
+    xp, hp = _ptr_of(w, x, bf16, M * desc.K, dev), _ptr_of(w, h, bf16, M * F, dev)
+    p = _packed_of(w, sizes, codes, gmeta, steps, dev)
+    s = None if saved is None else C.byref(_saved8_of(w, saved, 2 * M, F, dev))
+    workspace, wp = _workspace_of(w, workspace, need, dev, stream)
+    _run(w, dev, stream, lib().qlinear_gated, d, C.byref(p), xp, M, a, hp, s, wp, need)
 
 
 def qlinear_gemm_dx_workspace_bytes(desc: Desc, M: int) -> int:
@@ -444,14 +469,12 @@ def qlinear_gemm_dx(desc: Desc, codes, gmeta, steps, dy, M: int, dx, workspace=N
     qlinear_gemm_dx_workspace_bytes(desc, M) bytes; allocated here when omitted."""
     import torch
     w = "qlinear_gemm_dx"
-    need = qlinear_gemm_dx_workspace_bytes(desc, M)
-    dev = _need(w, dy, torch.bfloat16, M * desc.N)
-    _need(w, dx, torch.bfloat16, M * desc.K, dev)
-    _need_packed(w, desc, (codes, gmeta, steps), dev)
-    workspace = _workspace(workspace, need, dev, stream, w)
-    d, p = desc.c(), ql_packed(_ptr(codes), _ptr(gmeta), _ptr(steps))
-    _run(w, dev, stream, w, C.byref(d), C.byref(p), _ptr(dy), M, _ptr(dx), _ptr(workspace),
-         workspace.numel() * workspace.element_size())
+    _, d, sizes, need = _layer_plan("qlinear_gemm_dx_workspace_bytes", desc, M)
+    dev, bf16 = _device_of(w, dy), torch.bfloat16
+    yp, xp = _ptr_of(w, dy, bf16, M * desc.N, dev), _ptr_of(w, dx, bf16, M * desc.K, dev)
+    p = _packed_of(w, sizes, codes, gmeta, steps, dev)
+    workspace, wp = _workspace_of(w, workspace, need, dev, stream)
+    _run(w, dev, stream, lib().qlinear_gemm_dx, d, C.byref(p), yp, M, xp, wp, need)
 
 
 def qlinear_gated_backward(desc: Desc, codes, gmeta, steps, saved, dh, M: int, act: str, dx, dgu=None,
@@ -460,21 +483,17 @@ def qlinear_gated_backward(desc: Desc, codes, gmeta, steps, saved, dh, M: int, a
     (dg | du) in ``dgu`` [M][2 F] when given.  ``workspace``: as qlinear_gemm_dx."""
     import torch
     w = "qlinear_gated_backward"
-    need = qlinear_gemm_dx_workspace_bytes(desc, M)
-    a = _activation(w, act)
-    F = desc.N // 2
-    if F < 1:
-        raise QLinearError(QL_ERR_SHAPE, w)
-    dev = _need(w, dh, torch.bfloat16, M * F)
-    _need(w, dx, torch.bfloat16, M * desc.K, dev)
-    if dgu is not None:
-        _need(w, dgu, torch.bfloat16, M * desc.N, dev)
-    _need_packed(w, desc, (codes, gmeta, steps), dev)
-    s = _need_saved8(w, saved, 2 * M, F, dev)
-    workspace = _workspace(workspace, need, dev, stream, w)
-    d, p = desc.c(), ql_packed(_ptr(codes), _ptr(gmeta), _ptr(steps))
-    _run(w, dev, stream, w, C.byref(d), C.byref(p), C.byref(s), _ptr(dh), M, a, _ptr(dgu), _ptr(dx),
-         _ptr(workspace), workspace.numel() * workspace.element_size())
+    if desc.N % 2:
+        raise QLinearError(QL_ERR_SHAPE, f"{w}: the layer has an odd number of rows")
+    _, d, sizes, need = _layer_plan("qlinear_gemm_dx_workspace_bytes", desc, M)
+    a, F, bf16 = _activation(w, act), desc.N // 2, torch.bfloat16
+    dev = _device_of(w, dh)
+    hp, xp = _ptr_of(w, dh, bf16, M * F, dev), _ptr_of(w, dx, bf16, M * desc.K, dev)
+    gp = None if dgu is None else _ptr_of(w, dgu, bf16, M * desc.N, dev)
+    p = _packed_of(w, sizes, codes, gmeta, steps, dev)
+    s = _saved8_of(w, saved, 2 * M, F, dev)
+    workspace, wp = _workspace_of(w, workspace, need, dev, stream)
+    _run(w, dev, stream, lib().qlinear_gated_backward, d, C.byref(p), C.byref(s), hp, M, a, gp, xp, wp, need)
 
 
 def qlinear_set_withhold_copies(on: bool) -> None:

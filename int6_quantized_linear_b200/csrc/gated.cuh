@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) save8_kernel(const __nv_bfloat16 *x, int6
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   if (i >= groups) return;
   const uint4 *src = reinterpret_cast<const uint4 *>(x) + 2 * i;
-  const uint4 a = __ldg(src), b = __ldg(src + 1);
+  const uint4 a = __ldcs(src), b = __ldcs(src + 1);  // read once: what L2 should keep is the codes
   const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t top = 0u;  // the largest magnitude's bf16 bits (magnitudes order like their bits)
 #pragma unroll
@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(256) restore8_kernel(const int8_t *codes, cons
     o[2 * j + 1] = pack_bf16x2((float)(int8_t)(u[j] >> 16) * s, (float)(int8_t)(u[j] >> 24) * s);
   }
   uint4 *dst = reinterpret_cast<uint4 *>(out) + 2 * i;
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+  __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
 }
 
 // Rows of any length: their values start at any 2-byte boundary, so 16 lanes take a group, one value

@@ -99,13 +99,13 @@ inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
 // With few tokens pass 2 has few CTAs, and passes 2 and 3 run side by side.
 
 // ---- pass 1: row exponents ------------------------------------------------------------------------
-// One warp a row.  The bound on a row's weights need not be tight -- a looser one only moves the fp16 weights
+// Eight lanes a row.  The bound on a row's weights need not be tight -- a looser one only moves the fp16 weights
 // down, and they have 2^29 of range below the top -- so int4 and int6 take it from the steps alone: codes of
 // 255 (int6: -128) times the step.
 //
 // The row factor 2^(DY_BIAS - b_n) that multiplies dy is kept as its exponent byte; the bias brings the
 // factor of ordinary weights (b_n about -4) near 1, so that dy times it stays in range whenever dy does.
-constexpr int DY_BIAS = -4, RE_WARPS = 8;
+constexpr int DY_BIAS = -4, RE_ROWS = 32, RE_THREADS = 8 * RE_ROWS;
 // the exponent that a row's bound gets: the largest scale, at most bound / 15 (int4), bound / 32 (int6) or
 // 2 bound / (2^bits - 1) (affine), times 2^24 has to stay below 65504
 __host__ __device__ constexpr int w_top(int fmt, int bits) {
@@ -128,23 +128,23 @@ QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, 
 }
 
 template <int FMT, int BITS>
-__global__ void __launch_bounds__(32 * RE_WARPS) row_exp_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
-                                                                int64_t K, int G, Workspace ws) {
-  const int lane = threadIdx.x & 31;
-  const int64_t n = (int64_t)blockIdx.x * RE_WARPS + (threadIdx.x >> 5);  // < Np
+__global__ void __launch_bounds__(RE_THREADS) row_exp_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
+                                                             int64_t K, int G, Workspace ws) {
+  const int sub = threadIdx.x & 7;
+  const int64_t n = (int64_t)blockIdx.x * RE_ROWS + (threadIdx.x >> 3);  // < Np
   const int64_t words = FMT == FMT_AFFINE ? K / G : K / 256;
   pdl_wait();
   pdl_launch_dependents();
   float top = 0.f;
   if (n < N) {
-#pragma unroll 4
-    for (int64_t i = lane; i < words; i += 32) top = fmaxf(top, meta_bound<FMT, BITS>(gmeta, steps, n, i, K, G));
+#pragma unroll 8
+    for (int64_t i = sub; i < words; i += 8) top = fmaxf(top, meta_bound<FMT, BITS>(gmeta, steps, n, i, K, G));
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   // at most 120, so that 127 + DY_BIAS - b is an exponent byte (weights below 2^-126 lose bits then)
   const int b = n < N ? min(scale_exponent(top, w_top(FMT, BITS)), 120) : DY_BIAS;
-  if (lane == 0) ws.rowexp[n] = (uint8_t)(127 + DY_BIAS - b);
+  if (sub == 0) ws.rowexp[n] = (uint8_t)(127 + DY_BIAS - b);
 }
 
 // ---- pass 2: dy (or (dg | du)) to scaled fp16 rows ----------------------------------------------------
@@ -194,10 +194,12 @@ QL_DEVI void unpack8(uint4 q, float (&v)[8]) {
   }
 }
 
-constexpr int DY_THREADS = 256, DY_REGS = 4;
+constexpr int DY_REGS = 4;
+// threads a row: with 256 rows of up to 8192 stay in registers, with 1024 rows of up to 32768
+inline int dy_threads(int64_t N) { return N <= 8 * DY_REGS * 256 ? 256 : 1024; }
 
-// Rows of up to DY_REGS * DY_THREADS vectors of 8 are read once and kept; longer rows are read again.
-template <bool VEC>
+// Rows of up to DY_REGS vectors of 8 a thread are read once and kept; longer rows are read again.
+template <int DY_THREADS, bool VEC>
 __global__ void __launch_bounds__(DY_THREADS) dy_prep_kernel(const __nv_bfloat16 *dy, int64_t N, int64_t np,
                                                              Workspace ws) {
   __shared__ float red[DY_THREADS / 32];
@@ -267,95 +269,94 @@ struct GatedGrad {
   int64_t F, np;
 };
 
-constexpr int DGU_THREADS = 256;
 constexpr float MAX_SLOPE = 1.13f;  // of the activations; |act(g)| <= |g|
 
-// 16 exponent bytes of rows n .. n + 15 (bytes from `end` on as zeros).  VEC: n is a multiple of 16.
+// Eight exponent bytes of rows n .. n + 7 (bytes from `end` on as zeros).  VEC: n is a multiple of 8.
 template <bool VEC>
-QL_DEVI uint4 load_rowexp(const uint8_t *e, int64_t n, int64_t end) {
+QL_DEVI uint2 load_rowexp(const uint8_t *e, int64_t n, int64_t end) {
   if constexpr (VEC) {
-    return *reinterpret_cast<const uint4 *>(e + n);
+    return *reinterpret_cast<const uint2 *>(e + n);
   } else {
-    uint32_t u[4] = {0u, 0u, 0u, 0u};
+    uint32_t u[2] = {0u, 0u};
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < 8; ++j)
       if (n + j < end) u[j >> 2] |= (uint32_t)e[n + j] << (8 * (j & 3));
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    return make_uint2(u[0], u[1]);
   }
 }
 
-QL_DEVI uint32_t max_byte(uint4 v) {
-  uint32_t m = __vmaxu4(__vmaxu4(v.x, v.y), __vmaxu4(v.z, v.w));
+QL_DEVI uint32_t max_byte(uint2 v) {
+  uint32_t m = __vmaxu4(v.x, v.y);
   m = __vmaxu4(m, m >> 16);
   return max(m & 0xFFu, (m >> 8) & 0xFFu);
 }
 
-// Sixteen 16-bit values -> row elements n .. n + 15 (those below `end`).  VEC: 16-byte aligned, all of them.
+// Eight 16-bit values -> row elements n .. n + 7 (those below `end`).  VEC: 16-byte aligned, all of them.
 template <bool VEC>
-QL_DEVI void store16(void *row, int64_t n, int64_t end, const uint32_t (&o)[8]) {
+QL_DEVI void store8(void *row, int64_t n, int64_t end, const uint32_t (&o)[4]) {
   uint16_t *dst = static_cast<uint16_t *>(row) + n;
   if constexpr (VEC) {
-    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < 8; ++j)
       if (n + j < end) dst[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
   }
 }
 
-// A thread takes one group of 16 features at a time.  The row's scale comes from a bound that needs no
-// activation -- the group's largest |dh| times 127 steps of u (slope at most 1.13) or of g -- so every
+// A thread takes eight features (half a group of the checkpoint) at a time.  The row's scale comes from a bound that
+// needs no activation -- the eight's largest |dh| times 127 steps of u (slope at most 1.13) or of g -- so every
 // gradient is computed once; the bound's slack costs a few of the 29 powers of two that fp16 has below its
-// top.  Bound by instruction issue; the int8 codes become floats by a byte permute and one FMA.
-template <int ACT, bool VEC>
-__global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Workspace ws) {
-  __shared__ float red[DGU_THREADS / 32];
+// top.  The int8 codes become floats by a byte permute and one FMA.  VEC: F % 8 == 0.
+template <int ACT, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS) dgu_prep_kernel(GatedGrad p, Workspace ws) {
+  __shared__ float red[THREADS / 32];
   const int64_t m = blockIdx.x, N = 2 * p.F, fp = save8_cols(p.F);
-  const int groups = (int)(fp / 16);
+  const int units = (int)((p.F + 7) / 8);
   const __nv_bfloat16 *dh = p.dh + m * p.F;
-  const uint4 *cg = reinterpret_cast<const uint4 *>(p.codes + 2 * m * fp), *cu = cg + groups;
-  const uint8_t *eg = p.exps + 2 * m * groups, *eu = eg + groups;
+  const uint2 *cg = reinterpret_cast<const uint2 *>(p.codes + 2 * m * fp), *cu = cg + fp / 8;
+  const uint8_t *eg = p.exps + 2 * m * (fp / 16), *eu = eg + fp / 16;
   float top = 0.f;
   pdl_wait();  // the row exponents
   pdl_launch_dependents();
-  for (int i = threadIdx.x; i < groups; i += DGU_THREADS) {
-    const int64_t f = 16 * (int64_t)i;
-    const uint4 d0 = load8<VEC>(dh, f, p.F), d1 = load8<VEC>(dh, f + 8, p.F);
-    const uint4 rg = load_rowexp<VEC>(ws.rowexp, f, p.F), ru = load_rowexp<VEC>(ws.rowexp + p.F, f, p.F);
-    const float sg = save8_scale(__ldg(eg + i)), su = save8_scale(__ldg(eu + i));
-    const float dm = chunk_amax(d1, chunk_amax(d0, 0.f)) * 127.f;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < units; i += THREADS) {
+    const int64_t f = 8 * (int64_t)i;
+    const float dm = chunk_amax(load8<VEC>(dh, f, p.F), 0.f) * 127.f;
+    const uint2 rg = load_rowexp<VEC>(ws.rowexp, f, p.F), ru = load_rowexp<VEC>(ws.rowexp + p.F, f, p.F);
+    const float sg = save8_scale(__ldg(eg + (i >> 1))), su = save8_scale(__ldg(eu + (i >> 1)));
     top = fmaxf(top, dm * su * (MAX_SLOPE * __uint_as_float(max_byte(rg) << 23)));
     top = fmaxf(top, dm * sg * __uint_as_float(max_byte(ru) << 23));
   }
-  const int a = scale_exponent(block_max<DGU_THREADS>(top, red), 14);
+  const int a = scale_exponent(block_max<THREADS>(top, red), 14);
   const float sc = exp2i(a);
   __half *out = ws.dy16 + m * p.np;
-  for (int i = threadIdx.x; i < groups; i += DGU_THREADS) {
-    const int64_t f = 16 * (int64_t)i;
-    const uint4 d0 = load8<VEC>(dh, f, p.F), d1 = load8<VEC>(dh, f + 8, p.F);
-    const uint4 qg = __ldg(cg + i), qu = __ldg(cu + i);
-    const uint4 rg = load_rowexp<VEC>(ws.rowexp, f, p.F), ru = load_rowexp<VEC>(ws.rowexp + p.F, f, p.F);
-    const float sg = save8_scale(__ldg(eg + i)), su = save8_scale(__ldg(eu + i));
-    const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-    const uint32_t gw[4] = {qg.x, qg.y, qg.z, qg.w}, uw[4] = {qu.x, qu.y, qu.z, qu.w};
-    const uint32_t fg[4] = {rg.x, rg.y, rg.z, rg.w}, fu[4] = {ru.x, ru.y, ru.z, ru.w};
+#pragma unroll 1
+  for (int i = threadIdx.x; i < units; i += THREADS) {
+    const int64_t f = 8 * (int64_t)i;
+    const uint4 d = load8<VEC>(dh, f, p.F);
+    const uint2 qg = __ldg(cg + i), qu = __ldg(cu + i);
+    const uint2 rg = load_rowexp<VEC>(ws.rowexp, f, p.F), ru = load_rowexp<VEC>(ws.rowexp + p.F, f, p.F);
+    const float sg = save8_scale(__ldg(eg + (i >> 1))), su = save8_scale(__ldg(eu + (i >> 1)));
+    const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+    const uint32_t gw[2] = {qg.x ^ 0x80808080u, qg.y ^ 0x80808080u}, uw[2] = {qu.x ^ 0x80808080u, qu.y ^ 0x80808080u};
+    const uint32_t fg[2] = {rg.x, rg.y}, fu[2] = {ru.x, ru.y};
     // code c as the byte c + 128 in the mantissa of 2^23: value = (2^23 + 128 + c) s - (2^23 + 128) s, exact
     const float zg = -8388736.f * sg, zu = -8388736.f * su;
-    uint32_t og[8], ou[8], bg[8], bu[8];
+    uint32_t og[4], ou[4], bg[4], bu[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       float dgv[2], duv[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int e = 2 * j + h;
-        const float d = h ? __uint_as_float(dw[j] & 0xffff0000u) : __uint_as_float(dw[j] << 16);
-        const float g = fmaf(byte_of(gw[e >> 2] ^ 0x80808080u, e & 3), sg, zg);
-        const float u = fmaf(byte_of(uw[e >> 2] ^ 0x80808080u, e & 3), su, zu);
+        const float dv = h ? __uint_as_float(dw[j] & 0xffff0000u) : __uint_as_float(dw[j] << 16);
+        const float g = fmaf(byte_of(gw[e >> 2], e & 3), sg, zg);
+        const float u = fmaf(byte_of(uw[e >> 2], e & 3), su, zu);
         float av, ad;
         act_grad(ACT, g, av, ad);
-        dgv[h] = d * u * ad;
-        duv[h] = d * av;
+        dgv[h] = dv * u * ad;
+        duv[h] = dv * av;
       }
       if (p.dgu) {
         bg[j] = pack_bf16x2(dgv[0], dgv[1]);
@@ -365,11 +366,11 @@ __global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Work
       og[j] = pack_f16x2(dgv[0] * row_factor(fg[e >> 2], e & 3) * sc, dgv[1] * row_factor(fg[e >> 2], (e & 3) + 1) * sc);
       ou[j] = pack_f16x2(duv[0] * row_factor(fu[e >> 2], e & 3) * sc, duv[1] * row_factor(fu[e >> 2], (e & 3) + 1) * sc);
     }
-    store16<VEC>(out, f, p.F, og);
-    store16<VEC>(out + p.F, f, p.F, ou);
+    store8<VEC>(out, f, p.F, og);
+    store8<VEC>(out + p.F, f, p.F, ou);
     if (p.dgu) {
-      store16<VEC>(p.dgu + m * N, f, p.F, bg);
-      store16<VEC>(p.dgu + m * N + p.F, f, p.F, bu);
+      store8<VEC>(p.dgu + m * N, f, p.F, bg);
+      store8<VEC>(p.dgu + m * N + p.F, f, p.F, bu);
     }
   }
   if (threadIdx.x < p.np - N) out[N + threadIdx.x] = __float2half_rn(0.f);
@@ -377,22 +378,18 @@ __global__ void __launch_bounds__(DGU_THREADS) dgu_prep_kernel(GatedGrad p, Work
 }
 
 // ---- pass 3: scaled metadata, transposed ------------------------------------------------------------
-// The metadata of run r (of gran weights) of row n: the scales times 2^24 sc, -Z S and b times sc = 2^b_n.
+// The metadata of a run (of gran weights) from its group word c and its super-block's step word s: the scales times
+// 2^24 sc, -Z S and b times sc = 2^b_n.
 constexpr float SUB = 16777216.f;  // 2^24
 template <int FMT>
-QL_DEVI uint32_t scaled_meta(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t r, int64_t K, int G,
-                             float sc) {
+QL_DEVI uint32_t scaled_meta(uint32_t c, uint32_t s, float sc) {
   if constexpr (FMT == FMT_INT4) {
-    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta) + n * (K / 32) + r);
-    const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3));
     const float S = __fmul_rn((float)(c & 0xffu), f16_bits_to_f32(s)) * sc;
-    return pack_f16x2(S * SUB, -__fmul_rn((float)(c >> 8), f16_bits_to_f32(s >> 16)) * S);
+    return pack_f16x2(S * SUB, -__fmul_rn((float)((c >> 8) & 0xffu), f16_bits_to_f32(s >> 16)) * S);
   } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
-    const uint32_t c = __ldg(reinterpret_cast<const uint16_t *>(gmeta + n * (K / 16)) + r);
-    const float st = f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3)));
+    const float st = f16_bits_to_f32(s);
     return pack_f16x2(__fmul_rn((float)(int8_t)c, st) * sc * SUB, __fmul_rn((float)(int8_t)(c >> 8), st) * sc * SUB);
   } else {
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G) + r);
     return pack_f16x2(bf16_bits_to_f32(c) * sc * SUB, bf16_bits_to_f32(c >> 16) * sc);
   }
 }
@@ -406,15 +403,31 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS, r0 = (int64_t)blockIdx.y * WP_RUNS, runs = K / gran(FMT, G);
   pdl_launch_dependents();
+  // a lane takes runs 2 l and 2 l + 1 of its row: one word of 16-bit group words (int4, int6), two of affine
+  const int64_t r = r0 + 2 * lane;
+  uint32_t c[RW][2], st[RW];
 #pragma unroll
   for (int j = 0; j < RW; ++j) {
     const int64_t n = n0 + RW * warp + j;
-    const float sc = exp2i(127 + DY_BIAS - (int)ws.rowexp[n]);
-#pragma unroll
-    for (int i = 0; i < WP_RUNS / 32; ++i) {
-      const int64_t r = r0 + 32 * i + lane;
-      turn[RW * warp + j][32 * i + lane] = n < N && r < runs ? scaled_meta<FMT>(gmeta, steps, n, r, K, G, sc) : 0u;
+    c[j][0] = c[j][1] = st[j] = 0u;
+    if (n >= N || r >= runs) continue;
+    if constexpr (FMT == FMT_AFFINE) {
+      const uint32_t *src = reinterpret_cast<const uint32_t *>(gmeta) + n * runs + r;
+      c[j][0] = __ldg(src);
+      if (r + 1 < runs) c[j][1] = __ldg(src + 1);
+    } else {  // K % 256 == 0: eight runs a super-block
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(gmeta + 2 * (n * runs + r)));
+      c[j][0] = w & 0xffffu;
+      c[j][1] = w >> 16;
+      st[j] = FMT == FMT_INT4 ? __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3))
+                              : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3));
     }
+  }
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+    const float sc = exp2i(127 + DY_BIAS - (int)ws.rowexp[n0 + RW * warp + j]);
+    turn[RW * warp + j][2 * lane] = scaled_meta<FMT>(c[j][0], st[j], sc);
+    turn[RW * warp + j][2 * lane + 1] = scaled_meta<FMT>(c[j][1], st[j], sc);
   }
   __syncthreads();
 #pragma unroll

@@ -742,7 +742,7 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
       return cuda_failed();
     configured_dev = dev;
   }
-  if (!launch_dependent(row_exp_kernel<FMT, BITS>, dim3((unsigned)(np / RE_WARPS)), 32 * RE_WARPS, 0, st, gmeta, steps,
+  if (!launch_dependent(row_exp_kernel<FMT, BITS>, dim3((unsigned)(np / RE_ROWS)), RE_THREADS, 0, st, gmeta, steps,
                         N, K, d->group, ws) ||
       !prep(ws, np) ||
       !launch_dependent(meta_kernel<FMT>, dim3((unsigned)(np / WP_ROWS), (unsigned)((K / gr + WP_RUNS - 1) / WP_RUNS)),
@@ -780,6 +780,23 @@ ql_status gemm_dx_call(const ql_desc *d, const ql_packed_const *w, int64_t M, vo
       if (d->bits == 4) return launch_gemm_dx<FMT_AFFINE, 4>(d, w, M, dx_out, workspace, s, sms, prep);
       return launch_gemm_dx<FMT_AFFINE, 8>(d, w, M, dx_out, workspace, s, sms, prep);
   }
+}
+
+// The gated block's pass 2: more threads a row while there are fewer rows than SMs.
+template <int ACT>
+bool launch_dgu_prep_act(const dx::GatedGrad &g, int64_t M, const dx::Workspace &ws, cudaStream_t st) {
+  const bool vec = g.F % 8 == 0;
+  const dim3 grid((unsigned)M);
+  if (M > dx::DX_CTAS)
+    return launch_dependent(vec ? dx::dgu_prep_kernel<ACT, true, 256> : dx::dgu_prep_kernel<ACT, false, 256>, grid, 256,
+                            0, st, g, ws);
+  return launch_dependent(vec ? dx::dgu_prep_kernel<ACT, true, 512> : dx::dgu_prep_kernel<ACT, false, 512>, grid, 512,
+                          0, st, g, ws);
+}
+bool launch_dgu_prep(int act, const dx::GatedGrad &g, int64_t M, const dx::Workspace &ws, cudaStream_t st) {
+  if (act == ACT_SILU) return launch_dgu_prep_act<ACT_SILU>(g, M, ws, st);
+  if (act == ACT_GELU_TANH) return launch_dgu_prep_act<ACT_GELU_TANH>(g, M, ws, st);
+  return launch_dgu_prep_act<ACT_GELU>(g, M, ws, st);
 }
 
 inline size_t gemm_dx_workspace(const ql_desc *d, int64_t M) {
@@ -1268,8 +1285,11 @@ ql_status qlinear_gemm_dx(const ql_desc *d, const ql_packed_const *w, const void
   const int64_t N = d->N;
   const auto *yb = static_cast<const __nv_bfloat16 *>(dy);
   return gemm_dx_call(d, w, M, dx_out, workspace, s, di->sms, [=](const dx::Workspace &ws, int64_t np) {
-    return launch_dependent(N % 8 == 0 ? dx::dy_prep_kernel<true> : dx::dy_prep_kernel<false>, dim3((unsigned)M),
-                            dx::DY_THREADS, 0, s, yb, N, np, ws);
+    const bool vec = N % 8 == 0;
+    const int threads = dx::dy_threads(N);
+    auto *kern = threads == 256 ? (vec ? dx::dy_prep_kernel<256, true> : dx::dy_prep_kernel<256, false>)
+                                : (vec ? dx::dy_prep_kernel<1024, true> : dx::dy_prep_kernel<1024, false>);
+    return launch_dependent(kern, dim3((unsigned)M), threads, 0, s, yb, N, np, ws);
   });
 }
 
@@ -1298,12 +1318,7 @@ ql_status qlinear_gated_backward(const ql_desc *d, const ql_packed_const *w, con
   return gemm_dx_call(d, w, M, dx_out, workspace, s, di->sms, [=](const dx::Workspace &ws, int64_t np) {
     dx::GatedGrad g = g0;
     g.np = np;
-    const bool vec = g.F % 16 == 0;
-    auto *kern = act == ACT_SILU        ? (vec ? dx::dgu_prep_kernel<ACT_SILU, true> : dx::dgu_prep_kernel<ACT_SILU, false>)
-                 : act == ACT_GELU_TANH ? (vec ? dx::dgu_prep_kernel<ACT_GELU_TANH, true>
-                                               : dx::dgu_prep_kernel<ACT_GELU_TANH, false>)
-                                        : (vec ? dx::dgu_prep_kernel<ACT_GELU, true> : dx::dgu_prep_kernel<ACT_GELU, false>);
-    return launch_dependent(kern, dim3((unsigned)M), dx::DGU_THREADS, 0, s, g, ws);
+    return launch_dgu_prep(act, g, M, ws, s);
   });
 }
 
