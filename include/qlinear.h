@@ -456,8 +456,9 @@ ql_status qlinear_gated(const ql_desc *desc, const ql_packed_const *w, const voi
  * qlinear_gated_backward need (host-only, no CUDA call): with Np = N rounded up
  * to 64 and r = 32 (affine: the group), the sum of 2*M*Np (dy in fp16), 4*M,
  * Np, 4*(K/r)*Np (scaled metadata), each rounded up to 256, and 148 * 1024 * T
- * (partial sums), T the tokens of a tile: M spread evenly over ceil(M/C) tiles
- * (C = 32 up to M = 32, 128 up to 128, else 256) and rounded up to 16.
+ * (partial sums; twice that up to M = 64), T the tokens of a tile: M spread
+ * evenly over ceil(M/C) tiles (C = 32 up to M = 32, 64 up to 64, else 256) and
+ * rounded up to 16.
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_RANGE, QL_ERR_UNSUPPORTED. */
 ql_status qlinear_gemm_dx_workspace_bytes(const ql_desc *desc, int64_t M, size_t *bytes);
 

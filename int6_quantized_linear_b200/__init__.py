@@ -372,19 +372,27 @@ def _workspace_of(where: str, workspace, nbytes: int, dev: int, stream):
     return workspace, _buffer_of(where, workspace, nbytes, dev)
 
 
+@functools.lru_cache(maxsize=None)
+def _current_raw_stream():
+    """Device index -> address of its current stream: torch's own short way to it (a microsecond less a call than
+    through a Stream object), or that object where a torch lacks it."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _run(where: str, dev: int, stream, f, *args):
     import torch
     if stream is None:
-        s = torch.cuda.current_stream(dev)
+        s = _current_raw_stream()(dev)
     elif stream.device.index == dev:
-        s = stream
+        s = stream.cuda_stream
     else:
         raise QLinearError(QL_ERR_UNSUPPORTED, f"{where}: the stream belongs to another device than the tensors")
     if torch.cuda.current_device() == dev:
-        status = f(*args, s.cuda_stream)
+        status = f(*args, s)
     else:
         with torch.cuda.device(dev):
-            status = f(*args, s.cuda_stream)
+            status = f(*args, s)
     if status:
         raise QLinearError(status, where)
 

@@ -38,7 +38,7 @@
 //   meta   u32  [K / gran][Np]  scaled metadata of a run of gran weights, two words for each two rows n, n + 1
 //                            of fp16 pairs: their scales, then their offsets (int4 -Z S, affine b; int6 the scales
 //                            of the run's two 16-groups); zeros past N
-//   partial f32 [2 DX_CTAS][tokens a tile][128]
+//   partial f32 [2 DX_CTAS ctas_per_sm][tokens a tile][128]
 #pragma once
 #include "gated.cuh"
 #include "gemm_sm100.cuh"
@@ -48,11 +48,15 @@ namespace dx {
 
 constexpr int BN = 64;    // weight rows a stage (the contraction)
 constexpr int BKT = 128;  // k a tile (the MMA's M)
-constexpr int DX_CTAS = 148;       // CTAs of a launch at most: the SMs of a B200
+constexpr int DX_CTAS = 148;       // SMs a launch uses at most: those of a B200
 constexpr int MIN_SHARE = 8;       // stages a share of a split tile has at least
 // Token tiles: the class (most tokens of a tile, which sizes the rings) and the tokens that a launch's tiles
 // have, a multiple of 16 (the MMA's N) that spreads M evenly.
-constexpr int TT_LARGE = 256, TT_MEDIUM = 128, TT_SMALL = 32;
+constexpr int TT_LARGE = 256, TT_MEDIUM = 64, TT_SMALL = 32;
+// CTAs an SM: the one warp that issues a CTA's MMAs needs about 450 cycles a stage, and up to 64 tokens the MMAs
+// themselves take 230 to 250, so two CTAs share the tensor core (K = 5120, N = 27648, M = 4: 47.7 -> 44.3 us a call,
+// M = 64: 61.0 -> 55.4; at M = 128 one CTA is faster, 67.2 against 75.2).
+__host__ __device__ constexpr int ctas_per_sm(int tt) { return tt == TT_LARGE ? 1 : 2; }
 inline int tile_class(int64_t M) { return M <= TT_SMALL ? TT_SMALL : M <= TT_MEDIUM ? TT_MEDIUM : TT_LARGE; }
 inline int tile_tokens(int64_t M) {
   const int c = tile_class(M);
@@ -74,7 +78,7 @@ struct Workspace {
 inline size_t workspace_bytes(int64_t M, int64_t N, int64_t K, int g) {
   const size_t np = (size_t)padded_n(N);
   return align256((size_t)M * np * 2) + align256((size_t)M * 4) + align256(np) + align256((size_t)(K / g) * np * 4) +
-         (size_t)2 * DX_CTAS * tile_tokens(M) * BKT * 4;
+         (size_t)2 * DX_CTAS * ctas_per_sm(tile_class(M)) * tile_tokens(M) * BKT * 4;
 }
 
 inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
@@ -443,19 +447,22 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
 
 // ---- pass 4: the GEMM ------------------------------------------------------------------------------
 constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_EPI0 = 4, WARP_DEQ0 = 8, NPROD = 3;
-__host__ __device__ constexpr int deq_groups(int tt) { return tt == TT_LARGE ? 2 : 4; }
-__host__ __device__ constexpr int num_threads(int tt) { return (WARP_DEQ0 + 4 * deq_groups(tt)) * 32; }
+constexpr int NG = 2;  // dequantiser groups
+constexpr int NUM_THREADS = (WARP_DEQ0 + 4 * NG) * 32;
 
 // What TMA brings -- the dy tile (B), the packed codes and the metadata words -- waits in a ring as deep as shared
 // memory allows (up to 16): for few tokens the stream of codes bounds the kernel and needs bytes in flight.  The
 // weight tiles (A, 32 columns each) have a ring of up to eight beside the accumulators in tensor memory: two
-// accumulators (an epilogue beside the next tile's MMAs), or one of 256 columns.
+// accumulators (an epilogue beside the next tile's MMAs) of 32 columns, or one of 64 or 256.
 __host__ __device__ constexpr int code_row(int fmt, int bits) { return BKT * gemm::code_bits(fmt, bits) / 8; }
 __host__ __device__ constexpr int b_bytes(int tt) { return tt * BN * 2; }
 __host__ __device__ constexpr int p_bytes(int fmt, int bits) { return BN * code_row(fmt, bits); }
 constexpr int META_BYTES = BN * 4 * 4;  // up to four runs of 32 k
-constexpr uint32_t TMEM_COLS = 512, A_COLS = BN / 2;
-__host__ __device__ constexpr int num_acc(int tt) { return tt == TT_LARGE ? 1 : 2; }
+constexpr uint32_t A_COLS = BN / 2;
+__host__ __device__ constexpr uint32_t tmem_cols(int tt) { return 512u / ctas_per_sm(tt); }
+__host__ __device__ constexpr int num_acc(int tt) { return tt == TT_SMALL ? 2 : 1; }
+// dynamic shared memory of a CTA: an SM's 228 KB less 1 KB a CTA
+__host__ __device__ constexpr int smem_limit(int tt) { return 233472 / ctas_per_sm(tt) - 1024; }
 __host__ __device__ constexpr int stage_bytes(int fmt, int bits, int tt) {
   return b_bytes(tt) + p_bytes(fmt, bits) + META_BYTES;
 }
@@ -464,11 +471,12 @@ __host__ __device__ constexpr int smem_need(int fmt, int bits, int tt, int st) {
 }
 __host__ __device__ constexpr int stages(int fmt, int bits, int tt) {
   int st = 16;
-  while (smem_need(fmt, bits, tt, st) > gemm::SMEM_LIMIT) --st;
+  while (smem_need(fmt, bits, tt, st) > smem_limit(tt)) --st;
   return st;
 }
 __host__ __device__ constexpr int a_stages(int fmt, int bits, int tt) {
-  return stages(fmt, bits, tt) < 8 ? stages(fmt, bits, tt) : 8;
+  const int fit = (int)(tmem_cols(tt) - num_acc(tt) * tt) / (int)A_COLS, st = stages(fmt, bits, tt);
+  return st < fit ? (st < 8 ? st : 8) : (fit < 8 ? fit : 8);
 }
 __host__ __device__ constexpr int smem_bytes(int fmt, int bits, int tt) {
   return smem_need(fmt, bits, tt, stages(fmt, bits, tt));
@@ -485,13 +493,13 @@ struct Deal {
   __host__ __device__ int64_t share_begin(int c) const { return (int64_t)rest * steps * c / shares; }
 };
 
-inline Deal deal(int64_t M, int64_t N, int64_t K, int sms) {
+inline Deal deal(int64_t M, int64_t N, int64_t K, int sms) {  // the tile class is M's
   Deal d;
   d.tokens = tile_tokens(M);
   d.m_tiles = (M + d.tokens - 1) / d.tokens;
   d.k_tiles = (K + BKT - 1) / BKT;
   d.steps = (int)(padded_n(N) / BN);
-  d.ctas = sms < DX_CTAS ? sms : DX_CTAS;
+  d.ctas = (sms < DX_CTAS ? sms : DX_CTAS) * ctas_per_sm(tile_class(M));
   const int64_t tiles = d.m_tiles * d.k_tiles;
   d.waves = (int)(tiles / d.ctas);
   d.rest = (int)(tiles % d.ctas);
@@ -694,11 +702,11 @@ QL_DEVI void decode_stage(uint32_t codes, uint32_t meta, int wq, int lane, uint3
 // Warp roles: 0, 2 and 3 TMA producers, 1 tensor memory and MMA issue, 4-7 epilogue (one k a lane), 8..
 // dequantisers in groups of four warps (one a quarter of the TMEM lanes) that take the stages in turn.
 template <int FMT, int BITS, int TT>
-__global__ void __launch_bounds__(num_threads(TT), 1)
+__global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
     gemm_dx_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_codes,
                    const __grid_constant__ CUtensorMap map_codes_hi, const __grid_constant__ CUtensorMap map_meta,
                    Params p) {
-  constexpr int STAGES = stages(FMT, BITS, TT), AST = a_stages(FMT, BITS, TT), NG = deq_groups(TT);
+  constexpr int STAGES = stages(FMT, BITS, TT), AST = a_stages(FMT, BITS, TT);
   constexpr int NACC = num_acc(TT);
   constexpr int PROW = code_row(FMT, BITS);
   constexpr int OFF_P = b_bytes(TT), OFF_M = OFF_P + p_bytes(FMT, BITS);  // in a stage, after the dy tile
@@ -706,6 +714,7 @@ __global__ void __launch_bounds__(num_threads(TT), 1)
   constexpr uint32_t A_COL0 = NACC * TT;
   static_assert(STAGE % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
   static_assert(STAGES >= AST && NG <= STAGES && NPROD <= STAGES, "an A slot's previous MMAs are found by their stage");
+  constexpr uint32_t TMEM_COLS = tmem_cols(TT);
   static_assert(A_COL0 + AST * A_COLS <= TMEM_COLS, "A ring beside the accumulators");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

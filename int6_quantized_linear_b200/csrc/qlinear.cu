@@ -747,7 +747,7 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
       !prep(ws, np) ||
       !launch_dependent(meta_kernel<FMT>, dim3((unsigned)(np / WP_ROWS), (unsigned)((K / gr + WP_RUNS - 1) / WP_RUNS)),
                         WP_THREADS, 0, st, gmeta, steps, N, K, d->group, np, ws) ||
-      !launch_dependent(kern, dim3((unsigned)(p.deal.waves ? p.deal.ctas : p.deal.shares)), num_threads(TT), smem, st,
+      !launch_dependent(kern, dim3((unsigned)(p.deal.waves ? p.deal.ctas : p.deal.shares)), NUM_THREADS, smem, st,
                         my, mc, mh, mm, p))
     return cuda_failed();
   if (p.deal.joins() &&

@@ -159,10 +159,10 @@ def _a256(n):
 def test_dx_workspace_formula(lib, fmt, bits, group, N, K, M):
     np_ = (N + 63) // 64 * 64
     run = group if fmt == "affine" else 32
-    tiles = -(-M // (32 if M <= 32 else 128 if M <= 128 else 256))
+    tiles = -(-M // (32 if M <= 32 else 64 if M <= 64 else 256))
     tokens = -(-(-(-M // tiles)) // 16) * 16  # M spread evenly, rounded up to 16
     want = (_a256(2 * M * np_) + _a256(4 * M) + _a256(np_) + _a256(4 * (K // run) * np_)
-            + 148 * 1024 * tokens)
+            + 148 * 1024 * tokens * (2 if M <= 64 else 1))
     assert ql.qlinear_gemm_dx_workspace_bytes(ql.Desc(fmt, N, K, bits, group), M) == want
 
 
