@@ -280,12 +280,14 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
 // Up to 32 tokens: tiles of 32 tokens (MMA N = 32), so no MMA runs on padding tokens -- two CTAs an SM
 // when the layer has more 128-row tiles than SMs (every tile then runs at once instead of some SMs
 // taking two in turn); from 33 tokens: tiles of 256 tokens.  Both take 128 weight rows as the MMA's
-// M = 128 operand.
+// M = 128 operand.  The gated block also takes tiles of 32 tokens for more of them while those tiles fit the SMs
+// at once: a narrow block (few features) over a long K is then spread over up to eight times as many CTAs.
 template <int FMT, int BITS, bool GATED = false>
 ql_status launch_gemm(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, const void *bias,
                       void *y, void *workspace, cudaStream_t st, int sms, const GatedArgs &ga = {}) {
-  if (M <= gemm::TT_SMALL) {
-    if (gemm_row_tiles<GATED>(d->N) > sms)
+  const int64_t small_tiles = (M + gemm::TT_SMALL - 1) / gemm::TT_SMALL * gemm_row_tiles<GATED>(d->N);
+  if (M <= gemm::TT_SMALL || (GATED && small_tiles <= sms)) {
+    if (small_tiles > sms)
       return launch_gemm_tt<FMT, BITS, gemm::TT_SMALL, 2, GATED>(d, w, x, M, bias, y, workspace, st, sms, ga);
     return launch_gemm_tt<FMT, BITS, gemm::TT_SMALL, 1, GATED>(d, w, x, M, bias, y, workspace, st, sms, ga);
   }
