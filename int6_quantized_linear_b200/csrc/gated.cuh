@@ -65,7 +65,8 @@ QL_DEVI float save8_scale(uint32_t E) { return E == 255u ? __uint_as_float(0x7FC
 
 // Rows of whole groups (cols % 16 == 0): the rows follow each other without gaps, so group i of the
 // matrix is values 16 i .. of x, codes 16 i .. and exponent i.  One thread a group: 32 bytes in, 17 out.
-// Memory-bound; two 16-byte loads a thread at full occupancy keep enough bytes in flight.
+// The instructions a value are what bounds it (70 % of the issue slots with a conversion a value), so magnitudes
+// are compared two at a time as their bf16 bits, and a code is the low byte of v / scale + 1.5 2^23 (which rounds).
 __global__ void __launch_bounds__(256) save8_kernel(const __nv_bfloat16 *x, int64_t groups, int8_t *codes,
                                                     uint8_t *exps) {
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
@@ -73,18 +74,23 @@ __global__ void __launch_bounds__(256) save8_kernel(const __nv_bfloat16 *x, int6
   const uint4 *src = reinterpret_cast<const uint4 *>(x) + 2 * i;
   const uint4 a = __ldcs(src), b = __ldcs(src + 1);  // read once: what L2 should keep is the codes
   const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t top = 0u;  // the largest magnitude's bf16 bits (magnitudes order like their bits)
+  uint32_t top = 0u;  // magnitudes order like their bits
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, max(u[j] & 0x7FFFu, (u[j] >> 16) & 0x7FFFu));
+  for (int j = 0; j < 8; ++j) top = __vmaxu2(top, u[j] & 0x7FFF7FFFu);
+  top = max(top & 0xFFFFu, top >> 16);
   const uint32_t E = save8_exponent(save8_key(__uint_as_float(top << 16)));
   const float inv = save8_inverse(E);
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c0 = save8_code(bf16_bits_to_f32(u[2 * j]), inv), c1 = save8_code(bf16_bits_to_f32(u[2 * j] >> 16), inv);
-    const int c2 = save8_code(bf16_bits_to_f32(u[2 * j + 1]), inv);
-    const int c3 = save8_code(bf16_bits_to_f32(u[2 * j + 1] >> 16), inv);
-    o[j] = (c0 & 0xff) | ((c1 & 0xff) << 8) | ((c2 & 0xff) << 16) | ((uint32_t)c3 << 24);
+    uint32_t c[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const uint32_t w = u[2 * j + (h >> 1)];
+      c[h] = __float_as_uint(fmaf(__uint_as_float((h & 1) ? w & 0xffff0000u : w << 16), inv, 12582912.f));
+    }
+    o[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    if (E == 255u) o[j] = 0u;  // not finite
   }
   reinterpret_cast<uint4 *>(codes)[i] = make_uint4(o[0], o[1], o[2], o[3]);
   exps[i] = (uint8_t)E;
