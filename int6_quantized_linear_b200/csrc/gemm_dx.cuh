@@ -115,7 +115,7 @@ constexpr int DY_BIAS = -4, RE_ROWS = 32, RE_THREADS = 8 * RE_ROWS;
 __host__ __device__ constexpr int w_top(int fmt, int bits) {
   return fmt != FMT_AFFINE || bits == 8 ? -6 : bits == 4 ? -7 : -10;
 }
-constexpr int WP_ROWS = 32, WP_RUNS = 64, WP_THREADS = 256;
+constexpr int WP_ROWS = 64, WP_RUNS = 64, WP_THREADS = 256;
 
 template <int FMT, int BITS>
 QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t i, int64_t K, int G) {
@@ -382,28 +382,39 @@ __global__ void __launch_bounds__(THREADS) dgu_prep_kernel(GatedGrad p, Workspac
 }
 
 // ---- pass 3: scaled metadata, transposed ------------------------------------------------------------
-// The metadata of a run (of gran weights) from its group word c and its super-block's step word s: the scales times
-// 2^24 sc, -Z S and b times sc = 2^b_n.
+// Two neighbouring runs' metadata (gran weights each; int4 and int6: of one super-block) from their group words --
+// the two in w0 (int4, int6) or one each in w0 and w1 (affine) -- and their step word, for a row with sc = 2^b_n:
+// the scales times 2^24 sc; -Z S and b times sc.  The powers of two are exact, so they go into the steps first.
+// Byte codes become floats by a permute into the mantissa of 2^23 (a conversion unit has a quarter of the rate).
 constexpr float SUB = 16777216.f;  // 2^24
 template <int FMT>
-QL_DEVI uint32_t scaled_meta(uint32_t c, uint32_t s, float sc) {
+QL_DEVI void scaled_meta(uint32_t w0, uint32_t w1, uint32_t s, float sc, uint32_t (&o)[2]) {
   if constexpr (FMT == FMT_INT4) {
-    const float S = __fmul_rn((float)(c & 0xffu), f16_bits_to_f32(s)) * sc;
-    return pack_f16x2(S * SUB, -__fmul_rn((float)((c >> 8) & 0xffu), f16_bits_to_f32(s >> 16)) * S);
+    const float ss = f16_bits_to_f32(s) * sc * SUB, zs = f16_bits_to_f32(s >> 16) * (-1.f / SUB);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float S = __fmul_rn(byte_of(w0, 2 * i) - 8388608.f, ss);
+      o[i] = pack_f16x2(S, __fmul_rn(byte_of(w0, 2 * i + 1) - 8388608.f, zs) * S);
+    }
   } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
-    const float st = f16_bits_to_f32(s);
-    return pack_f16x2(__fmul_rn((float)(int8_t)c, st) * sc * SUB, __fmul_rn((float)(int8_t)(c >> 8), st) * sc * SUB);
+    const float st = f16_bits_to_f32(s) * sc * SUB;
+    w0 ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      o[i] = pack_f16x2(__fmul_rn(byte_of(w0, 2 * i) - 8388736.f, st), __fmul_rn(byte_of(w0, 2 * i + 1) - 8388736.f, st));
   } else {
-    return pack_f16x2(bf16_bits_to_f32(c) * sc * SUB, bf16_bits_to_f32(c >> 16) * sc);
+    o[0] = pack_f16x2(bf16_bits_to_f32(w0) * sc * SUB, bf16_bits_to_f32(w0 >> 16) * sc);
+    o[1] = pack_f16x2(bf16_bits_to_f32(w1) * sc * SUB, bf16_bits_to_f32(w1 >> 16) * sc);
   }
 }
 
-// A CTA turns the words of 32 rows x 64 runs through shared memory, read along the row and written along n.
+// A CTA turns the words of 64 rows x 64 runs through shared memory, read along the row and written along n.
 template <int FMT>
 __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
                                                           int64_t K, int G, int64_t np, Workspace ws) {
   constexpr int RW = WP_ROWS / (WP_THREADS / 32);  // rows a warp
-  __shared__ uint32_t turn[WP_ROWS][WP_RUNS + 1];
+  __shared__ uint32_t turn[WP_ROWS][WP_RUNS + 1];  // even rows, then odd; even runs, then odd (no bank conflicts)
+  static_assert(WP_ROWS == 64 && WP_RUNS == 64, "a lane a row pair and a run pair");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS, r0 = (int64_t)blockIdx.y * WP_RUNS, runs = K / gran(FMT, G);
   pdl_launch_dependents();
@@ -420,9 +431,7 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
       c[j][0] = __ldg(src);
       if (r + 1 < runs) c[j][1] = __ldg(src + 1);
     } else {  // K % 256 == 0: eight runs a super-block
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(gmeta + 2 * (n * runs + r)));
-      c[j][0] = w & 0xffffu;
-      c[j][1] = w >> 16;
+      c[j][0] = __ldg(reinterpret_cast<const uint32_t *>(gmeta + 2 * (n * runs + r)));
       st[j] = FMT == FMT_INT4 ? __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3))
                               : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3));
     }
@@ -430,17 +439,23 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
 #pragma unroll
   for (int j = 0; j < RW; ++j) {
     const float sc = exp2i(127 + DY_BIAS - (int)ws.rowexp[n0 + RW * warp + j]);
-    turn[RW * warp + j][2 * lane] = scaled_meta<FMT>(c[j][0], st[j], sc);
-    turn[RW * warp + j][2 * lane + 1] = scaled_meta<FMT>(c[j][1], st[j], sc);
+    uint32_t o[2];
+    scaled_meta<FMT>(c[j][0], c[j][1], st[j], sc, o);
+    const int row = RW * warp + j, at = (row >> 1) + WP_ROWS / 2 * (row & 1);
+    turn[at][lane] = o[0];
+    turn[at][WP_RUNS / 2 + lane] = o[1];
   }
   __syncthreads();
+  uint32_t *out = ws.meta + (r0 + warp) * np + n0 + 2 * lane;
 #pragma unroll
   for (int i = 0; i < WP_RUNS / (WP_THREADS / 32); ++i) {
     const int r = warp + (WP_THREADS / 32) * i;
     if (r0 + r < runs) {  // rows n, n + 1: their low halves, then their high halves
-      const uint32_t own = turn[lane][r], other = turn[lane ^ 1][r];
-      ws.meta[(r0 + r) * np + n0 + lane] = (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+      const int col = (r >> 1) + WP_RUNS / 2 * (r & 1);
+      const uint32_t a = turn[lane][col], b = turn[WP_ROWS / 2 + lane][col];
+      *reinterpret_cast<uint2 *>(out) = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     }
+    out += (WP_THREADS / 32) * np;
   }
   pdl_wait();  // for pass 2
 }
@@ -940,50 +955,44 @@ __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
 }
 
 // ---- pass 5: the sums of the split tiles' parts -------------------------------------------------------
-// A CTA takes 32 tokens of a tile, a thread 16 k of one of them; the parts are added in the order of the shares.
-constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 16);
+// A CTA takes 8 tokens of a tile, a thread 4 k of one of them; the parts are added in the order of the shares, four
+// loads in flight (they come from L2 and their latency is what this pass takes).
+constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 4), JOIN_LOADS = 4;
 
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
-  __shared__ int range[3];  // first share, its slot, end of the shares
   const Deal &d = p.deal;
-  const int64_t rest_tile = blockIdx.x, tile = (int64_t)d.waves * d.ctas + rest_tile;
-  if (threadIdx.x == 0) {
-    const int64_t lo = rest_tile * d.steps, hi = lo + d.steps, all = (int64_t)d.rest * d.steps;
-    int c = (int)(lo * d.shares / all);  // at or just before the share that holds stage lo
-    while (d.share_begin(c + 1) <= lo) ++c;
-    range[0] = c;
-    range[1] = 2 * c + (d.share_begin(c) < lo ? 1 : 0);  // its second piece if it began in the tile before
-    int e = (int)(hi * d.shares / all);  // the last share that begins below hi, or one after
-    while (e < d.shares && d.share_begin(e) < hi) ++e;
-    while (d.share_begin(e - 1) >= hi) --e;
-    range[2] = e;
-  }
+  const int rest_tile = (int)blockIdx.x;
+  const int64_t tile = (int64_t)d.waves * d.ctas + rest_tile;
+  // The shares that touch the tile: from the last one, first, that begins at or before its stage 0 (share c begins at
+  // stage floor(all c / shares)) up to the first, end, that begins at or behind its last.
+  const int64_t all = (int64_t)d.rest * d.steps, lo = (int64_t)rest_tile * d.steps;
+  int first = rest_tile * d.shares / d.rest;
+  while (all * (first + 1) < (lo + 1) * d.shares) ++first;
+  const int end = ((rest_tile + 1) * d.shares + d.rest - 1) / d.rest;
+  const bool second = all * first < lo * d.shares;  // share `first` began in the tile before: its second piece
+  const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
+  const int t = blockIdx.y * JOIN_TOKENS + threadIdx.x / (BKT / 4), r = 4 * (threadIdx.x % (BKT / 4));
+  const int64_t m = m_tile * d.tokens + t, k = k_tile * BKT + r;
   pdl_launch_dependents();
   pdl_wait();  // the parts
-  __syncthreads();
-  const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
-  const int t = blockIdx.y * JOIN_TOKENS + threadIdx.x / (BKT / 16), r = 16 * (threadIdx.x % (BKT / 16));
-  const int64_t m = m_tile * d.tokens + t, k = k_tile * BKT + r;
   if (t >= d.tokens || m >= p.M || k >= p.K) return;
-  const int end = range[2];
-  int slot = range[1];
-  float v[16] = {};
-  for (int c = range[0]; c < end; ++c) {
-    const float4 *src = reinterpret_cast<const float4 *>(p.partial + ((int64_t)slot * d.tokens + t) * BKT + r);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 x = __ldcg(src + j);
-      v[4 * j] += x.x; v[4 * j + 1] += x.y; v[4 * j + 2] += x.z; v[4 * j + 3] += x.w;
-    }
-    slot = 2 * (c + 1);
-  }
   const int e = __ldg(p.dexp + m);
+  const float *src = p.partial + (int64_t)t * BKT + r;
+  const int64_t slot = (int64_t)d.tokens * BKT;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = first; c < end; c += JOIN_LOADS) {
+    float4 x[JOIN_LOADS];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = mul_pow2(v[i], e);
-  uint4 *dst = reinterpret_cast<uint4 *>(p.dx + m * p.K + k);
-  dst[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  dst[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
-                      pack_bf16x2(v[14], v[15]));
+    for (int j = 0; j < JOIN_LOADS; ++j)
+      x[j] = c + j < end ? __ldcg(reinterpret_cast<const float4 *>(src + slot * (2 * (c + j) + (second && c + j == first))))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < JOIN_LOADS; ++j) {
+      v.x += x[j].x; v.y += x[j].y; v.z += x[j].z; v.w += x[j].w;
+    }
+  }
+  *reinterpret_cast<uint2 *>(p.dx + m * p.K + k) =
+      make_uint2(pack_bf16x2(mul_pow2(v.x, e), mul_pow2(v.y, e)), pack_bf16x2(mul_pow2(v.z, e), mul_pow2(v.w, e)));
 }
 
 }  // namespace dx
