@@ -500,7 +500,7 @@ __host__ __device__ constexpr int smem_bytes(int fmt, int bits, int tt) {
 // How the tiles are dealt: `waves` whole waves of `ctas` tiles, then the `rest` tiles that are left, their
 // rest * steps stages cut into `shares` equal ranges, one a CTA.
 struct Deal {
-  int64_t m_tiles, k_tiles;
+  int m_tiles, k_tiles;
   int tokens;  // a tile
   int steps;   // stages a tile: Np / 64
   int ctas, waves, rest, shares;
@@ -511,11 +511,11 @@ struct Deal {
 inline Deal deal(int64_t M, int64_t N, int64_t K, int sms) {  // the tile class is M's
   Deal d;
   d.tokens = tile_tokens(M);
-  d.m_tiles = (M + d.tokens - 1) / d.tokens;
-  d.k_tiles = (K + BKT - 1) / BKT;
+  d.m_tiles = (int)((M + d.tokens - 1) / d.tokens);
+  d.k_tiles = (int)((K + BKT - 1) / BKT);
   d.steps = (int)(padded_n(N) / BN);
   d.ctas = (sms < DX_CTAS ? sms : DX_CTAS) * ctas_per_sm(tile_class(M));
-  const int64_t tiles = d.m_tiles * d.k_tiles;
+  const int64_t tiles = (int64_t)d.m_tiles * d.k_tiles;
   d.waves = (int)(tiles / d.ctas);
   d.rest = (int)(tiles % d.ctas);
   const int64_t left = (int64_t)d.rest * d.steps;
@@ -526,27 +526,36 @@ inline Deal deal(int64_t M, int64_t N, int64_t K, int sms) {  // the tile class 
   return d;
 }
 
+// A CTA's share of the rest: stages [step0, step1) of rest tile `tile` and [0, step2) of the next.  It is worked out
+// once a CTA (three 64-bit divisions take about a microsecond), while the kernel before this one runs.
+struct Share {
+  int tile, step0, step1, step2;
+};
+QL_DEVI Share get_share(const Deal &d, int c) {
+  if (c >= d.shares) return Share{0, 0, 0, 0};
+  const int64_t b = d.share_begin(c), e = d.share_begin(c + 1), t0 = b / d.steps, left = e - t0 * d.steps;
+  return Share{(int)t0, (int)(b - t0 * d.steps), (int)(left < d.steps ? left : d.steps),
+               left > d.steps ? (int)(left - d.steps) : 0};
+}
+
 // The i-th piece of work of CTA c: stages [step0, step1) of a tile; slot < 0: the whole tile, stored as dx;
 // otherwise the slot of its partial sums.  A share is at most a tile long, so it has at most two pieces.
 struct Piece {
-  int64_t tile;
+  uint32_t tile;
   int step0, step1, slot;
 };
-QL_DEVI bool get_piece(const Deal &d, int c, int i, Piece &p) {
+QL_DEVI bool get_piece(const Deal &d, const Share &sh, int c, int i, Piece &p) {
   if (i < d.waves) {
-    p = Piece{(int64_t)i * d.ctas + c, 0, d.steps, -1};
+    p = Piece{(uint32_t)(i * d.ctas + c), 0, d.steps, -1};
     return true;
   }
-  if (c >= d.shares) return false;
-  const int64_t b = d.share_begin(c), e = d.share_begin(c + 1), t0 = b / d.steps, cut = (t0 + 1) * d.steps;
-  const int64_t first = (int64_t)d.waves * d.ctas;
-  if (i == d.waves && b < e) {
-    p = Piece{first + t0, (int)(b - t0 * d.steps), (int)((e < cut ? e : cut) - t0 * d.steps),
-              d.joins() ? 2 * c : -1};
+  const uint32_t tile = (uint32_t)(d.waves * d.ctas + sh.tile);
+  if (i == d.waves && sh.step0 < sh.step1) {
+    p = Piece{tile, sh.step0, sh.step1, d.joins() ? 2 * c : -1};
     return true;
   }
-  if (i == d.waves + 1 && e > cut) {
-    p = Piece{first + t0 + 1, 0, (int)(e - cut), 2 * c + 1};
+  if (i == d.waves + 1 && sh.step2 > 0) {
+    p = Piece{tile + 1, 0, sh.step2, 2 * c + 1};
     return true;
   }
   return false;
@@ -758,6 +767,8 @@ __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
     }
   };
 
+  __shared__ Share own_share;
+  if (threadIdx.x == WARP_EPI0 * 32) own_share = get_share(p.deal, cta);
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_tma_full(s), 1);
@@ -780,6 +791,7 @@ __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  const Share share = own_share;
   pdl_launch_dependents();
   pdl_wait();  // the preparation passes' results
 
@@ -799,9 +811,9 @@ __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
       const bool start = !copies_withheld();
       int st = first;  // this producer's next stage, counted from the piece's first
       Piece pc;
-      for (int i = 0; ok && start && get_piece(p.deal, cta, i, pc); ++i) {
-        const int64_t k_tile = pc.tile / p.deal.m_tiles;
-        const int32_t m0 = (int32_t)((pc.tile - k_tile * p.deal.m_tiles) * tokens);
+      for (int i = 0; ok && start && get_piece(p.deal, share, cta, i, pc); ++i) {
+        const uint32_t k_tile = pc.tile / (uint32_t)p.deal.m_tiles;
+        const int32_t m0 = (int32_t)(pc.tile - k_tile * p.deal.m_tiles) * tokens;
         const int32_t x = FMT == FMT_INT6P ? (int32_t)(192 * (k_tile >> 1) + 64 * (k_tile & 1)) : (int32_t)(k_tile * PROW);
         const int32_t xh = (int32_t)(192 * (k_tile >> 1) + 128 + 32 * (k_tile & 1));
         const int32_t run0 = (int32_t)(k_tile * BKT / gran(FMT, p.G));
@@ -838,7 +850,7 @@ __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
     uint32_t ph = 0, aph = 0;
     bool ok = true, issued = false;
     Piece pc;
-    for (int i = 0; ok && get_piece(p.deal, cta, i, pc); ++i) {
+    for (int i = 0; ok && get_piece(p.deal, share, cta, i, pc); ++i) {
       const int a = i % NACC;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_acc_empty(a), ((i / NACC) & 1) ^ 1, abort_flag))) break;
       tc_fence_after();
@@ -868,11 +880,11 @@ __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
   } else if (warp >= WARP_EPI0 && warp < WARP_EPI0 + 4) {
     const int e = warp - WARP_EPI0;  // TMEM lane quarter
     Piece pc;
-    for (int i = 0; get_piece(p.deal, cta, i, pc); ++i) {
+    for (int i = 0; get_piece(p.deal, share, cta, i, pc); ++i) {
       const int a = i % NACC;
-      const int64_t k_tile = pc.tile / p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
-      const int64_t k = k_tile * BKT + out_k<FMT, BITS>(32 * e + lane);
-      const int64_t m0 = m_tile * tokens;
+      const uint32_t k_tile = pc.tile / (uint32_t)p.deal.m_tiles, m_tile = pc.tile - k_tile * p.deal.m_tiles;
+      const int64_t k = (int64_t)k_tile * BKT + out_k<FMT, BITS>(32 * e + lane);
+      const int64_t m0 = (int64_t)m_tile * tokens;
       const int valid = (int)(p.M - m0 < tokens ? p.M - m0 : tokens);
       if (!mbar_wait_suspend(bar_acc_full(a), (i / NACC) & 1, abort_flag)) break;
       tc_fence_after();
@@ -914,7 +926,7 @@ __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm(TT))
     const uint32_t t_row = tmem_base + ((uint32_t)(32 * wq) << 16) + A_COL0;
     int64_t total = 0;  // this CTA's stages
     Piece pc;
-    for (int i = 0; get_piece(p.deal, cta, i, pc); ++i) total += pc.step1 - pc.step0;
+    for (int i = 0; get_piece(p.deal, share, cta, i, pc); ++i) total += pc.step1 - pc.step0;
     int s = g, as = g % AST;
     uint32_t ph = 0;
     // the stage of the step AST before, whose MMAs read this step's A slot, and its phase (the first AST steps
@@ -962,7 +974,7 @@ constexpr int JOIN_THREADS = 256, JOIN_TOKENS = JOIN_THREADS / (BKT / 4), JOIN_L
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
   const Deal &d = p.deal;
   const int rest_tile = (int)blockIdx.x;
-  const int64_t tile = (int64_t)d.waves * d.ctas + rest_tile;
+  const uint32_t tile = (uint32_t)(d.waves * d.ctas + rest_tile);
   // The shares that touch the tile: from the last one, first, that begins at or before its stage 0 (share c begins at
   // stage floor(all c / shares)) up to the first, end, that begins at or behind its last.
   const int64_t all = (int64_t)d.rest * d.steps, lo = (int64_t)rest_tile * d.steps;
@@ -970,9 +982,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(Params p) {
   while (all * (first + 1) < (lo + 1) * d.shares) ++first;
   const int end = ((rest_tile + 1) * d.shares + d.rest - 1) / d.rest;
   const bool second = all * first < lo * d.shares;  // share `first` began in the tile before: its second piece
-  const int64_t k_tile = tile / d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
+  const uint32_t k_tile = tile / (uint32_t)d.m_tiles, m_tile = tile - k_tile * d.m_tiles;
   const int t = blockIdx.y * JOIN_TOKENS + threadIdx.x / (BKT / 4), r = 4 * (threadIdx.x % (BKT / 4));
-  const int64_t m = m_tile * d.tokens + t, k = k_tile * BKT + r;
+  const int64_t m = (int64_t)m_tile * d.tokens + t, k = (int64_t)k_tile * BKT + r;
   pdl_launch_dependents();
   pdl_wait();  // the parts
   if (t >= d.tokens || m >= p.M || k >= p.K) return;
