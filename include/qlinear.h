@@ -425,7 +425,7 @@ ql_status qlinear_restore8(const ql_saved8_const *in, int64_t rows, int64_t cols
  * layer plus, when M > 32, 131072 * min(148, ceil(M/256) * ceil(F/64))
  * (accumulators on their way out); or that of qlinear_gemv where the call runs
  * on it and that is more.
- * Errors: QL_ERR_NULL, QL_ERR_SHAPE (also: N odd or K % 64 != 0),
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (also: N odd, K % 64 != 0, or either above 2^31 - 1),
  * QL_ERR_RANGE, QL_ERR_UNSUPPORTED. */
 ql_status qlinear_gated_workspace_bytes(const ql_desc *desc, int64_t M, size_t *bytes);
 
@@ -459,7 +459,8 @@ ql_status qlinear_gated(const ql_desc *desc, const ql_packed_const *w, const voi
  * (partial sums; twice that up to M = 64), T the tokens of a tile: M spread
  * evenly over ceil(M/C) tiles (C = 32 up to M = 32, 64 up to 64, else 256) and
  * rounded up to 16.
- * Errors: QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_RANGE, QL_ERR_UNSUPPORTED. */
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_RANGE (also: K above 2^26 or M * K
+ * above 2^40), QL_ERR_UNSUPPORTED. */
 ql_status qlinear_gemm_dx_workspace_bytes(const ql_desc *desc, int64_t M, size_t *bytes);
 
 /* Input gradient of the layer: dx[M][K] (bf16) = dy[M][N] (bf16) . W, any

@@ -851,7 +851,8 @@ ql_status check_saved8(int64_t rows, int64_t cols) {
 ql_status check_gated(const ql_desc *d, int64_t M, int32_t act) {
   const ql_status st = check_desc(d);
   if (st != QL_OK) return st;
-  if (d->N % 2 != 0 || d->K % gemm::BK != 0 || d->N > (int64_t)INT32_MAX) return QL_ERR_SHAPE;
+  if (d->N % 2 != 0 || d->K % gemm::BK != 0 || d->N > (int64_t)INT32_MAX || d->K > (int64_t)INT32_MAX)
+    return QL_ERR_SHAPE;
   if (act != QL_ACT_SILU && act != QL_ACT_GELU_TANH && act != QL_ACT_GELU) return QL_ERR_UNSUPPORTED;
   if (M < 1 || M > (int64_t)INT32_MAX) return QL_ERR_RANGE;
   return QL_OK;
@@ -862,7 +863,8 @@ ql_status check_dx(const ql_desc *d, int64_t M) {
   const ql_status st = check_desc(d);
   if (st != QL_OK) return st;
   if (d->N > (int64_t)INT32_MAX - 64 || d->K > (int64_t)INT32_MAX) return QL_ERR_SHAPE;
-  if (M < 1 || M > (int64_t)INT32_MAX) return QL_ERR_RANGE;
+  // K: the metadata pass's grid has a row of CTAs for 64 runs of at least 32; M * K: tiles are counted in 32 bits
+  if (M < 1 || M > (int64_t)INT32_MAX || d->K > (int64_t)1 << 26 || M > ((int64_t)1 << 40) / d->K) return QL_ERR_RANGE;
   return QL_OK;
 }
 

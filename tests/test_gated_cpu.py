@@ -191,3 +191,25 @@ def test_binding_refuses_host_tensors(lib):
     with pytest.raises(ql.QLinearError) as e:
         ql.qlinear_gated(d, *w, bf(1, 256), 1, "tanh", bf(1, 16))
     assert e.value.status == ql.QL_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", [_dx, _backward])
+def test_dx_refuses_what_its_grids_cannot_count(lib, call):
+    """K above 2^26 (the metadata pass's grid) or M * K above 2^40 (tiles counted in 32 bits); the largest that
+    fit are accepted (their workspace is worked out)."""
+    most = 1 << 26
+    n = C.c_size_t()
+    for K, M in ((most + 256, 1), (1 << 30, 1), (most, (1 << 14) + 1), (1 << 20, (1 << 20) + 1)):
+        d = ql.Desc("int4", 64, K)
+        assert call(lib, d, M=M) == ql.QL_ERR_RANGE
+        assert lib.qlinear_gemm_dx_workspace_bytes(C.byref(d.c()), M, C.byref(n)) == ql.QL_ERR_RANGE
+    for K, M in ((most, 1 << 14), (1 << 20, 1 << 20)):
+        assert ql.qlinear_gemm_dx_workspace_bytes(ql.Desc("int4", 64, K), M) > 2 * M * 64
+
+
+def test_gated_refuses_rows_past_32_bits(lib):
+    """k is a 32-bit coordinate of the copies."""
+    d = ql.Desc("int4", 64, 1 << 31)
+    assert _gated(lib, d) == ql.QL_ERR_SHAPE
+    n = C.c_size_t()
+    assert lib.qlinear_gated_workspace_bytes(C.byref(d.c()), 1, C.byref(n)) == ql.QL_ERR_SHAPE
