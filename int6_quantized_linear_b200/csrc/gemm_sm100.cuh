@@ -138,6 +138,7 @@ struct Params {
   int8_t *saved;        // codes [M][2][save8_cols(N / 2)] of (g, u), or NULL
   uint8_t *saved_exps;  // [M][2][save8_cols(N / 2) / 16]
   float4 *scratch;      // TT = 256: [CTA][TT / 4][BN]
+  bool share_tiles;     // TT = 256: the dequantisers help to finish every tile, not the last alone
 };
 
 // The gated form: the layer's rows are F = N / 2 gate rows, then F up rows, and a tile is 64 features:
@@ -583,6 +584,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
                 Params p) {
   constexpr int NACC = num_acc(TT);  // accumulators in TMEM
   constexpr uint32_t A_COL0 = ta_acol0(TT);
+  constexpr bool SHARES = GATED && NACC == 1;  // the dequantisers help to finish tiles
   // dequantising warps per stage: TT = 256 alternates stages between two groups of four
   static_assert(CPS == 1 || (CPS == 2 && TT != BM), "two CTAs an SM: the 32-token form only");
   constexpr int DEQ_WARPS = deq_warps(TT, CPS), NG = DEQ_WARPS / 4;  // dequantiser groups
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_acc_full(a), 1);
-      mbar_init(bar_acc_empty(a), 4);
+      mbar_init(bar_acc_empty(a), SHARES && p.share_tiles ? 4 + DEQ_WARPS : 4);
     }
     mbar_init(bar_final, 1);
     if constexpr (FMT == FMT_INT4) {
@@ -814,12 +816,13 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       // only start once it has been read, and act and the rounding to 8 bits take longer than the reading,
       // so a tile is first moved as it is to this CTA's scratch (in L2) and finished from there beside the
       // next tile's MMAs; each thread reads back what it wrote itself.  Nothing follows the last tile, so it is
-      // finished from tensor memory, by the dequantisers too.
+      // finished from tensor memory, by the dequantisers too; and so is every tile while K is short (share_tiles:
+      // the next tile's stages then take less time than a third of the work on this one's elements).
       float4 *scratch = p.scratch + (int64_t)blockIdx.x * (BN * TT / 4) + 32 * e + lane;
       for (int64_t tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
         const int64_t n_tile = tile / m_tiles, m_tile = tile - n_tile * m_tiles;
         const int a = (int)(tcount % NACC);
-        const bool moved = NACC == 1 && tile + gridDim.x < num_tiles;
+        const bool moved = NACC == 1 && !p.share_tiles && tile + gridDim.x < num_tiles;
         const bool shared_out = NACC == 1 && !moved;
         const GatedRow row(p, n_tile, m_tile, TT, e, lane, gated_down<FMT, BITS>());
         if (!mbar_wait_suspend(bar_acc_full(a), (uint32_t)(tcount / NACC) & 1, abort_flag)) break;
@@ -985,7 +988,34 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       }
       sc = row_scale(row_of(cur.n_tile));
     }
-    for (int64_t it = g; it < total_it; it += NG) {
+    // Gated, one accumulator: this group's chunks (1 + g, 2 + NG + g, ..) of the CTA's tile number t
+    auto finish_tile = [&](int64_t t) {
+      if (!__all_sync(0xffffffffu, mbar_wait_suspend(bar_acc_full(0), (uint32_t)t & 1, abort_flag))) return false;
+      tc_fence_after();
+      const int64_t tile = blockIdx.x + t * gridDim.x, n_tile = tile / m_tiles;
+      const GatedRow row(p, n_tile, tile - n_tile * m_tiles, TT, wd & 3, lane, gated_down<FMT, BITS>());
+#pragma unroll 1
+      for (int c = 1 + g; c < row.chunks; c += 1 + NG) {
+        uint32_t r16[16];
+        tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * (wd & 3)) << 16) + 16 * c, r16);
+        ChunkExp xe;
+        xe.load(p, row, c);
+        tmem_ld_wait();
+        gated_chunk(p, row, r16, xe, c, lane);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (p.share_tiles && lane == 0) mbar_arrive(bar_acc_empty(0));
+      return true;
+    };
+    int64_t done = 0, tile_end = num_kb;  // tiles whose stages this group is done with; the end of the next
+    for (int64_t it = g; SHARES || it < total_it; it += NG) {
+      if constexpr (SHARES) {
+        bool ok = true;
+        for (; ok && done < my_tiles && it >= tile_end; ++done, tile_end += num_kb)
+          if (p.share_tiles || done + 1 == my_tiles) ok = finish_tile(done);
+        if (!ok || it >= total_it) break;
+      }
       Cursor nx = cur;  // this group's next stage
       for (int j = 0; j < NG; ++j) advance(nx);
       uint32_t ngm[2] = {0, 0}, nst[2] = {0, 0};
@@ -1080,24 +1110,6 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       gm[1] = ngm[1];
       st[0] = nst[0];
       st[1] = nst[1];
-    }
-    if constexpr (GATED && NACC == 1) {
-      // the CTA's last tile: chunks 1 + g, 2 + NG + g, .. are this group's once every MMA has retired
-      if (my_tiles > 0 && !*abort_flag && __all_sync(0xffffffffu, mbar_wait_bounded(bar_final, 0, abort_flag))) {
-        tc_fence_after();
-        const int64_t tile = blockIdx.x + (my_tiles - 1) * gridDim.x, n_tile = tile / m_tiles;
-        const GatedRow row(p, n_tile, tile - n_tile * m_tiles, TT, wd & 3, lane, gated_down<FMT, BITS>());
-#pragma unroll 1
-        for (int c = 1 + g; c < row.chunks; c += 1 + NG) {
-          uint32_t r16[16];
-          tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * (wd & 3)) << 16) + 16 * c, r16);
-          ChunkExp xe;
-          xe.load(p, row, c);
-          tmem_ld_wait();
-          gated_chunk(p, row, r16, xe, c, lane);
-        }
-        tc_fence_before();
-      }
     }
   }
 

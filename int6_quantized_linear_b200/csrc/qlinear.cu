@@ -193,6 +193,8 @@ constexpr uint32_t gemv_box_rows() { return GATED ? GATED_ROWS : 64; }
 // CTAs an SM's worth of the gated GEMM at most: the SMs of a B200 (its workspace is sized without a device)
 constexpr int GATED_CTAS = 148;
 
+constexpr int64_t GATED_SHARE_K = 2048, GATED_SHARE_K_SAVED = 4096;
+
 // What the gated forms of the launches take besides the layer's arguments (y is then h [M][N / 2]).
 struct GatedArgs {
   int act = ACT_SILU;
@@ -253,6 +255,7 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
   p.saved = ga.saved;
   p.saved_exps = ga.saved_exps;
   p.scratch = reinterpret_cast<float4 *>(static_cast<uint8_t *>(workspace) + gemm_workspace_bytes(M, N, K));
+  p.share_tiles = GATED && K <= (ga.saved ? GATED_SHARE_K_SAVED : GATED_SHARE_K);
   const int smem = smem_bytes(FMT, BITS, TT);
   auto kern = gemm_kernel<FMT, BITS, TT, CPS, GATED>;
   static thread_local int configured_dev = -1;  // per (kernel instantiation, thread)
