@@ -317,26 +317,65 @@ QL_DEVI void chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], const uint
 // fours (codes) after a transposition among neighbouring lanes, and a group's scale is reduced once, not in
 // every lane.
 
-// h of 8 tokens.  Words of two tokens become words of two features: the even lane of a pair keeps the
+// What a lane needs of its row of a gated tile: its feature, its scale exponent, the tile's tokens, where its outputs
+// go, and whether every exponent sum of the warp's rows and these tokens is that of a normal float (then D * 2^e is
+// one multiplication by 2^e built from its bits, the same single rounding as mul_pow2).  A lane finishes 8 of a
+// chunk's 16 tokens (first: 0 or 8).
+struct GatedRow {
+  int64_t f, F, m0;
+  int we, chunks;  // chunks of 16 tokens that hold any
+  int left, left_saved;  // tokens of the tile from `first` on whose h, whose codes this lane stores
+  bool one_mul;
+  __nv_bfloat16 *h;  // of its first store
+  int8_t *codes;
+  uint8_t *exps;
+  QL_DEVI GatedRow(const Params &p, int64_t n_tile, int64_t m_tile, int tt, int e, int lane, int down) {
+    const int64_t n = layer_row<true>(n_tile, box_row<true>(32 * e + lane), p.N);
+    we = (n < p.N ? p.ws.wexp[n] : 0) + down;  // the weights sit 2^-down below the row scales
+    f = n_tile * GATED_F + 16 * e + (lane & 15);
+    F = p.N / 2;
+    m0 = m_tile * tt;
+    const int64_t rest = p.M - m0;
+    const int tokens = (int)(rest < tt ? rest : tt);
+    chunks = (tokens + 15) / 16;
+    int lo = 1 << 20, hi = -(1 << 20);
+    for (int t = lane; t < tokens; t += 32) {
+      const int xe = __ldg(p.ws.xexp + m0 + t);
+      lo = min(lo, xe);
+      hi = max(hi, xe);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    one_mul = __all_sync(0xffffffffu, lo + we >= -126 && hi + we <= 127);
+    const int first = lane < 16 ? 0 : 8, l = lane & 15;
+    const int64_t fp = save8_cols(F), m = m0 + first;
+    left = f < F ? tokens - first : 0;
+    left_saved = f < fp ? tokens - first : 0;
+    h = F % 2 == 0 ? p.y + (m + (lane & 1)) * F + (f & ~(int64_t)1) : p.y + m * F + f;
+    codes = p.saved + 2 * (m + (lane & 3)) * fp + (f & ~(int64_t)3);
+    exps = p.saved_exps + ((m + 2 * ((l >> 1) & 3) + (l & 1)) * 2 + (l >> 3)) * (fp / 16) + (f >> 4);
+  }
+};
+
+// h of 8 tokens of chunk c.  Words of two tokens become words of two features: the even lane of a pair keeps the
 // first token, the odd lane the second.
-QL_DEVI void gated_store_h(const Params &p, const float (&h)[8], int64_t F, int64_t f, int64_t m0, int64_t rows_left,
-                           int lane) {
-  if (F % 2 == 0) {
-    const bool odd = lane & 1;
-    __nv_bfloat16 *dst = p.y + (m0 + odd) * F + (f & ~(int64_t)1);
+QL_DEVI void gated_store_h(const GatedRow &row, const float (&h)[8], int c, int lane) {
+  const int left = row.left - 16 * c;
+  __nv_bfloat16 *dst = row.h + (int64_t)(16 * c) * row.F;
+  if (row.F % 2 == 0) {
+    const int odd = lane & 1;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t own = pack_bf16x2(h[2 * j], h[2 * j + 1]), other = __shfl_xor_sync(0xffffffffu, own, 1);
-      const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-      if (f < F && 2 * j + odd < rows_left) *reinterpret_cast<uint32_t *>(dst) = w;
-      dst += 2 * F;
+      const uint32_t w = __byte_perm(own, other, odd ? 0x3276 : 0x5410);
+      if (2 * j + odd < left) *reinterpret_cast<uint32_t *>(dst) = w;
+      dst += 2 * row.F;
     }
   } else {
-    __nv_bfloat16 *dst = p.y + m0 * F + f;
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      if (f < F && t < rows_left) *dst = __float2bfloat16_rn(h[t]);
-      dst += F;
+      if (t < left) *dst = __float2bfloat16_rn(h[t]);
+      dst += row.F;
     }
   }
 }
@@ -344,8 +383,7 @@ QL_DEVI void gated_store_h(const Params &p, const float (&h)[8], int64_t F, int6
 // The checkpoint of 8 tokens' g and u.  The 16 lanes' features are one group of each token and projection.
 // A value's upper 16 bits plus one, without the sign, order like save8_key and hold it in their upper bits
 // (the sum is the key's carry); two values share a word.  Words 0-3 are the tokens' g, 4-7 their u.
-QL_DEVI void gated_save(const Params &p, const float (&g)[8], const float (&u)[8], int64_t F, int64_t f, int64_t m0,
-                        int64_t rows_left, int lane) {
+QL_DEVI void gated_save(const GatedRow &row, const float (&g)[8], const float (&u)[8], int ch, int lane) {
   const int l = lane & 15;
   uint32_t k[8];
 #pragma unroll
@@ -368,43 +406,47 @@ QL_DEVI void gated_save(const Params &p, const float (&g)[8], const float (&u)[8
   }
   uint32_t w = __vmaxu2((l & 2) ? a2[1] : a2[0], __shfl_xor_sync(0xffffffffu, (l & 2) ? a2[0] : a2[1], 2));
   w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, 1));
-  // lane l now has the two keys of word l >> 1; exponents, and the exponents of the inverse scales
+  // lane l now has the two keys of word l >> 1; exponents, and the inverse scales' upper 16 bits
   const uint32_t e0 = save8_exponent(min((w & 0xFFFFu) >> 7, 255u)), e1 = save8_exponent(min(w >> 23, 255u));
-  const uint32_t inv = (254u - min(e0, 254u)) | ((254u - min(e1, 254u)) << 16);  // 0 for E = 255
-  const int64_t fp = save8_cols(F);
-  const bool live = f < fp;  // the same for the half-warp
-  {
-    const int t = 2 * ((l >> 1) & 3) + (l & 1);  // token of the key this lane stores: g's in lanes 0-7, u's in 8-15
-    if (live && t < rows_left)
-      p.saved_exps[((m0 + t) * 2 + (l >> 3)) * (fp / 16) + (f >> 4)] = (uint8_t)((l & 1) ? e1 : e0);
-  }
+  const uint32_t inv = ((254u - min(e0, 254u)) << 7) | ((254u - min(e1, 254u)) << 23);  // 0 for E = 255
+  const int64_t fp = save8_cols(row.F);
+  const int left = row.left_saved - 16 * ch;
+  // this lane stores its key's exponent of token 2 ((l >> 1) & 3) + (l & 1): g's in lanes 0-7, u's in 8-15
+  if (2 * ((l >> 1) & 3) + (l & 1) < left) row.exps[2 * ch * fp] = (uint8_t)((l & 1) ? e1 : e0);
   // codes: v 2^(127 - E) + 1.5 2^23 holds rint(v 2^(127 - E)) in its low byte
-  uint32_t c[4] = {0u, 0u, 0u, 0u};  // bytes of tokens 0-3, 4-7 of g, then of u
+  uint32_t c[4];  // bytes of tokens 0-3, 4-7 of g, then of u
+  const bool finite = !__any_sync(0xffffffffu, e0 == 255u || e1 == 255u);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t iw = __shfl_sync(0xffffffffu, inv, (lane & 16) + 2 * j);
-    const float i0 = __uint_as_float(iw << 23), i1 = __uint_as_float((iw & 0xFFFF0000u) << 7);
-    const float v0 = j < 4 ? g[2 * j] : u[2 * j - 8], v1 = j < 4 ? g[2 * j + 1] : u[2 * j - 7];
-    uint32_t b0 = __float_as_uint(fmaf(v0, i0, 12582912.f)), b1 = __float_as_uint(fmaf(v1, i1, 12582912.f));
-    if (i0 == 0.f) b0 = 0u;  // a group that is not finite
-    if (i1 == 0.f) b1 = 0u;
-    c[j >> 1] |= (j & 1) ? __byte_perm(b0, b1, 0x4044) & 0xFFFF0000u : __byte_perm(b0, b1, 0x0040) & 0xFFFFu;
+  for (int i = 0; i < 4; ++i) {
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t iw = __shfl_sync(0xffffffffu, inv, (lane & 16) + 4 * i + 2 * j);
+      const float i0 = __uint_as_float(iw << 16), i1 = __uint_as_float(iw & 0xFFFF0000u);
+      const int t = 4 * (i & 1) + 2 * j;
+      b[2 * j] = __float_as_uint(fmaf(i < 2 ? g[t] : u[t], i0, 12582912.f));
+      b[2 * j + 1] = __float_as_uint(fmaf(i < 2 ? g[t + 1] : u[t + 1], i1, 12582912.f));
+      if (!finite) {  // codes of groups that are not are 0
+        if (i0 == 0.f) b[2 * j] = 0u;
+        if (i1 == 0.f) b[2 * j + 1] = 0u;
+      }
+    }
+    c[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
   // 4 x 4 bytes turn among four lanes: lane q of a quad gets token q (or 4 + q) of the quad's features
   const int q = lane & 3;
-  int8_t *dst = p.saved + 2 * (m0 + q) * fp + (f & ~(int64_t)3);
+  const uint32_t turn1 = (q & 1) ? 0x3715u : 0x6240u, turn2 = (q & 2) ? 0x3276u : 0x5410u;
+  int8_t *dst = row.codes + 32 * ch * fp;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t v = c[i], o = __shfl_xor_sync(0xffffffffu, v, 1);
-    v = (q & 1) ? __byte_perm(v, o, 0x3715) : __byte_perm(v, o, 0x6240);  // bytes (t, t of the neighbour) x 2 tokens
-    o = __shfl_xor_sync(0xffffffffu, v, 2);
-    v = (q & 2) ? __byte_perm(v, o, 0x3276) : __byte_perm(v, o, 0x5410);
-    if (live && 4 * (i & 1) + q < rows_left) *reinterpret_cast<uint32_t *>(dst + (i >> 1) * fp + 8 * (i & 1) * fp) = v;
+    uint32_t v = c[i];
+    v = __byte_perm(v, __shfl_xor_sync(0xffffffffu, v, 1), turn1);  // bytes (t, t of the neighbour) x 2 tokens
+    v = __byte_perm(v, __shfl_xor_sync(0xffffffffu, v, 2), turn2);
+    if (4 * (i & 1) + q < left) *reinterpret_cast<uint32_t *>(dst + (i >> 1) * fp + 8 * (i & 1) * fp) = v;
   }
 }
 
-QL_DEVI void gated_store(const Params &p, const uint32_t (&r)[16], int64_t f, int64_t m0, int lane) {
-  const int64_t F = p.N / 2;
+QL_DEVI void gated_store(const Params &p, const GatedRow &row, const uint32_t (&r)[16], int c, int lane) {
   const bool up = lane >= 16;
   float g[8], u[8], h[8];
 #pragma unroll
@@ -413,12 +455,10 @@ QL_DEVI void gated_store(const Params &p, const uint32_t (&r)[16], int64_t f, in
     g[t] = up ? other : __uint_as_float(r[t]);
     u[t] = up ? __uint_as_float(r[8 + t]) : other;
   }
-  if (f >= F) {  // features past the last: zeros in the checkpoint's padding
+  if (row.f >= row.F) {  // features past the last: zeros in the checkpoint's padding
 #pragma unroll
     for (int t = 0; t < 8; ++t) g[t] = u[t] = 0.f;
   }
-  m0 += up ? 8 : 0;
-  const int64_t rows_left = p.M - m0;
   if (p.act == ACT_SILU) {
 #pragma unroll
     for (int t = 0; t < 8; ++t) h[t] = act_value(ACT_SILU, g[t]) * u[t];
@@ -426,8 +466,8 @@ QL_DEVI void gated_store(const Params &p, const uint32_t (&r)[16], int64_t f, in
 #pragma unroll
     for (int t = 0; t < 8; ++t) h[t] = act_value(p.act, g[t]) * u[t];
   }
-  gated_store_h(p, h, F, f, m0, rows_left, lane);
-  if (p.saved) gated_save(p, g, u, F, f, m0, rows_left, lane);
+  gated_store_h(row, h, c, lane);
+  if (p.saved) gated_save(row, g, u, c, lane);
 }
 
 // chunk_to_f16 of the gated form: the codes enter as the fp16 subnormals q 2^-24 that a mask leaves in the low bits
@@ -524,33 +564,6 @@ QL_DEVI void gated_chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], cons
   }
 }
 
-// What a lane needs of its row of a gated tile: its feature, its scale exponent, the tile's tokens, and
-// whether every exponent sum of the warp's rows and these tokens is that of a normal float (then D * 2^e is
-// one multiplication by 2^e built from its bits, the same single rounding as mul_pow2).
-struct GatedRow {
-  int64_t f, m0;
-  int we, chunks;  // chunks of 16 tokens that hold any
-  bool one_mul;
-  QL_DEVI GatedRow(const Params &p, int64_t n_tile, int64_t m_tile, int tt, int e, int lane, int down) {
-    const int64_t n = layer_row<true>(n_tile, box_row<true>(32 * e + lane), p.N);
-    we = (n < p.N ? p.ws.wexp[n] : 0) + down;  // the weights sit 2^-down below the row scales
-    f = n_tile * GATED_F + 16 * e + (lane & 15);
-    m0 = m_tile * tt;
-    const int64_t left = p.M - m0;
-    const int tokens = (int)(left < tt ? left : tt);
-    chunks = (tokens + 15) / 16;
-    int lo = 1 << 20, hi = -(1 << 20);
-    for (int t = lane; t < tokens; t += 32) {
-      const int xe = __ldg(p.ws.xexp + m0 + t);
-      lo = min(lo, xe);
-      hi = max(hi, xe);
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    one_mul = __all_sync(0xffffffffu, lo + we >= -126 && hi + we <= 127);
-  }
-};
-
 // The token exponents of chunk c (those of tokens past M are read, their section of the workspace being
 // padded, and not used).
 struct ChunkExp {
@@ -575,7 +588,7 @@ QL_DEVI void gated_chunk(const Params &p, const GatedRow &row, uint32_t (&r)[16]
 #pragma unroll
     for (int t = 0; t < 16; ++t) r[t] = __float_as_uint(mul_pow2(__uint_as_float(r[t]), xe[t] + row.we));
   }
-  gated_store(p, r, row.f, row.m0 + 16 * c, lane);
+  gated_store(p, row, r, c, lane);
 }
 
 template <int FMT, int BITS, int TT, int CPS = 1, bool GATED = false>
@@ -990,10 +1003,10 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
     }
     // Gated, one accumulator: this group's chunks (1 + g, 2 + NG + g, ..) of the CTA's tile number t
     auto finish_tile = [&](int64_t t) {
-      if (!__all_sync(0xffffffffu, mbar_wait_suspend(bar_acc_full(0), (uint32_t)t & 1, abort_flag))) return false;
-      tc_fence_after();
       const int64_t tile = blockIdx.x + t * gridDim.x, n_tile = tile / m_tiles;
       const GatedRow row(p, n_tile, tile - n_tile * m_tiles, TT, wd & 3, lane, gated_down<FMT, BITS>());
+      if (!__all_sync(0xffffffffu, mbar_wait_suspend(bar_acc_full(0), (uint32_t)t & 1, abort_flag))) return false;
+      tc_fence_after();
 #pragma unroll 1
       for (int c = 1 + g; c < row.chunks; c += 1 + NG) {
         uint32_t r16[16];
