@@ -39,8 +39,8 @@ FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustain
 
 # DRAM bytes per GEMV launch from one ncu capture (dram__bytes_read.sum + dram__bytes_write.sum),
 # valid only while the GEMV source is unchanged (hash of csrc/gemv.cuh at capture time).
-NCU_TRAFFIC = {"gemv_src_sha256": "e96a8dbc0350f04aaba0ef5fcaa3db81b517d0102074e935a68b0e258c1b5f39",
-               "bytes_per_launch": 83039104}  # mean over the two decode layers
+NCU_TRAFFIC = {"gemv_src_sha256": "7fa4b49eaa71e7c856d1749c462f7ae4c1feab041a8be7df85fddef8577670af",
+               "bytes_per_launch": 82932992}  # mean over the two decode layers
 
 
 def parse_args(argv=None):

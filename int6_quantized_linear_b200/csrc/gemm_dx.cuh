@@ -8,9 +8,9 @@
 // nothing: a matrix load with transposition (ldmatrix .trans on 16-bit elements) of eight rows' packed codes
 // gives each thread 16 bits of codes of two neighbouring rows n, n + 1 side by side -- four nibbles, two bytes or
 // eight 2-bit fields of consecutive k -- and each mask of that word is a pair (n, n + 1) of one k: a TMEM word.
-// (A first form decoded along the rows and let the tensor core transpose an M-major A tile in shared memory.  Its
-// stores, the tensor core's reads of it and dy's went through shared memory at 832 of 821 measured cycles a
-// stage against the MMAs' 512; without the tile it is 576.)
+// (A first form decoded along the rows and let the tensor core transpose an M-major A tile in shared memory: 821
+// cycles a stage of 256 tokens, all of them shared-memory traffic -- its stores, the tensor core's reads of it and of
+// dy -- against the MMAs' 512; without the tile it is about 580.)
 //
 // Operands are fp16 with exact power-of-two scales, as in the forward GEMM (gemm_prep.cuh).  A weight row's
 // scale 2^b_n cannot be undone after a sum over rows, so its inverse goes into the other operand:
@@ -25,7 +25,7 @@
 // Passes: (1) row exponents b_n; (2) dy to scaled fp16 rows; (3) the scaled group metadata, transposed so that a
 // stage's words are one TMA box; (4) the GEMM; (5) the sum of the parts of split tiles.
 //
-// A CTA an SM.  The tiles of whole waves (as many tiles as CTAs, again and again) are computed alone, all
+// One or two CTAs an SM (ctas_per_sm).  The tiles of whole waves (as many tiles as CTAs, again and again) are computed alone, all
 // CTAs moving along n together so that each code row and each dy column is fetched from memory about once
 // a wave; the tiles of the last, partial wave are cut along n into equal shares, one a CTA, whose fp32 sums
 // go to the workspace and are added in a fixed order (a full last wave costs as much as the others however
@@ -53,9 +53,10 @@ constexpr int MIN_SHARE = 8;       // stages a share of a split tile has at leas
 // Token tiles: the class (most tokens of a tile, which sizes the rings) and the tokens that a launch's tiles
 // have, a multiple of 16 (the MMA's N) that spreads M evenly.
 constexpr int TT_LARGE = 256, TT_MEDIUM = 64, TT_SMALL = 32;
-// CTAs an SM: the one warp that issues a CTA's MMAs needs about 450 cycles a stage, and up to 64 tokens the MMAs
-// themselves take 230 to 250, so two CTAs share the tensor core (K = 5120, N = 27648, M = 4: 47.7 -> 44.3 us a call,
-// M = 64: 61.0 -> 55.4; at M = 128 one CTA is faster, 67.2 against 75.2).
+// CTAs an SM: a CTA's chain of copy, decoding, MMA and release takes more than 500 cycles a stage, and up to 64
+// tokens the MMAs themselves take 230 to 250, so two CTAs share the tensor core (int4, K = 5120, N = 27648, M = 4: 38.1
+// us a call against 46.7, M = 64: 45.9 against 49.7; int6, K = 4096, N = 8192, M = 12: 23.0 against 22.7; with tiles of
+// 128 tokens one CTA was faster, 67.2 against 75.2 at M = 128).
 __host__ __device__ constexpr int ctas_per_sm(int tt) { return tt == TT_LARGE ? 1 : 2; }
 inline int tile_class(int64_t M) { return M <= TT_SMALL ? TT_SMALL : M <= TT_MEDIUM ? TT_MEDIUM : TT_LARGE; }
 inline int tile_tokens(int64_t M) {
@@ -408,7 +409,8 @@ QL_DEVI void scaled_meta(uint32_t w0, uint32_t w1, uint32_t s, float sc, uint32_
   }
 }
 
-// A CTA turns the words of 64 rows x 64 runs through shared memory, read along the row and written along n.
+// A CTA turns the words of 64 rows x 64 runs through shared memory, read along the row and written along n.  9.5 us for
+// 27648 x 160 runs (28 MB in and out; with a conversion a byte and a word a store it was 13.2).
 template <int FMT>
 __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
                                                           int64_t K, int G, int64_t np, Workspace ws) {

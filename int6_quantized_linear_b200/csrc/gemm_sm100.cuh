@@ -10,9 +10,7 @@
 // it.  Shared memory then carries only the x tile (written once by TMA, read
 // once by the tensor core) and the packed codes: a shared-memory weight tile
 // would add its store, and a second token half would read it again, roughly
-// doubling the bytes shared memory moves per MMA.  Within a tile the pace is
-// set by the one thread that issues the MMAs (its per-stage waits, commits and
-// bookkeeping).  Two token tiles:
+// doubling the bytes shared memory moves per MMA.  Two token tiles:
 //   TT = 256 (prefill): one M = 128, N = 256 MMA per 16-k slice.  The
 //     accumulator (128 lanes x 256 columns) and a ring of A stages (32 columns
 //     each) share the 512 TMEM columns, so there is one accumulator and the
@@ -22,7 +20,8 @@
 // Warp roles:
 //   warp 0      TMA producer: scaled fp16 x tile (TT x 64, 128-byte
 //               swizzle) and the packed code tile (128 rows x BK codes)
-//   warp 1      TMEM allocator; lane 0 issues tcgen05.mma (f16 x f16 -> f32)
+//   warp 1      TMEM allocator; the whole warp runs the MMA loop and an elected
+//               lane issues tcgen05.mma (f16 x f16 -> f32)
 //   warps 2-3   (int4) copy each super-block's group and step words into a
 //               metadata ring, MSLOTS super-blocks ahead
 //   warps 4-7   epilogue: tcgen05.ld the accumulator (warp w reads TMEM lanes
@@ -312,8 +311,8 @@ QL_DEVI void chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], const uint
 // Epilogue of the gated form for 16 tokens (m0 ..) of one feature f: lanes 0-15 of the warp hold the 16
 // tokens' g in r, lanes 16-31 the same features' u.  Each lane sends half of its tokens to its partner
 // (lane ^ 16) and receives the other projection of the half it keeps: lanes 0-15 finish tokens 0-7, lanes
-// 16-31 tokens 8-15, 16 contiguous features of each.  This warp runs beside the dequantisers, whose issue
-// slots it takes, so it is written for few instructions: values travel and are stored in pairs (h) and
+// 16-31 tokens 8-15, 16 contiguous features of each.  These warps run beside the dequantisers, whose issue
+// slots they take, so this is written for few instructions: values travel and are stored in pairs (h) and
 // fours (codes) after a transposition among neighbouring lanes, and a group's scale is reduced once, not in
 // every lane.
 

@@ -193,6 +193,9 @@ constexpr uint32_t gemv_box_rows() { return GATED ? GATED_ROWS : 64; }
 // CTAs an SM's worth of the gated GEMM at most: the SMs of a B200 (its workspace is sized without a device)
 constexpr int GATED_CTAS = 148;
 
+// Up to this K the gated GEMM's dequantisers help to finish every tile of 256 tokens (with a checkpoint, whose rounding
+// is more work, up to the larger one).  int4, M = 2048, N = 8192: K = 1024 50.7 us against 60.6, K = 2048 81 against 84, at
+// K = 4096 equal; with a checkpoint K = 1024 69.1 against 89.2, K = 4096 161 against 170 (int6: 189 against 188).
 constexpr int64_t GATED_SHARE_K = 2048, GATED_SHARE_K_SAVED = 4096;
 
 // What the gated forms of the launches take besides the layer's arguments (y is then h [M][N / 2]).
@@ -284,7 +287,9 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
 // when the layer has more 128-row tiles than SMs (every tile then runs at once instead of some SMs
 // taking two in turn); from 33 tokens: tiles of 256 tokens.  Both take 128 weight rows as the MMA's
 // M = 128 operand.  The gated block also takes tiles of 32 tokens for more of them while those tiles fit the SMs
-// at once: a narrow block (few features) over a long K is then spread over up to eight times as many CTAs.
+// at once: a narrow block (few features) is then spread over up to eight times as many CTAs (int4, M = 696, N = 138,
+// K = 4096: 24.2 us against 31.4; int6, M = 3484, N = 40, K = 9472: 74.6 against 97.0; int4, M = 256, N = 1024, K = 512:
+// 9.0 against 11.7).
 template <int FMT, int BITS, bool GATED = false>
 ql_status launch_gemm(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, const void *bias,
                       void *y, void *workspace, cudaStream_t st, int sms, const GatedArgs &ga = {}) {
