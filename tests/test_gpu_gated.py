@@ -228,6 +228,31 @@ def test_gated_checkpoint(cuda, fmt, M, F, K):
     assert np.array_equal(f64(back), got)
 
 
+# More tiles than SMs, two tiles of tokens: a CTA finishes several tiles, alone from its scratch tile (long K) or with the
+# dequantisers' help (short K: one stage a tile, fewer stages than the ring, an odd number of them; with and without a
+# checkpoint the two meet at different K)
+@pytest.mark.parametrize("save", [False, True])
+@pytest.mark.parametrize("fmt,bits,group,K", [("affine", 4, 64, 64), ("affine", 8, 64, 192), ("affine", 2, 64, 320),
+                                              ("int6", 0, 0, 512), ("int4", 0, 0, 2048), ("int4", 0, 0, 2304),
+                                              ("int6p", 0, 0, 4352)])
+def test_gated_many_tiles(cuda, fmt, bits, group, K, save):
+    M, F = 270, 5010
+    L = layer(fmt, 2 * F, K, K, bits, group)
+    xb = scaled_x(L, M, K + 1)
+    h, saved = run_gated(L, xb, M, "silu", save)
+    gu = bf16_to_f64(xb) @ L.wref.T
+    check_h(f64(h), gu[:, :F], gu[:, F:], "silu", f"{fmt} K={K}")
+    again, saved2 = run_gated(L, xb, M, "silu", save)
+    assert torch.equal(h, again)
+    if save:
+        assert torch.equal(saved[0], saved2[0]) and torch.equal(saved[1], saved2[1])
+        gu = gu.reshape(2 * M, F)
+        exps = saved[1].cpu().numpy()
+        step = np.repeat(np.ldexp(1.0, exps.astype(int) - 127), 16, axis=1)[:, :F]
+        got = R.restore8(saved[0].cpu().numpy(), exps, F)
+        assert np.all(np.abs(got - gu) <= 0.5 * step + 1e-2 * max(2.0, rms(gu)))
+
+
 # ---- backward ----------------------------------------------------------------------------------------------
 
 SHAPES = [(1, 34, 256), (5, 200, 512), (32, 2006, 768), (33, 66, 512), (77, 130, 1280), (300, 1000, 512)]
