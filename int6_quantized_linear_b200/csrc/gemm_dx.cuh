@@ -409,8 +409,8 @@ QL_DEVI void scaled_meta(uint32_t w0, uint32_t w1, uint32_t s, float sc, uint32_
   }
 }
 
-// A CTA turns the words of 64 rows x 64 runs through shared memory, read along the row and written along n.  9.5 us for
-// 27648 x 160 runs (28 MB in and out; with a conversion a byte and a word a store it was 13.2).
+// A CTA turns the words of 64 rows x 64 runs through shared memory, read along the row and written along n.  About 10 us
+// for 27648 x 160 runs (28 MB in and out; with a conversion a byte and a word a store it was 13.2), issue 70 %.
 template <int FMT>
 __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
                                                           int64_t K, int G, int64_t np, Workspace ws) {
@@ -421,26 +421,33 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
   const int64_t n0 = (int64_t)blockIdx.x * WP_ROWS, r0 = (int64_t)blockIdx.y * WP_RUNS, runs = K / gran(FMT, G);
   pdl_launch_dependents();
   // a lane takes runs 2 l and 2 l + 1 of its row: one word of 16-bit group words (int4, int6), two of affine
-  const int64_t r = r0 + 2 * lane;
+  static_assert(RW == 8, "a warp's exponent bytes are one load");
+  const int64_t r = r0 + 2 * lane, first = n0 + RW * warp;
+  const int rows = r < runs ? (int)(N - first < RW ? N - first : RW) : 0;  // rows of this lane that exist
   uint32_t c[RW][2], st[RW];
+  constexpr int GB = FMT == FMT_AFFINE ? 4 : 2, SB = FMT == FMT_INT4 ? 4 : 2;  // bytes of a group word, of a step word
+  const uint8_t *gsrc = gmeta + GB * (first * runs + r), *ssrc = steps + SB * (first * (K / 256) + (r >> 3));
 #pragma unroll
   for (int j = 0; j < RW; ++j) {
-    const int64_t n = n0 + RW * warp + j;
     c[j][0] = c[j][1] = st[j] = 0u;
-    if (n >= N || r >= runs) continue;
-    if constexpr (FMT == FMT_AFFINE) {
-      const uint32_t *src = reinterpret_cast<const uint32_t *>(gmeta) + n * runs + r;
-      c[j][0] = __ldg(src);
-      if (r + 1 < runs) c[j][1] = __ldg(src + 1);
-    } else {  // K % 256 == 0: eight runs a super-block
-      c[j][0] = __ldg(reinterpret_cast<const uint32_t *>(gmeta + 2 * (n * runs + r)));
-      st[j] = FMT == FMT_INT4 ? __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + (r >> 3))
-                              : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + (r >> 3));
+    if (j < rows) {
+      c[j][0] = __ldg(reinterpret_cast<const uint32_t *>(gsrc));
+      if constexpr (FMT == FMT_AFFINE) {
+        if (r + 1 < runs) c[j][1] = __ldg(reinterpret_cast<const uint32_t *>(gsrc) + 1);
+      } else {  // K % 256 == 0: eight runs a super-block
+        st[j] = FMT == FMT_INT4 ? __ldg(reinterpret_cast<const uint32_t *>(ssrc))
+                                : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(ssrc));
+      }
     }
+    gsrc += GB * runs;
+    ssrc += SB * (K / 256);
   }
+  const uint2 eb = *reinterpret_cast<const uint2 *>(ws.rowexp + first);
 #pragma unroll
   for (int j = 0; j < RW; ++j) {
-    const float sc = exp2i(127 + DY_BIAS - (int)ws.rowexp[n0 + RW * warp + j]);
+    // 2^b_n from the byte 127 + DY_BIAS - b_n, b_n in [-126, 120]
+    const uint32_t byte = ((j < 4 ? eb.x : eb.y) >> (8 * (j & 3))) & 0xFFu;
+    const float sc = __uint_as_float((uint32_t)(254 + DY_BIAS - (int)byte) << 23);
     uint32_t o[2];
     scaled_meta<FMT>(c[j][0], c[j][1], st[j], sc, o);
     const int row = RW * warp + j, at = (row >> 1) + WP_ROWS / 2 * (row & 1);
@@ -449,11 +456,11 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
   }
   __syncthreads();
   uint32_t *out = ws.meta + (r0 + warp) * np + n0 + 2 * lane;
+  const int left = (int)(runs - r0 < WP_RUNS ? runs - r0 : WP_RUNS) - warp;
 #pragma unroll
   for (int i = 0; i < WP_RUNS / (WP_THREADS / 32); ++i) {
-    const int r = warp + (WP_THREADS / 32) * i;
-    if (r0 + r < runs) {  // rows n, n + 1: their low halves, then their high halves
-      const int col = (r >> 1) + WP_RUNS / 2 * (r & 1);
+    if ((WP_THREADS / 32) * i < left) {  // rows n, n + 1: their low halves, then their high halves
+      const int col = (warp >> 1) + WP_RUNS / 2 * (warp & 1) + (WP_THREADS / 64) * i;
       const uint32_t a = turn[lane][col], b = turn[WP_ROWS / 2 + lane][col];
       *reinterpret_cast<uint2 *>(out) = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     }
