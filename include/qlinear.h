@@ -430,12 +430,20 @@ ql_status qlinear_restore8(const ql_saved8_const *in, int64_t rows, int64_t cols
 ql_status qlinear_gated_workspace_bytes(const ql_desc *desc, int64_t M, size_t *bytes);
 
 /* h[M][F] (bf16) = act(g) * u, x bf16 [M][K], any M >= 1, K % 64 == 0, N = 2F.
- * g and u are the accumulators of qlinear_gemv / qlinear_gemm; activation and
- * product are taken in fp32 from them, with one rounding to bf16.  Decode
- * (M <= 8; affine with group 32 or 64 and K % 256 == 0: M <= 32) runs on the
- * GEMV kernels, each CTA streaming the gate and up rows of the same features;
- * everything else, and every call with a checkpoint, on the tcgen05 GEMM, whose
- * tiles are 64 gate rows and the same features' 64 up rows.
+ * g and u are fp32 sums; activation and product are taken in fp32 from them,
+ * with one rounding to bf16.  Decode (M <= 8; affine with group 32 or 64 and
+ * K % 256 == 0: M <= 32) runs on the GEMV kernels, each CTA streaming the gate
+ * and up rows of the same features; g and u are then qlinear_gemv's sums.
+ * Everything else, and every call with a checkpoint, runs on the tcgen05 GEMM,
+ * whose tiles are 64 gate rows and the same features' 64 up rows.  x enters it
+ * as in qlinear_gemm.  So do the weights (fp16 against a power of two for each
+ * row), with two differences: int6 rounds its group's scale to fp16 and then
+ * the product; and int4 and affine weights lie 2^-15 lower, so that a group
+ * keeps fp16's 11 bits (of its largest weight) while that is at least 2^-13 of
+ * its row's largest, and one bit less for each power of two below.
+ * qlinear_gemm's error of an int4 weight at or near its zero point (up to
+ * 2^-11 (|q| + |Z| + |q - Z|) |S|) is that of this form too: where an element of
+ * x 2^7 or more times the others meets such a weight it can be seen in g and u.
  * x is finite: an infinity or a NaN in a token spoils that token's h in the
  * GEMM form and gives an unspecified h for it in the decode forms (whose x is
  * fixed point, as qlinear_gemv's); other tokens are not affected.

@@ -471,23 +471,31 @@ QL_DEVI void gated_store(const Params &p, const GatedRow &row, const uint32_t (&
   if (p.saved) gated_save(row, g, u, c, lane);
 }
 
-// chunk_to_f16 of the gated form: the codes enter as the fp16 subnormals q 2^-24 that a mask leaves in the low bits
-// of a half (up to bit 9), and 2^24 goes into the scale, so a pair of weights is a mask and a fused multiply-add.
-// For that scale to be an fp16 number the weights are 2^-GATED_DOWN lower than the row scales of the prep pass put
-// them (int4: S <= 2^15 / 7.5, affine: s <= 2^16 / (2^bits - 1)); int6 rounds its scale and its product.
+// chunk_to_f16 of the gated form, whose epilogue shares the issue slots.  int4 and affine codes are shifted to the top of
+// a half's ten mantissa bits, where alone they are the fp16 subnormal q 2^-18 (2-bit: 2^-16, 8-bit: 2^-22); the inverse
+// power goes into the scale, and a pair of weights is a shift, a mask and one fused multiply-add.  For that scale to be
+// an fp16 number (the prep pass leaves S <= 2^15 / 7.5 and s <= 2^16 / (2^bits - 1)) a row's weights lie below 1, 2^-15
+// of where the plain GEMM has them.  fp16 keeps 11 bits down to 2^-14: a group whose largest weight is 2^-13 of the row's
+// or more has its weights to 2^-11 of that largest one, a smaller group one bit less a power of two.  (Codes left at the
+// bottom of the half, q 2^-24, are a shift less and reach 2^-7, 2-bit ones 2^-4: too little for a layer whose columns
+// differ, and 0 to 5 % faster.)  The plain GEMM's way, 1024 + q and a subtraction, reaches 2^-28, but the half-precision
+// pipe then sets the pace: M = 2048, K = 5120, N = 27648: int4 600 us against 542; K = 4096, N = 14336: 4-bit 306 against
+// 284, 2-bit 306 against 278, 8-bit 302 against 306; M = 20, N = 27648: int4 60 against 54, 8-bit 73 against 64.
+// int6 does subtract, and multiplies by its scale as an fp16 number (two roundings, 2^-12 of the weight each): 596 us
+// where the plain GEMM's product in fp32 takes 690.
 template <int FMT, int BITS>
-__host__ __device__ constexpr int gated_down() { return FMT == FMT_AFFINE && BITS == 2 ? 24 : 21; }
+__host__ __device__ constexpr int gated_down() { return FMT == FMT_INT6 || FMT == FMT_INT6P ? 0 : 15; }
 
 template <int FMT, int BITS>
 QL_DEVI void gated_chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], const uint8_t *src, const uint8_t *src_hi,
                                 uint32_t gm, uint32_t st, float sc, uint32_t (&o)[16]) {
-  constexpr float UP = (float)(1 << (24 - gated_down<FMT, BITS>()));  // 2^24 times 2^-GATED_DOWN
-  auto fma2 = [](uint32_t q, __half2 s, __half2 z) {
-    const __half2 w = __hfma2(*reinterpret_cast<const __half2 *>(&q), s, z);
-    return *reinterpret_cast<const uint32_t *>(&w);
-  };
-  constexpr float DOWN = 1.f / (float)(1 << gated_down<FMT, BITS>());
-  if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {
+  auto half2_of = [](uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); };
+  auto word_of = [](__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); };
+  if constexpr (FMT == FMT_INT4 || FMT == FMT_AFFINE) {
+    // 2^(24 - TOP) undoes the code's place (its lowest bit is mantissa bit TOP), 2^-DOWN lowers the row
+    constexpr int TOP = 10 - (FMT == FMT_INT4 ? 4 : BITS);
+    constexpr float DOWN = 1.f / (float)(1 << gated_down<FMT, BITS>()), UP = (float)(1 << (24 - TOP)) * DOWN;
+    constexpr uint32_t MASK = 0x00010001u * (uint32_t)(1024 - (1 << TOP));
     float S, z;
     if constexpr (FMT == FMT_INT4) {
       const float scf = __uint_as_float(0x4B000000u | (gm & 0xffu)) - 8388608.f;
@@ -498,41 +506,33 @@ QL_DEVI void gated_chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], cons
       S = bf16_bits_to_f32(gm) * sc;
       z = bf16_bits_to_f32(gm >> 16) * sc * DOWN;
     }
-    const __half2 s0 = __float2half2_rn(S * UP), s1 = __hmul2(s0, __float2half2_rn(0.0625f)), z2 = __float2half2_rn(z);
+    const __half2 s2 = __float2half2_rn(S * UP), z2 = __float2half2_rn(z);
+    auto weight = [&](uint32_t q) { return word_of(__hfma2(half2_of(BITS == 8 ? q : q & MASK), s2, z2)); };
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t w8 = cw[q] >> 8;
-      o[4 * q] = fma2(cw[q] & 0x000F000Fu, s0, z2);
-      o[4 * q + 1] = fma2(cw[q] & 0x00F000F0u, s1, z2);
-      o[4 * q + 2] = fma2(w8 & 0x000F000Fu, s0, z2);
-      o[4 * q + 3] = fma2(w8 & 0x00F000F0u, s1, z2);
-    }
-  } else if constexpr (FMT == FMT_AFFINE) {
-    const __half2 z2 = __float2half2_rn(bf16_bits_to_f32(gm >> 16) * sc * DOWN);
-    __half2 s[4];
-    s[0] = __float2half2_rn(bf16_bits_to_f32(gm) * sc * UP);
-#pragma unroll
-    for (int e = 1; e < 4; ++e) s[e] = BITS == 2 ? __hmul2(s[e - 1], __float2half2_rn(0.25f)) : s[0];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if constexpr (BITS == 8) {
+      if constexpr (FMT == FMT_INT4 || BITS == 4) {
+        o[4 * q] = weight(cw[q] << 6);
+        o[4 * q + 1] = weight(cw[q] << 2);
+        o[4 * q + 2] = weight(cw[q] >> 2);
+        o[4 * q + 3] = weight(cw[q] >> 6);
+      } else if constexpr (BITS == 8) {
         const uint32_t w0 = cw[2 * q], w1 = cw[2 * q + 1];
         const uint32_t t0 = __byte_perm(w0, w1, 0x5140), t1 = __byte_perm(w0, w1, 0x7362);  // (0 4 1 5) (2 6 3 7)
-        o[4 * q] = fma2(__byte_perm(t0, 0u, 0x4140), s[0], z2);
-        o[4 * q + 1] = fma2(__byte_perm(t0, 0u, 0x4342), s[0], z2);
-        o[4 * q + 2] = fma2(__byte_perm(t1, 0u, 0x4140), s[0], z2);
-        o[4 * q + 3] = fma2(__byte_perm(t1, 0u, 0x4342), s[0], z2);
+        o[4 * q] = weight(__byte_perm(t0, 0u, 0x4140) << TOP);
+        o[4 * q + 1] = weight(__byte_perm(t0, 0u, 0x4342) << TOP);
+        o[4 * q + 2] = weight(__byte_perm(t1, 0u, 0x4140) << TOP);
+        o[4 * q + 3] = weight(__byte_perm(t1, 0u, 0x4342) << TOP);
       } else {
         const uint32_t u = __byte_perm(cw[q >> 1] >> (16 * (q & 1)), 0u, 0x4140);  // codes 0-3 in byte 0, 4-7 in byte 2
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[4 * q + e] = fma2(u & (0x00030003u << (2 * e)), s[e], z2);
+        for (int e = 0; e < 4; ++e) o[4 * q + e] = weight(u << (TOP - 2 * e));
       }
     }
-  } else {  // int6: fields f = q & 63, q = (f ^ 32) - 32; two 16-weight groups
-    const float step = f16_bits_to_f32(st) * sc * UP;
+  } else {  // int6: fields f = q + 32 (the code's sign bit flipped) as 1024 + f; two 16-weight groups
+    const float step = f16_bits_to_f32(st) * sc;
     const __half2 s[2] = {__float2half2_rn((float)(int8_t)gm * step), __float2half2_rn((float)(int8_t)(gm >> 8) * step)};
-    const __half2 m32 = __float2half2_rn(-32.f / 16777216.f);
-    const __half2 z[2] = {__hmul2(s[0], m32), __hmul2(s[1], m32)};
+    const __half2 m1056 = __float2half2_rn(1056.f);
+    auto weight = [&](uint32_t f, __half2 sq) { return word_of(__hmul2(__hsub2(half2_of(f ^ 0x64206420u), m1056), sq)); };
     if constexpr (FMT == FMT_INT6P) {
       const uint4 l = *reinterpret_cast<const uint4 *>(src);
       const uint2 h = *reinterpret_cast<const uint2 *>(src_hi);
@@ -540,11 +540,10 @@ QL_DEVI void gated_chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], cons
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t u = __byte_perm(hi[q], 0u, 0x4140);
-        const __half2 sq = s[q >> 1], zq = z[q >> 1];
-        o[4 * q] = fma2(((c[q] & 0x000F000Fu) | ((u << 4) & 0x00300030u)) ^ 0x00200020u, sq, zq);
-        o[4 * q + 1] = fma2((((c[q] >> 4) & 0x000F000Fu) | ((u << 2) & 0x00300030u)) ^ 0x00200020u, sq, zq);
-        o[4 * q + 2] = fma2((((c[q] >> 8) & 0x000F000Fu) | (u & 0x00300030u)) ^ 0x00200020u, sq, zq);
-        o[4 * q + 3] = fma2((((c[q] >> 12) & 0x000F000Fu) | ((u >> 2) & 0x00300030u)) ^ 0x00200020u, sq, zq);
+        o[4 * q] = weight((c[q] & 0x000F000Fu) | ((u << 4) & 0x00300030u), s[q >> 1]);
+        o[4 * q + 1] = weight(((c[q] >> 4) & 0x000F000Fu) | ((u << 2) & 0x00300030u), s[q >> 1]);
+        o[4 * q + 2] = weight(((c[q] >> 8) & 0x000F000Fu) | (u & 0x00300030u), s[q >> 1]);
+        o[4 * q + 3] = weight(((c[q] >> 12) & 0x000F000Fu) | ((u >> 2) & 0x00300030u), s[q >> 1]);
       }
     } else {  // eight 24-bit units of four codes
       const uint2 *s2 = reinterpret_cast<const uint2 *>(src);
@@ -555,11 +554,10 @@ QL_DEVI void gated_chunk_to_f16(const uint32_t (&cw)[code_bits(FMT, BITS)], cons
       for (int q = 0; q < 4; ++q) {
         const uint32_t a = __byte_perm(u[2 * q], u[2 * q + 1], 0x5410);
         const uint32_t b = __byte_perm(u[2 * q] >> 12, u[2 * q + 1] >> 12, 0x5410);
-        const __half2 sq = s[q >> 1], zq = z[q >> 1];
-        o[4 * q] = fma2((a & 0x003F003Fu) ^ 0x00200020u, sq, zq);
-        o[4 * q + 1] = fma2(((a >> 6) & 0x003F003Fu) ^ 0x00200020u, sq, zq);
-        o[4 * q + 2] = fma2((b & 0x003F003Fu) ^ 0x00200020u, sq, zq);
-        o[4 * q + 3] = fma2(((b >> 6) & 0x003F003Fu) ^ 0x00200020u, sq, zq);
+        o[4 * q] = weight(a & 0x003F003Fu, s[q >> 1]);
+        o[4 * q + 1] = weight((a >> 6) & 0x003F003Fu, s[q >> 1]);
+        o[4 * q + 2] = weight(b & 0x003F003Fu, s[q >> 1]);
+        o[4 * q + 3] = weight((b >> 6) & 0x003F003Fu, s[q >> 1]);
       }
     }
   }
