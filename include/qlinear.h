@@ -474,9 +474,12 @@ ql_status qlinear_gemm_dx_workspace_bytes(const ql_desc *desc, int64_t M, size_t
 /* Input gradient of the layer: dx[M][K] (bf16) = dy[M][N] (bf16) . W, any
  * M >= 1 and every N and K of the format.  On the tcgen05 tensor cores, the
  * dequantisation fused: each dy row is scaled to fp16 against the power-of-two
- * scales that the weight rows get (as qlinear_gemm's operands, rounded once
- * each), fp32 accumulation, one rounding to bf16.  Results do not depend on
- * timing (split sums are added in a fixed order).
+ * scales that the weight rows get, one rounding an element; the weights are
+ * those of qlinear_gated's GEMM form; fp32 accumulation, one rounding to bf16.
+ * A column of dx depends on that column of W alone, so what a group keeps that
+ * lies far below its row's largest is what its columns have where it does so in
+ * every row.  Results do not depend on timing (split sums are added in a fixed
+ * order).
  * `workspace`: at least qlinear_gemm_dx_workspace_bytes(), 256-byte aligned,
  * overwritten; calls sharing one must not overlap on the GPU.  dx must not
  * overlap dy.

@@ -14,13 +14,15 @@
 //
 // Operands are fp16 with exact power-of-two scales, as in the forward GEMM (gemm_prep.cuh).  A weight row's
 // scale 2^b_n cannot be undone after a sum over rows, so its inverse goes into the other operand:
-//     dx[m][k] = 2^-a_m sum_n (dy[m][n] 2^(a_m - b_n)) (w[n][k] 2^b_n),
+//     dx[m][k] = 2^-(a_m + w_top) sum_n (dy[m][n] 2^(a_m + w_top - b_n)) (w[n][k] 2^b_n),
 // with a_m chosen so that the row's largest scaled magnitude lies in [2^14, 2^15).
 //
-// A code enters the arithmetic as it lies: masked into the low ten bits of a half it is the subnormal
-// q 2^-24, so one mask and one fused multiply-add (with 2^24 times the scale) make a weight, without the
-// detour through 1024 + q.  For 2^24 times the scale to be an fp16 number the scaled weights sit lower than in
-// the forward kernels, below 2^-5 (4-bit affine 2^-6, 2-bit 2^-9); fp16 has 2^15 and more of range below that.
+// Codes become weights as in the gated GEMM (gated_chunk_to_f16): 4-, 2- and 8-bit codes shifted to the top of a half's
+// mantissa are subnormals, and one fused multiply-add with the inverse power in the scale makes a weight below 1; int6
+// goes through 1024 + f.  A column of dx depends on that column of W alone, so the range below a row's largest weight
+// matters here: a group whose largest weight is 2^-13 of it has its weights to 2^-11 of that one, a smaller group one bit
+// less a power of two (int6: 2^-28).  (A subtraction from 1024 + q as in the forward GEMM reaches 2^-28 for all; equal at
+// M = 2048, but K = 5120, N = 27648, M = 4 took 45.1 us against 41.5.)
 //
 // Passes: (1) row exponents b_n; (2) dy to scaled fp16 rows; (3) the scaled group metadata, transposed so that a
 // stage's words are one TMA box; (4) the GEMM; (5) the sum of the parts of split tiles.
@@ -33,8 +35,8 @@
 //
 // Workspace (256-byte aligned sections, Np = N rounded up to 64):
 //   dy16   fp16 [M][Np]      scaled dy, zeros past N
-//   dexp   s32  [M]          -(a_m + DY_BIAS)
-//   rowexp u8   [Np]         exponent byte of 2^(DY_BIAS - b_n)
+//   dexp   s32  [M]          -(a_m + w_top)
+//   rowexp u8   [Np]         exponent byte of 2^(w_top - b_n), 0 for rows of zeros
 //   meta   u32  [K / gran][Np]  scaled metadata of a run of gran weights, two words for each two rows n, n + 1
 //                            of fp16 pairs: their scales, then their offsets (int4 -Z S, affine b; int6 the scales
 //                            of the run's two 16-groups); zeros past N
@@ -74,6 +76,7 @@ struct Workspace {
   uint8_t *rowexp;
   uint32_t *meta;
   float *partial;
+  int w_top;  // of the layer's format
 };
 
 inline size_t workspace_bytes(int64_t M, int64_t N, int64_t K, int g) {
@@ -82,7 +85,7 @@ inline size_t workspace_bytes(int64_t M, int64_t N, int64_t K, int g) {
          (size_t)2 * DX_CTAS * ctas_per_sm(tile_class(M)) * tile_tokens(M) * BKT * 4;
 }
 
-inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
+inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g, int w_top) {
   const size_t np = (size_t)padded_n(N);
   uint8_t *p = static_cast<uint8_t *>(base);
   Workspace w;
@@ -95,6 +98,7 @@ inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
   w.meta = reinterpret_cast<uint32_t *>(p);
   p += align256((size_t)(K / g) * np * 4);
   w.partial = reinterpret_cast<float *>(p);
+  w.w_top = w_top;
   return w;
 }
 
@@ -104,63 +108,101 @@ inline Workspace carve(void *base, int64_t M, int64_t N, int64_t K, int g) {
 // With few tokens pass 2 has few CTAs, and passes 2 and 3 run side by side.
 
 // ---- pass 1: row exponents ------------------------------------------------------------------------
-// Eight lanes a row.  The bound on a row's weights need not be tight -- a looser one only moves the fp16 weights
-// down, and they have 2^29 of range below the top -- so int4 and int6 take it from the steps alone: codes of
-// 255 (int6: -128) times the step.
+// b_n puts the bound on row n's weights that its group words give (as the forward kernels', see gemm_prep.cuh) into
+// [2^w_top, 2 2^w_top).  The row factor 2^(w_top - b_n) that multiplies dy, the power of two at or below that bound, is
+// kept as its exponent byte: a product of dy and it is out of range only where dx is.  A row of zeros has the factor 0,
+// so that its dy does not count in a token's scale.
 //
-// The row factor 2^(DY_BIAS - b_n) that multiplies dy is kept as its exponent byte; the bias brings the
-// factor of ordinary weights (b_n about -4) near 1, so that dy times it stays in range whenever dy does.
-constexpr int DY_BIAS = -4, RE_ROWS = 32, RE_THREADS = 8 * RE_ROWS;
-// the exponent that a row's bound gets: the largest scale, at most bound / 15 (int4), bound / 32 (int6) or
-// 2 bound / (2^bits - 1) (affine), times 2^24 has to stay below 65504
-__host__ __device__ constexpr int w_top(int fmt, int bits) {
-  return fmt != FMT_AFFINE || bits == 8 ? -6 : bits == 4 ? -7 : -10;
+// 16 lanes a row, or 32 where the rows are few for the GPU and a row has a word for each lane (int4, M = 4: N = 5120,
+// K = 27648 39.6 us a call against 43.7, N = 27648, K = 5120 41.5 against 40.5; the call took 37.5 with bounds from
+// the steps alone, which a large step that no group uses makes useless).
+constexpr int RE_THREADS = 256;
+__host__ __device__ constexpr int w_top(int fmt) { return fmt == FMT_INT6 || fmt == FMT_INT6P ? 14 : -1; }
+__host__ __device__ constexpr int64_t meta_words(int fmt, int64_t K, int G) { return fmt == FMT_AFFINE ? K / G : K / 256; }
+inline int row_exp_lanes(int fmt, int64_t N, int64_t K, int G) {
+  return N <= DX_CTAS * 64 && meta_words(fmt, K, G) >= 32 ? 32 : 16;
 }
 constexpr int WP_ROWS = 64, WP_RUNS = 64, WP_THREADS = 256;
 
+// Byte i of a word in the mantissa of 2^23
+QL_DEVI float byte_of(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | i)); }
+
+// Group words and step word of one super-block (int4, int6: 16 bytes of group words) or group (affine) of a row,
+// and a bound on its weights.  Words of zeros have the bound 0.
+template <int FMT>
+struct MetaWords {
+  uint4 g;
+  uint32_t s;
+};
+template <>
+struct MetaWords<FMT_AFFINE> {
+  uint32_t g;
+};
+template <int FMT>
+QL_DEVI MetaWords<FMT> load_meta_words(const uint8_t *gmeta, const uint8_t *steps, int64_t at) {
+  if constexpr (FMT == FMT_AFFINE) return {__ldg(reinterpret_cast<const uint32_t *>(gmeta) + at)};
+  else if constexpr (FMT == FMT_INT4)
+    return {__ldg(reinterpret_cast<const uint4 *>(gmeta) + at), __ldg(reinterpret_cast<const uint32_t *>(steps) + at)};
+  else
+    return {__ldg(reinterpret_cast<const uint4 *>(gmeta) + at),
+            (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(steps) + at)};
+}
 template <int FMT, int BITS>
-QL_DEVI float meta_bound(const uint8_t *gmeta, const uint8_t *steps, int64_t n, int64_t i, int64_t K, int G) {
-  if constexpr (FMT == FMT_INT4) {
-    const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(steps) + n * (K / 256) + i);
-    return 255.f * fabsf(f16_bits_to_f32(s)) * fmaxf(15.f, 255.f * fabsf(f16_bits_to_f32(s >> 16)));
-  } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
-    return 4096.f * fabsf(f16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t *>(steps) + n * (K / 256) + i)));
-  } else {
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(gmeta) + n * (K / G) + i);
-    const float s = bf16_bits_to_f32(c), b = bf16_bits_to_f32(c >> 16);
+QL_DEVI float meta_bound(const MetaWords<FMT> &m) {
+  if constexpr (FMT == FMT_AFFINE) {
+    const float s = bf16_bits_to_f32(m.g), b = bf16_bits_to_f32(m.g >> 16);
     return fmaxf(fabsf(b), fabsf(fmaf((float)((1 << BITS) - 1), s, b)));
+  } else {
+    const uint32_t w[4] = {m.g.x, m.g.y, m.g.z, m.g.w};
+    if constexpr (FMT == FMT_INT4) {
+      const float zs = f16_bits_to_f32(m.s >> 16), nzs = -8388608.f * zs;
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float Z = fmaf(byte_of(w[j >> 1], 2 * (j & 1) + 1), zs, nzs);
+        top = fmaxf(top, (byte_of(w[j >> 1], 2 * (j & 1)) - 8388608.f) * fmaxf(fabsf(Z), fabsf(15.f - Z)));
+      }
+      return top * fabsf(f16_bits_to_f32(m.s));
+    } else {
+      uint32_t hi = 0x00800080u, lo = 0x00800080u;  // of the codes plus 128, two a word
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t c = w[j] ^ 0x80808080u, a = c & 0x00FF00FFu, b = (c >> 8) & 0x00FF00FFu;
+        hi = __vmaxu2(hi, __vmaxu2(a, b));
+        lo = __vminu2(lo, __vminu2(a, b));
+      }
+      const int top = max((int)max(hi & 0xFFFFu, hi >> 16) - 128, 128 - (int)min(lo & 0xFFFFu, lo >> 16));
+      return 32.f * (float)top * fabsf(f16_bits_to_f32(m.s));
+    }
   }
 }
 
-template <int FMT, int BITS>
+template <int FMT, int BITS, int LANES>
 __global__ void __launch_bounds__(RE_THREADS) row_exp_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
                                                              int64_t K, int G, Workspace ws) {
-  const int sub = threadIdx.x & 7;
-  const int64_t n = (int64_t)blockIdx.x * RE_ROWS + (threadIdx.x >> 3);  // < Np
-  const int64_t words = FMT == FMT_AFFINE ? K / G : K / 256;
+  const int sub = threadIdx.x % LANES;
+  const int64_t n = (int64_t)blockIdx.x * (RE_THREADS / LANES) + threadIdx.x / LANES;  // < Np
+  const int64_t words = n < N ? meta_words(FMT, K, G) : 0, first = n * words;
   pdl_wait();
   pdl_launch_dependents();
   float top = 0.f;
-  if (n < N) {
-#pragma unroll 8
-    for (int64_t i = sub; i < words; i += 8) top = fmaxf(top, meta_bound<FMT, BITS>(gmeta, steps, n, i, K, G));
-  }
+#pragma unroll 1
+  for (int64_t i = sub; i < words; i += LANES)
+    top = fmaxf(top, meta_bound<FMT, BITS>(load_meta_words<FMT>(gmeta, steps, first + i)));
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  // at most 120, so that 127 + DY_BIAS - b is an exponent byte (weights below 2^-126 lose bits then)
-  const int b = n < N ? min(scale_exponent(top, w_top(FMT, BITS)), 120) : DY_BIAS;
-  if (sub == 0) ws.rowexp[n] = (uint8_t)(127 + DY_BIAS - b);
+  for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // b in [-126, 120], so that it and 127 + w_top - b are exponents: rows below 2^-106 lie lower, and affine weights of
+  // 2^126 and more are out of range
+  constexpr int TOP = w_top(FMT);
+  if (sub == 0) ws.rowexp[n] = (uint8_t)(top == 0.f ? 0 : 127 + TOP - min(scale_exponent(top, TOP), 120));
 }
 
 // ---- pass 2: dy (or (dg | du)) to scaled fp16 rows ----------------------------------------------------
-// One CTA a token row; an element enters the product as v 2^(DY_BIAS - b_n) 2^a, the row's a from a bound on
+// One CTA a token row; an element enters the product as v 2^(w_top - b_n) 2^a, the row's a from a bound on
 // its scaled magnitudes.
 
 // The exponent bytes of four rows -> their factors, i = 0..3
 QL_DEVI float row_factor(uint32_t bytes, int i) { return __uint_as_float(__byte_perm(bytes, 0u, 0x0444 | (i << 12)) >> 1); }
-
-// Byte i of a word in the mantissa of 2^23
-QL_DEVI float byte_of(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | i)); }
 
 // The largest value of every thread's v over the CTA.
 template <int THREADS>
@@ -263,7 +305,7 @@ __global__ void __launch_bounds__(DY_THREADS) dy_prep_kernel(const __nv_bfloat16
     for (int64_t i = threadIdx.x; i < nv; i += DY_THREADS) out[i] = put8(load8<VEC>(row, 8 * i, N), fac[i], sc);
   }
   if (threadIdx.x < np / 8 - nv) out[nv + threadIdx.x] = zero;
-  if (threadIdx.x == 0) ws.dexp[m] = -(a + DY_BIAS);
+  if (threadIdx.x == 0) ws.dexp[m] = -(a + ws.w_top);
 }
 
 struct GatedGrad {
@@ -379,39 +421,43 @@ __global__ void __launch_bounds__(THREADS) dgu_prep_kernel(GatedGrad p, Workspac
     }
   }
   if (threadIdx.x < p.np - N) out[N + threadIdx.x] = __float2half_rn(0.f);
-  if (threadIdx.x == 0) ws.dexp[m] = -(a + DY_BIAS);
+  if (threadIdx.x == 0) ws.dexp[m] = -(a + ws.w_top);
 }
 
 // ---- pass 3: scaled metadata, transposed ------------------------------------------------------------
 // Two neighbouring runs' metadata (gran weights each; int4 and int6: of one super-block) from their group words --
 // the two in w0 (int4, int6) or one each in w0 and w1 (affine) -- and their step word, for a row with sc = 2^b_n:
-// the scales times 2^24 sc; -Z S and b times sc.  The powers of two are exact, so they go into the steps first.
-// Byte codes become floats by a permute into the mantissa of 2^23 (a conversion unit has a quarter of the rate).
-constexpr float SUB = 16777216.f;  // 2^24
-template <int FMT>
+// the scales times sc and what undoes the codes' place in a half, 2^code_up; -Z S and b times sc.  The powers of two
+// are exact, so they go into the steps first.  Byte codes become floats by a permute into the mantissa of 2^23 (a
+// conversion unit has a quarter of the rate).
+__host__ __device__ constexpr int code_up(int fmt, int bits) {  // int6's codes are whole numbers
+  return fmt == FMT_INT6 || fmt == FMT_INT6P ? 0 : 14 + bits;
+}
+template <int FMT, int BITS>
 QL_DEVI void scaled_meta(uint32_t w0, uint32_t w1, uint32_t s, float sc, uint32_t (&o)[2]) {
+  constexpr float UP = (float)(1 << code_up(FMT, BITS));
   if constexpr (FMT == FMT_INT4) {
-    const float ss = f16_bits_to_f32(s) * sc * SUB, zs = f16_bits_to_f32(s >> 16) * (-1.f / SUB);
+    const float ss = f16_bits_to_f32(s) * sc * UP, zs = f16_bits_to_f32(s >> 16) * (-1.f / UP);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float S = __fmul_rn(byte_of(w0, 2 * i) - 8388608.f, ss);
       o[i] = pack_f16x2(S, __fmul_rn(byte_of(w0, 2 * i + 1) - 8388608.f, zs) * S);
     }
   } else if constexpr (FMT == FMT_INT6 || FMT == FMT_INT6P) {
-    const float st = f16_bits_to_f32(s) * sc * SUB;
+    const float st = f16_bits_to_f32(s) * sc;
     w0 ^= 0x80808080u;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       o[i] = pack_f16x2(__fmul_rn(byte_of(w0, 2 * i) - 8388736.f, st), __fmul_rn(byte_of(w0, 2 * i + 1) - 8388736.f, st));
   } else {
-    o[0] = pack_f16x2(bf16_bits_to_f32(w0) * sc * SUB, bf16_bits_to_f32(w0 >> 16) * sc);
-    o[1] = pack_f16x2(bf16_bits_to_f32(w1) * sc * SUB, bf16_bits_to_f32(w1 >> 16) * sc);
+    o[0] = pack_f16x2(bf16_bits_to_f32(w0) * sc * UP, bf16_bits_to_f32(w0 >> 16) * sc);
+    o[1] = pack_f16x2(bf16_bits_to_f32(w1) * sc * UP, bf16_bits_to_f32(w1 >> 16) * sc);
   }
 }
 
 // A CTA turns the words of 64 rows x 64 runs through shared memory, read along the row and written along n.  About 10 us
 // for 27648 x 160 runs (28 MB in and out; with a conversion a byte and a word a store it was 13.2), issue 70 %.
-template <int FMT>
+template <int FMT, int BITS>
 __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, const uint8_t *steps, int64_t N,
                                                           int64_t K, int G, int64_t np, Workspace ws) {
   constexpr int RW = WP_ROWS / (WP_THREADS / 32);  // rows a warp
@@ -445,11 +491,11 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
   const uint2 eb = *reinterpret_cast<const uint2 *>(ws.rowexp + first);
 #pragma unroll
   for (int j = 0; j < RW; ++j) {
-    // 2^b_n from the byte 127 + DY_BIAS - b_n, b_n in [-126, 120]
+    // 2^b_n from the byte 127 + w_top - b_n, b_n in [-126, 120]; any for rows of zeros
     const uint32_t byte = ((j < 4 ? eb.x : eb.y) >> (8 * (j & 3))) & 0xFFu;
-    const float sc = __uint_as_float((uint32_t)(254 + DY_BIAS - (int)byte) << 23);
+    const float sc = __uint_as_float((uint32_t)min(254 + w_top(FMT) - (int)byte, 254) << 23);
     uint32_t o[2];
-    scaled_meta<FMT>(c[j][0], c[j][1], st[j], sc, o);
+    scaled_meta<FMT, BITS>(c[j][0], c[j][1], st[j], sc, o);
     const int row = RW * warp + j, at = (row >> 1) + WP_ROWS / 2 * (row & 1);
     turn[at][lane] = o[0];
     turn[at][WP_RUNS / 2 + lane] = o[1];
@@ -629,9 +675,15 @@ QL_DEVI void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
 
 // A warp's 32 k (quarter wq of the tile's 128) of a stage's 64 rows: its code tile at shared address `codes`, its
 // metadata words at `meta` + the thread's offset -> the words of lanes 0-15 (lo) and 16-31 (hi) of the quarter.
-// A mask leaves codes in bits 0-3 or 4-7 of the halves (2-bit: 0-1 to 6-7), which the scale makes up for.
 template <int FMT, int BITS>
 QL_DEVI void decode_stage(uint32_t codes, uint32_t meta, int wq, int lane, uint32_t (&lo)[16], uint32_t (&hi)[16]) {
+  // codes at the top of a half's mantissa, its lowest bit bit TOP; int6 fields f = (q & 63) ^ 32 = q + 32 as 1024 + f
+  constexpr int TOP = 10 - BITS;
+  constexpr uint32_t MASK = 0x00010001u * (uint32_t)(1024 - (1 << TOP)), M6 = 0x64206420u;
+  auto weight6 = [](uint32_t f, __half2 s) {
+    const __half2 w = __hmul2(__hsub2(as_h2(f), __float2half2_rn(1056.f)), s);
+    return *reinterpret_cast<const uint32_t *>(&w);
+  };
   if constexpr (FMT == FMT_INT4 || (FMT == FMT_AFFINE && BITS == 4)) {  // rows of 64 bytes, 64-byte swizzle
     uint32_t c[8];
 #pragma unroll
@@ -642,12 +694,11 @@ QL_DEVI void decode_stage(uint32_t codes, uint32_t meta, int wq, int lane, uint3
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint2 m = lds_u2(meta + 32 * j);
-      const __half2 s0 = as_h2(m.x), s1 = __hmul2(s0, __float2half2_rn(0.0625f)), z = as_h2(m.y);
-      const uint32_t c8 = c[j] >> 8;
-      lo[2 * j] = fma_h2(c[j] & 0x000F000Fu, s0, z);
-      lo[2 * j + 1] = fma_h2(c[j] & 0x00F000F0u, s1, z);
-      hi[2 * j] = fma_h2(c8 & 0x000F000Fu, s0, z);
-      hi[2 * j + 1] = fma_h2(c8 & 0x00F000F0u, s1, z);
+      const __half2 s = as_h2(m.x), z = as_h2(m.y);
+      lo[2 * j] = fma_h2((c[j] << 6) & MASK, s, z);
+      lo[2 * j + 1] = fma_h2((c[j] << 2) & MASK, s, z);
+      hi[2 * j] = fma_h2((c[j] >> 2) & MASK, s, z);
+      hi[2 * j + 1] = fma_h2((c[j] >> 6) & MASK, s, z);
     }
   } else if constexpr (FMT == FMT_AFFINE && BITS == 8) {  // rows of 128 bytes, 128-byte swizzle
     uint32_t c[2][8];
@@ -662,10 +713,10 @@ QL_DEVI void decode_stage(uint32_t codes, uint32_t meta, int wq, int lane, uint3
     for (int j = 0; j < 8; ++j) {
       const uint2 m = lds_u2(meta + 32 * j);
       const __half2 s = as_h2(m.x), z = as_h2(m.y);
-      lo[2 * j] = fma_h2(c[0][j] & 0x00FF00FFu, s, z);
-      lo[2 * j + 1] = fma_h2(__byte_perm(c[0][j], 0u, 0x4341), s, z);
-      hi[2 * j] = fma_h2(c[1][j] & 0x00FF00FFu, s, z);
-      hi[2 * j + 1] = fma_h2(__byte_perm(c[1][j], 0u, 0x4341), s, z);
+      lo[2 * j] = fma_h2((c[0][j] << 2) & MASK, s, z);
+      lo[2 * j + 1] = fma_h2((c[0][j] >> 6) & MASK, s, z);
+      hi[2 * j] = fma_h2((c[1][j] << 2) & MASK, s, z);
+      hi[2 * j + 1] = fma_h2((c[1][j] >> 6) & MASK, s, z);
     }
   } else if constexpr (FMT == FMT_AFFINE) {  // 2-bit: rows of 32 bytes, two 64-k halves
     uint32_t c[8];
@@ -674,60 +725,54 @@ QL_DEVI void decode_stage(uint32_t codes, uint32_t meta, int wq, int lane, uint3
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint2 m = lds_u2(meta + 32 * j);
-      const __half2 quarter = __float2half2_rn(0.25f), z = as_h2(m.y);
-      const __half2 s0 = as_h2(m.x), s1 = __hmul2(s0, quarter), s2 = __hmul2(s1, quarter), s3 = __hmul2(s2, quarter);
+      const __half2 s = as_h2(m.x), z = as_h2(m.y);
       const uint32_t v = c[j] >> (8 * (wq & 1));
-      lo[2 * j] = fma_h2(v & 0x00030003u, s0, z);
-      lo[2 * j + 1] = fma_h2(v & 0x000C000Cu, s1, z);
-      hi[2 * j] = fma_h2(v & 0x00300030u, s2, z);
-      hi[2 * j + 1] = fma_h2(v & 0x00C000C0u, s3, z);
+      lo[2 * j] = fma_h2((v << 8) & MASK, s, z);
+      lo[2 * j + 1] = fma_h2((v << 6) & MASK, s, z);
+      hi[2 * j] = fma_h2((v << 4) & MASK, s, z);
+      hi[2 * j + 1] = fma_h2((v << 2) & MASK, s, z);
     }
-  } else {  // int6: fields f = q & 63, q = (f ^ 32) - 32
-    const __half2 m32 = __float2half2_rn(-32.f / SUB);
-    if constexpr (FMT == FMT_INT6P) {  // nibbles as int4, then the high plane, rows of 32 bytes for 128 k
-      uint32_t c[8], h[8];
-      const int g = lane >> 2;
-      // thread t needs the high fields of nibble column t / 4: a byte of the high plane's column 4 (wq & 1) + t / 8
-      const int src = 4 * (4 * (wq & 1) + (g >> 1)) + (lane & 3);
+  } else if constexpr (FMT == FMT_INT6P) {  // nibbles as int4, then the high plane, rows of 32 bytes for 128 k
+    uint32_t c[8], h[8];
+    const int g = lane >> 2;
+    // thread t needs the high fields of nibble column t / 4: a byte of the high plane's column 4 (wq & 1) + t / 8
+    const int src = 4 * (4 * (wq & 1) + (g >> 1)) + (lane & 3);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int n = 32 * x + lane;
-        ldmatrix_x4_trans(codes + n * 64 + ((wq ^ ((n >> 1) & 3)) << 4), c + 4 * x);
-        ldmatrix_x4_trans(codes + BN * 64 + n * 32 + 16 * (wq >> 1), h + 4 * x);
-      }
+    for (int x = 0; x < 2; ++x) {
+      const int n = 32 * x + lane;
+      ldmatrix_x4_trans(codes + n * 64 + ((wq ^ ((n >> 1) & 3)) << 4), c + 4 * x);
+      ldmatrix_x4_trans(codes + BN * 64 + n * 32 + 16 * (wq >> 1), h + 4 * x);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __half2 s = as_h2(lds_u1(meta + 32 * j + (g & 4))), z = __hmul2(s, m32);  // 16-weight groups: g / 4
-        const uint32_t hv = __shfl_sync(0xffffffffu, h[j], src) >> (8 * (g & 1));
-        lo[2 * j] = fma_h2(((c[j] & 0x000F000Fu) | ((hv << 4) & 0x00300030u)) ^ 0x00200020u, s, z);
-        lo[2 * j + 1] = fma_h2((((c[j] >> 4) & 0x000F000Fu) | ((hv << 2) & 0x00300030u)) ^ 0x00200020u, s, z);
-        hi[2 * j] = fma_h2((((c[j] >> 8) & 0x000F000Fu) | (hv & 0x00300030u)) ^ 0x00200020u, s, z);
-        hi[2 * j + 1] = fma_h2((((c[j] >> 12) & 0x000F000Fu) | ((hv >> 2) & 0x00300030u)) ^ 0x00200020u, s, z);
-      }
-    } else {
-      // dense: thread t takes row t / 4 of eight and, of each 8 codes (two 24-bit units), codes t % 4 and 4 + t % 4 as
-      // the elements 2 (t % 4), + 1 of an 8 x 8 matrix, which movmatrix transposes: row p is k = p / 2 + 4 (p % 2)
-      const int g = lane >> 2, sh = 6 * (lane & 3);
+    for (int j = 0; j < 8; ++j) {
+      const __half2 s = as_h2(lds_u1(meta + 32 * j + (g & 4)));  // 16-weight groups: g / 4
+      const uint32_t hv = __shfl_sync(0xffffffffu, h[j], src) >> (8 * (g & 1));
+      lo[2 * j] = weight6(((c[j] & 0x000F000Fu) | ((hv << 4) & 0x00300030u)) ^ M6, s);
+      lo[2 * j + 1] = weight6((((c[j] >> 4) & 0x000F000Fu) | ((hv << 2) & 0x00300030u)) ^ M6, s);
+      hi[2 * j] = weight6((((c[j] >> 8) & 0x000F000Fu) | (hv & 0x00300030u)) ^ M6, s);
+      hi[2 * j + 1] = weight6((((c[j] >> 12) & 0x000F000Fu) | ((hv >> 2) & 0x00300030u)) ^ M6, s);
+    }
+  } else {
+    // dense int6: thread t takes row t / 4 of eight and, of each 8 codes (two 24-bit units), codes t % 4 and 4 + t % 4
+    // as the elements 2 (t % 4), + 1 of an 8 x 8 matrix, which movmatrix transposes: row p is k = p / 2 + 4 (p % 2)
+    const int g = lane >> 2, sh = 6 * (lane & 3);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t row = codes + (8 * j + g) * code_row(FMT, BITS) + 24 * wq;
-        const uint2 x = lds_u2(row), y = lds_u2(row + 8), w = lds_u2(row + 16);
-        const uint32_t u[8] = {x.x, __funnelshift_r(x.x, x.y, 24), __funnelshift_r(x.y, y.x, 16), y.x >> 8,
-                               y.y, __funnelshift_r(y.y, w.x, 24), __funnelshift_r(w.x, w.y, 16), w.y >> 8};
-        const uint2 m = lds_u2(meta + 32 * j);
-        const __half2 s[2] = {as_h2(m.x), as_h2(m.y)};
-        const __half2 z[2] = {__hmul2(s[0], m32), __hmul2(s[1], m32)};
-        uint32_t o[4];
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t row = codes + (8 * j + g) * code_row(FMT, BITS) + 24 * wq;
+      const uint2 x = lds_u2(row), y = lds_u2(row + 8), w = lds_u2(row + 16);
+      const uint32_t u[8] = {x.x, __funnelshift_r(x.x, x.y, 24), __funnelshift_r(x.y, y.x, 16), y.x >> 8,
+                             y.y, __funnelshift_r(y.y, w.x, 24), __funnelshift_r(w.x, w.y, 16), w.y >> 8};
+      const uint2 m = lds_u2(meta + 32 * j);
+      const __half2 s[2] = {as_h2(m.x), as_h2(m.y)};
+      uint32_t o[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t f = (__byte_perm(u[2 * b] >> sh, u[2 * b + 1] >> sh, 0x5410) & 0x003F003Fu) ^ 0x00200020u;
-          o[b] = fma_h2(movmatrix_trans(f), s[b >> 1], z[b >> 1]);
-        }
-        lo[2 * j] = o[0];
-        lo[2 * j + 1] = o[1];
-        hi[2 * j] = o[2];
-        hi[2 * j + 1] = o[3];
-      }
+      for (int b = 0; b < 4; ++b)
+        o[b] = weight6(movmatrix_trans((__byte_perm(u[2 * b] >> sh, u[2 * b + 1] >> sh, 0x5410) & 0x003F003Fu) ^ M6),
+                    s[b >> 1]);
+      lo[2 * j] = o[0];
+      lo[2 * j + 1] = o[1];
+      hi[2 * j] = o[2];
+      hi[2 * j + 1] = o[3];
     }
   }
 }

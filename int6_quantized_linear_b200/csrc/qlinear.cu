@@ -718,7 +718,7 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
   using namespace ql::dx;
   const int64_t N = d->N, K = d->K, np = padded_n(N);
   const int gr = gran(FMT, d->group);
-  const Workspace ws = carve(workspace, M, N, K, gr);
+  const Workspace ws = carve(workspace, M, N, K, gr, w_top(FMT));
   const auto *gmeta = static_cast<const uint8_t *>(w->gmeta), *steps = static_cast<const uint8_t *>(w->steps);
   Params p;
   p.M = M; p.N = N; p.K = K; p.G = d->group;
@@ -752,10 +752,12 @@ ql_status launch_gemm_dx_tt(const ql_desc *d, const ql_packed_const *w, int64_t 
       return cuda_failed();
     configured_dev = dev;
   }
-  if (!launch_dependent(row_exp_kernel<FMT, BITS>, dim3((unsigned)(np / RE_ROWS)), RE_THREADS, 0, st, gmeta, steps,
-                        N, K, d->group, ws) ||
+  const int lanes = row_exp_lanes(FMT, N, K, d->group);
+  auto *row_exp = lanes == 16 ? row_exp_kernel<FMT, BITS, 16> : row_exp_kernel<FMT, BITS, 32>;
+  if (!launch_dependent(row_exp, dim3((unsigned)(np * lanes / RE_THREADS)), RE_THREADS, 0, st, gmeta, steps, N, K,
+                        d->group, ws) ||
       !prep(ws, np) ||
-      !launch_dependent(meta_kernel<FMT>, dim3((unsigned)(np / WP_ROWS), (unsigned)((K / gr + WP_RUNS - 1) / WP_RUNS)),
+      !launch_dependent(meta_kernel<FMT, BITS>, dim3((unsigned)(np / WP_ROWS), (unsigned)((K / gr + WP_RUNS - 1) / WP_RUNS)),
                         WP_THREADS, 0, st, gmeta, steps, N, K, d->group, np, ws) ||
       !launch_dependent(kern, dim3((unsigned)(p.deal.waves ? p.deal.ctas : p.deal.shares)), NUM_THREADS, smem, st,
                         my, mc, mh, mm, p))
