@@ -354,7 +354,7 @@ QL_DEVI void store8(void *row, int64_t n, int64_t end, const uint32_t (&o)[4]) {
 // A thread takes eight features (half a group of the checkpoint) at a time.  The row's scale comes from a bound that
 // needs no activation -- the eight's largest |dh| times 127 steps of u (slope at most 1.13) or of g -- so every
 // gradient is computed once; the bound's slack costs a few of the 29 powers of two that fp16 has below its
-// top.  The int8 codes become floats by a byte permute and one FMA.  VEC: F % 8 == 0.
+// top.  The int8 codes become floats by a byte permute and a subtraction.  VEC: F % 8 == 0.
 template <int ACT, bool VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) dgu_prep_kernel(GatedGrad p, Workspace ws) {
   __shared__ float red[THREADS / 32];
@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(THREADS) dgu_prep_kernel(GatedGrad p, Workspac
     top = fmaxf(top, dm * su * (MAX_SLOPE * __uint_as_float(max_byte(rg) << 23)));
     top = fmaxf(top, dm * sg * __uint_as_float(max_byte(ru) << 23));
   }
-  const int a = scale_exponent(block_max<THREADS>(top, red), 14);
+  // (the bound may pass the largest float where no gradient does)
+  const int a = scale_exponent(fminf(block_max<THREADS>(top, red), 3.402823466e38f), 14);
   const float sc = exp2i(a);
   __half *out = ws.dy16 + m * p.np;
 #pragma unroll 1
@@ -388,8 +389,6 @@ __global__ void __launch_bounds__(THREADS) dgu_prep_kernel(GatedGrad p, Workspac
     const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
     const uint32_t gw[2] = {qg.x ^ 0x80808080u, qg.y ^ 0x80808080u}, uw[2] = {qu.x ^ 0x80808080u, qu.y ^ 0x80808080u};
     const uint32_t fg[2] = {rg.x, rg.y}, fu[2] = {ru.x, ru.y};
-    // code c as the byte c + 128 in the mantissa of 2^23: value = (2^23 + 128 + c) s - (2^23 + 128) s, exact
-    const float zg = -8388736.f * sg, zu = -8388736.f * su;
     uint32_t og[4], ou[4], bg[4], bu[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -398,8 +397,9 @@ __global__ void __launch_bounds__(THREADS) dgu_prep_kernel(GatedGrad p, Workspac
       for (int h = 0; h < 2; ++h) {
         const int e = 2 * j + h;
         const float dv = h ? __uint_as_float(dw[j] & 0xffff0000u) : __uint_as_float(dw[j] << 16);
-        const float g = fmaf(byte_of(gw[e >> 2], e & 3), sg, zg);
-        const float u = fmaf(byte_of(uw[e >> 2], e & 3), su, zu);
+        // code c as the byte c + 128 in the mantissa of 2^23 (one FMA with (2^23 + 128) s would overflow from s = 2^105)
+        const float g = (byte_of(gw[e >> 2], e & 3) - 8388736.f) * sg;
+        const float u = (byte_of(uw[e >> 2], e & 3) - 8388736.f) * su;
         float av, ad;
         act_grad(ACT, g, av, ad);
         dgv[h] = dv * u * ad;

@@ -5,12 +5,14 @@ for each value and 4e-3 for the norm of the error, the tolerances of tests/test_
 """
 import numpy as np
 import pytest
+import torch
 
 import int6_quantized_linear_b200 as ql
 from int6_quantized_linear_b200 import synth
 from tests.gpu_helpers import Layer, bf16_to_f64, half_ulp_bf16
-from tests.test_gpu_gated import FORMATS, bf16, check_dx, close, f64, out, rms, to_dev, untouched
+from tests.test_gpu_gated import FORMATS, bf16, check_dx, close, f64, layer, out, rms, saved_of, to_dev, untouched
 from tests.test_gpu_gated_ranges import unlike_layer
+from tests import ffn_reference as R
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +84,36 @@ def test_dx_rows_of_unlike_magnitude(cuda, fmt, bits, group, M):
     yb = bf16(y)
     yb[M - 1, [7, 100]] = 0  # one token without them
     check_dx(run_dx(L, yb, M), bf16_to_f64(yb), L.wref, f"{fmt}{bits} rows")
+
+
+@pytest.mark.parametrize("kind", R.ACTS)
+def test_backward_of_large_values(cuda, kind):
+    """g and u up to the largest that the 8-bit form holds (2^127), dh so that the gradients stay in range; and dh up
+    to 2^120 with small u."""
+    F, K = 64, 256
+    L = layer("int4", 2 * F, K, 360)
+    rng = np.random.default_rng(361)
+    es = [20, 60, 90, 104, 105, 110, 118, 122, 126]
+    v = rng.uniform(1.0, 1.9, size=(2 * len(es), 2, F)) * np.where(rng.random((2 * len(es), 2, F)) < 0.5, -1, 1)
+    dh = rng.normal(size=(2 * len(es), F))
+    for i, e in enumerate(es):
+        v[i] *= 2.0 ** e
+        dh[i] *= 2.0 ** -e
+        v[len(es) + i] *= 2.0 ** -10
+        dh[len(es) + i] *= 2.0 ** min(e, 120)
+    M = 2 * len(es)
+    saved, g, u = saved_of(v, M, F)
+    hb = bf16(dh)
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    dgu = torch.empty((M, 2 * F), dtype=torch.bfloat16, device="cuda")
+    ql.qlinear_gated_backward(L.desc, *L.packed(), saved, to_dev(hb), M, kind, dx, dgu=dgu)
+    assert ql.qlinear_sync_status() == ql.QL_OK
+    dh = bf16_to_f64(hb)
+    d = R.gated_backward(np.clip(g, -1e4, 1e4), u, dh, kind)  # past 1e4 the slope is 0 or 1, and act is 0 or g
+    d[:, F:] = np.where(g > 1e4, dh * g, np.where(g < -1e4, 0.0, d[:, F:]))
+    got = f64(dgu)
+    size = np.concatenate((np.abs(dh * u), np.abs(dh * g)), 1)
+    assert np.all(np.abs(got - d) <= half_ulp_bf16(d) * (1 + 1e-3) + 1e-5 * size)
+    gotx, ref = f64(dx), d @ L.wref
+    for m in range(M):
+        close(gotx[m], ref[m], 1e-2 * rms(ref[m]) + half_ulp_bf16(ref[m]), f"row {m}")
