@@ -1,4 +1,5 @@
-"""Input gradients of layers whose groups, rows and metadata differ much in magnitude (GPU only).
+"""Input gradients of layers whose groups, rows and metadata differ much in magnitude, the dealing of split tiles,
+and long rows of dy (GPU only).
 
 A column of dx depends on that column of the weights alone, so small columns are held to their own rms: 1e-2 of it
 for each value and 4e-3 for the norm of the error, the tolerances of tests/test_gpu_gated.
@@ -10,6 +11,7 @@ import torch
 import int6_quantized_linear_b200 as ql
 from int6_quantized_linear_b200 import synth
 from tests.gpu_helpers import Layer, bf16_to_f64, half_ulp_bf16
+from tests.test_gpu_edge_cases import edge_layer
 from tests.test_gpu_gated import FORMATS, bf16, check_dx, close, f64, layer, out, rms, saved_of, to_dev, untouched
 from tests.test_gpu_gated_ranges import unlike_layer
 from tests import ffn_reference as R
@@ -84,6 +86,95 @@ def test_dx_rows_of_unlike_magnitude(cuda, fmt, bits, group, M):
     yb = bf16(y)
     yb[M - 1, [7, 100]] = 0  # one token without them
     check_dx(run_dx(L, yb, M), bf16_to_f64(yb), L.wref, f"{fmt}{bits} rows")
+
+
+@pytest.mark.parametrize("fmt,bits,group", FORMATS)
+def test_dx_edge_inputs(cuda, fmt, bits, group):
+    """tests/edge_inputs' weight categories: a token's dy is zero but for the rows of one category, and the token is
+    held to its own rms.  dy is large enough for the smallest weights' gradients to be normal numbers."""
+    N, K, M = 300, 2048, 42
+    L, cats, names = edge_layer(fmt, N, K, bits, group, seed=25)
+    w = L.oracle_w().astype(np.float64)
+    y = np.random.default_rng(26).normal(size=(M, N)) * 2.0 ** 20
+    y[cats[None, :] != (np.arange(M) % len(names))[:, None]] = 0
+    yb = bf16(y)
+    got, ref = run_dx(L, yb, M), bf16_to_f64(yb) @ w
+    for m in range(M):
+        close(got[m], ref[m], 1e-2 * rms(ref[m]) + half_ulp_bf16(ref[m]), f"{fmt}{bits} {names[m % len(names)]}")
+
+
+# ---- the dealing of tiles ---------------------------------------------------------------------------------------
+
+def dealing(M, N, K):
+    """(tile class, whole waves, tiles of the rest, shares, shares that straddle two tiles, most pieces of a CTA), by
+    the rule in csrc/gemm_dx.cuh."""
+    c = 32 if M <= 32 else 64 if M <= 64 else 256
+    tiles = -(-M // c)
+    tokens = -(-(-(-M // tiles)) // 16) * 16
+    ctas = min(148, torch.cuda.get_device_properties(0).multi_processor_count) * (1 if c == 256 else 2)
+    all_tiles = -(-M // tokens) * -(-K // 128)
+    steps = -(-N // 64)
+    waves, rest = divmod(all_tiles, ctas)
+    shares = max(rest, min(ctas, rest * steps // 8)) if rest else 0
+    begin = [rest * steps * i // max(shares, 1) for i in range(shares + 1)]
+    straddle = [(begin[i + 1] - 1) // steps > begin[i] // steps for i in range(shares)]
+    return c, waves, rest, shares, sum(straddle), waves + (2 if any(straddle) else 1 if rest else 0)
+
+
+# (M, N, K) of each tile class with split tiles alone and behind whole waves; the last has four pieces in a CTA, which
+# takes the two accumulators of small tiles round twice
+DEALS = [(300, 1250, 6400, 256, 0), (2100, 3000, 2304, 256, 1), (700, 700, 14336, 256, 2), (50, 1000, 25600, 64, 0),
+         (50, 1400, 38400, 64, 1), (5, 1000, 25600, 32, 0), (5, 1400, 38400, 32, 1), (20, 600, 76800, 32, 2)]
+
+
+@pytest.mark.parametrize("M,N,K,tile,waves", DEALS)
+def test_dx_split_tiles(cuda, M, N, K, tile, waves):
+    c, w, rest, shares, straddle, pieces = dealing(M, N, K)
+    assert (c, w) == (tile, waves) and rest < shares and shares % rest and straddle > 0, "sizes that the rule splits"
+    assert waves < 2 or pieces == 4
+    L = layer("int4", N, K, 330)
+    yb = bf16(np.random.default_rng(331).normal(size=(M, N)) * 1e-3)
+    got = run_dx(L, yb, M)
+    check_dx(got, bf16_to_f64(yb), L.wref, f"M={M} N={N} K={K}")
+    assert np.array_equal(got, run_dx(L, yb, M))
+
+
+@pytest.mark.parametrize("M,K", [(40, 256 * 148), (20, 256 * 148), (1000, 4736)])
+def test_dx_whole_waves_only(cuda, M, K):
+    c, waves, rest, _, _, _ = dealing(M, 64, K)
+    assert waves >= 1 and rest == 0
+    L = layer("affine", 64, K, 332, 8, 64)
+    yb = bf16(np.random.default_rng(333).normal(size=(M, 64)))
+    check_dx(run_dx(L, yb, M), bf16_to_f64(yb), L.wref, f"M={M}")
+
+
+# ---- long rows of dy --------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N", [9001, 32768 + 8, 33333, 70000])
+@pytest.mark.parametrize("M", [3, 70])
+def test_dx_long_rows(cuda, N, M):
+    """Rows of dy that more threads keep in registers, and rows that are read twice; with and without 16-byte rows."""
+    K = 64
+    L = layer("affine", N, K, 340, 4, 64)
+    yb = bf16(np.random.default_rng(341).normal(size=(M, N)) * 1e-2)
+    check_dx(run_dx(L, yb, M), bf16_to_f64(yb), L.wref, f"N={N}")
+
+
+# ---- the backward pass ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,N,K", [(5, 200, 512), (33, 66, 512), (300, 1000, 512)])
+@pytest.mark.parametrize("fmt,bits,group", FORMATS[4:])
+def test_backward_of_the_other_formats(cuda, fmt, bits, group, M, N, K):
+    F, kind = N // 2, R.ACTS[M % 3]
+    L = layer(fmt, N, K, 350, bits, group)
+    rng = np.random.default_rng(351)
+    saved, g, u = saved_of(rng.normal(size=(M, 2, F)) * 2.0, M, F)
+    hb = bf16(rng.normal(size=(M, F)) * 1e-3)
+    full, dx = out(M, K)
+    ql.qlinear_gated_backward(L.desc, *L.packed(), saved, to_dev(hb), M, kind, dx)
+    assert ql.qlinear_sync_status() == ql.QL_OK
+    check_dx(f64(dx), R.gated_backward(g, u, bf16_to_f64(hb), kind), L.wref, f"{fmt}{bits} M={M}")
+    assert untouched(full, M, K)
 
 
 @pytest.mark.parametrize("kind", R.ACTS)
