@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(WP_THREADS) meta_kernel(const uint8_t *gmeta, 
     gsrc += GB * runs;
     ssrc += SB * (K / 256);
   }
-  const uint2 eb = *reinterpret_cast<const uint2 *>(ws.rowexp + first);
+  // (pass 2 waited for pass 1 before it let this one start; from L2, where its stores are)
+  const uint2 eb = __ldcg(reinterpret_cast<const uint2 *>(ws.rowexp + first));
 #pragma unroll
   for (int j = 0; j < RW; ++j) {
     // 2^b_n from the byte 127 + w_top - b_n, b_n in [-126, 120]; any for rows of zeros

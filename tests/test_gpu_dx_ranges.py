@@ -160,6 +160,54 @@ def test_dx_long_rows(cuda, N, M):
     check_dx(run_dx(L, yb, M), bf16_to_f64(yb), L.wref, f"N={N}")
 
 
+# ---- one workspace for many layers ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [4, 40, 300])
+def test_calls_share_a_workspace(cuda, M):
+    """Layers of unlike scales, one after the other on one stream with one workspace, eager and in a graph: each call
+    gives what it gives with a workspace of its own."""
+    F, K = 192, 512
+    layers = []
+    for i, e in enumerate((0, 6, -4, 9)):
+        w = synth.int4_weights(370 + i, 2 * F, K)
+        w["ss"] = (w["ss"].view(np.float16).astype(np.float64) * 2.0 ** e).astype(np.float16).view(np.uint16)
+        layers.append(of_weights("int4", 2 * F, K, w))
+    rng = np.random.default_rng(375)
+    x, dy = to_dev(bf16(rng.normal(size=(M, K)) * 0.1)), to_dev(bf16(rng.normal(size=(M, 2 * F))))
+    dh = to_dev(bf16(rng.normal(size=(M, F))))
+    need = max(ql.qlinear_gated_workspace_bytes(layers[0].desc, M), ql.qlinear_gemm_dx_workspace_bytes(layers[0].desc, M))
+    bf = lambda r, c: torch.empty((r, c), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+
+    def run(shared, o):
+        for L, (h, saved, dx, dx2) in zip(layers, o):
+            ql.qlinear_gated(L.desc, *L.packed(), x, M, "silu", h, saved=saved, workspace=shared)
+            ql.qlinear_gemm_dx(L.desc, *L.packed(), dy, M, dx, workspace=shared)
+            ql.qlinear_gated_backward(L.desc, *L.packed(), saved, dh, M, "silu", dx2, workspace=shared)
+
+    outs = lambda: [(bf(M, F), ql.alloc_saved8(2 * M, F), bf(M, K), bf(M, K)) for _ in layers]  # noqa: E731
+    want, eager, replayed = outs(), outs(), outs()
+    for L, o in zip(layers, want):
+        ql.qlinear_gated(L.desc, *L.packed(), x, M, "silu", o[0], saved=o[1])
+        torch.cuda.synchronize()
+        ql.qlinear_gemm_dx(L.desc, *L.packed(), dy, M, o[2])
+        torch.cuda.synchronize()
+        ql.qlinear_gated_backward(L.desc, *L.packed(), o[1], dh, M, "silu", o[3])
+        torch.cuda.synchronize()
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        run(ws, eager)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(ws, replayed)
+    for _ in range(5):
+        g.replay()
+    assert ql.qlinear_sync_status() == ql.QL_OK
+    for a in (eager, replayed):
+        for p, q in zip(a, want):
+            assert torch.equal(p[0], q[0]) and torch.equal(p[2], q[2]) and torch.equal(p[3], q[3])
+            assert torch.equal(p[1][0], q[1][0]) and torch.equal(p[1][1], q[1][1])
+
+
 # ---- the backward pass ------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("M,N,K", [(5, 200, 512), (33, 66, 512), (300, 1000, 512)])
