@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(num_threads(TT, CPS), CPS)
       // so a tile is first moved as it is to this CTA's scratch (in L2) and finished from there beside the
       // next tile's MMAs; each thread reads back what it wrote itself.  Nothing follows the last tile, so it is
       // finished from tensor memory, by the dequantisers too; and so is every tile while K is short (share_tiles:
-      // the next tile's stages then take less time than a third of the work on this one's elements).
+      // the next tile's stages then take less time than the two thirds of this one's elements that they take over).
       float4 *scratch = p.scratch + (int64_t)blockIdx.x * (BN * TT / 4) + 32 * e + lane;
       for (int64_t tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
         const int64_t n_tile = tile / m_tiles, m_tile = tile - n_tile * m_tiles;

@@ -194,9 +194,14 @@ constexpr uint32_t gemv_box_rows() { return GATED ? GATED_ROWS : 64; }
 constexpr int GATED_CTAS = 148;
 
 // Up to this K the gated GEMM's dequantisers help to finish every tile of 256 tokens (with a checkpoint, whose rounding
-// is more work, up to the larger one).  int4, M = 2048, N = 8192: K = 1024 50.7 us against 60.6, K = 2048 81 against 84, at
-// K = 4096 equal; with a checkpoint K = 1024 69.1 against 89.2, K = 4096 161 against 170 (int6: 189 against 188).
-constexpr int64_t GATED_SHARE_K = 2048, GATED_SHARE_K_SAVED = 4096;
+// is more work, up to the larger one).  M = 2048, us with their help and without:
+//                            int4            int6           4-bit          8-bit         int4, N = 27648  8-bit, N = 27648
+//   N = 8192      K = 1024   50.5 |  59.2    53.3 |  59.5   57.1 |  60.8   60.4 |  62.8   150 | 190        180 | 184
+//                 K = 2048   84.8 |  83.8    95.0 |  91.5   93.6 |  89.1   101  |  96.5   259 | 254        313 | 294
+//   checkpoint    K = 1024   69.8 |  86.7    71.9 |  85.5   75.7 |  87.0   78.8 |  89.7   194 | 262        225 | 264
+//                 K = 2048   96.6 | 111.4   107.3 | 111.1  111.0 | 107.8  116.5 | 114.5   296 | 343        361 | 350
+//                 K = 4096  167.7 | 170.4   191.7 | 184.6  193.8 | 180.5  206.1 | 191.9   517 | 501        625 | 570
+constexpr int64_t GATED_SHARE_K = 1536, GATED_SHARE_K_SAVED = 2048;
 
 // What the gated forms of the launches take besides the layer's arguments (y is then h [M][N / 2]).
 struct GatedArgs {
@@ -259,6 +264,9 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
   p.saved_exps = ga.saved_exps;
   p.scratch = reinterpret_cast<float4 *>(static_cast<uint8_t *>(workspace) + gemm_workspace_bytes(M, N, K));
   p.share_tiles = GATED && K <= (ga.saved ? GATED_SHARE_K_SAVED : GATED_SHARE_K);
+  // a dequantiser that waits for its last tile's accumulator alone finds the one before it over only if it has waited
+  // for a stage of that tile, so unshared tiles have at least a ring of stages
+  static_assert(GATED_SHARE_K >= stages(FMT, BITS, gemm::BM) * BK, "short tiles are shared");
   const int smem = smem_bytes(FMT, BITS, TT);
   auto kern = gemm_kernel<FMT, BITS, TT, CPS, GATED>;
   static thread_local int configured_dev = -1;  // per (kernel instantiation, thread)
