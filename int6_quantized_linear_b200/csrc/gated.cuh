@@ -11,8 +11,8 @@
 // A power of two (rather than top / 127) makes the scaling exact, the exponent the only thing to
 // reduce over a group, and every restored value exact in bf16 (seven significant bits); the up to
 // one bit that it gives away is repaid by groups of 16, whose largest value is nearer the others than
-// that of a longer group.  A group of values that are not all finite (or one above 255/256 * 2^128,
-// which bf16 does not hold) gets E = 255 and is restored as NaN.
+// that of a longer group.  A group of values that are not all finite, or with one of at least
+// 255/256 * 2^128 (bf16's largest, which would round to 2^128), gets E = 255 and is restored as NaN.
 #pragma once
 #include "formats.cuh"
 
@@ -23,8 +23,8 @@ enum : int { ACT_SILU = 0, ACT_GELU_TANH = 1, ACT_GELU = 2 };
 constexpr float GELU_C = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float GELU_B = 0.044715f;
 
-// act(g) and act'(g).  exp and the reciprocal are the fast forms (a few 2^-23 off); the results are
-// rounded to bf16 or to an fp16 operand.
+// act(g) and act'(g).  exp and the reciprocal are the fast forms (a few 2^-23 off, the exponential |z| / 2^23 more
+// for an argument z; a sigmoid below 2^-126 is 0); the results are rounded to bf16 or to an fp16 operand.
 QL_DEVI float sigmoid_fast(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 QL_DEVI float act_value(int act, float g) {
