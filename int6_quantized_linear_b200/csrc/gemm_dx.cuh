@@ -27,8 +27,8 @@
 // Passes: (1) row exponents b_n; (2) dy to scaled fp16 rows; (3) the scaled group metadata, transposed so that a
 // stage's words are one TMA box; (4) the GEMM; (5) the sum of the parts of split tiles.
 //
-// One or two CTAs an SM (ctas_per_sm).  The tiles of whole waves (as many tiles as CTAs, again and again) are computed alone, all
-// CTAs moving along n together so that each code row and each dy column is fetched from memory about once
+// One or two CTAs an SM (ctas_per_sm).  The tiles of whole waves (as many tiles as CTAs, again and again) are computed
+// alone, all CTAs moving along n together so that each code row and each dy column is fetched from memory about once
 // a wave; the tiles of the last, partial wave are cut along n into equal shares, one a CTA, whose fp32 sums
 // go to the workspace and are added in a fixed order (a full last wave costs as much as the others however
 // few tiles it has: at M = 2048, K = 5120 it would be a third wave for 24 of 148 CTAs).
@@ -56,8 +56,8 @@ constexpr int MIN_SHARE = 8;       // stages a share of a split tile has at leas
 // have, a multiple of 16 (the MMA's N) that spreads M evenly.
 constexpr int TT_LARGE = 256, TT_MEDIUM = 64, TT_SMALL = 32;
 // CTAs an SM: a CTA's chain of copy, decoding, MMA and release takes more than 500 cycles a stage, and up to 64
-// tokens the MMAs themselves take 230 to 250, so two CTAs share the tensor core (int4, K = 5120, N = 27648, M = 4: 38.1
-// us a call against 46.7, M = 64: 45.9 against 49.7; int6, K = 4096, N = 8192, M = 12: 23.0 against 22.7; with tiles of
+// tokens the MMAs themselves take 230 to 250, so two CTAs share the tensor core (int4, K = 5120, N = 27648, M = 4: 40.4
+// us a call against 47.7, M = 64: 45.5 against 54.4; int6, K = 4096, N = 8192, M = 12: 23.7 against 24.2; with tiles of
 // 128 tokens one CTA was faster, 67.2 against 75.2 at M = 128).
 __host__ __device__ constexpr int ctas_per_sm(int tt) { return tt == TT_LARGE ? 1 : 2; }
 inline int tile_class(int64_t M) { return M <= TT_SMALL ? TT_SMALL : M <= TT_MEDIUM ? TT_MEDIUM : TT_LARGE; }

@@ -296,8 +296,8 @@ ql_status launch_gemm_tt(const ql_desc *d, const ql_packed_const *w, const void 
 // taking two in turn); from 33 tokens: tiles of 256 tokens.  Both take 128 weight rows as the MMA's
 // M = 128 operand.  The gated block also takes tiles of 32 tokens for more of them while those tiles fit the SMs
 // at once: a narrow block (few features) is then spread over up to eight times as many CTAs (int4, M = 696, N = 138,
-// K = 4096: 24.2 us against 31.4; int6, M = 3484, N = 40, K = 9472: 74.6 against 97.0; int4, M = 256, N = 1024, K = 512:
-// 9.0 against 11.7).
+// K = 4096: 25.1 us against 31.5; int6, M = 3484, N = 40, K = 9472: 76.9 against 91.3; int4, M = 256, N = 1024, K = 512:
+// 9.3 against 11.7).
 template <int FMT, int BITS, bool GATED = false>
 ql_status launch_gemm(const ql_desc *d, const ql_packed_const *w, const void *x, int64_t M, const void *bias,
                       void *y, void *workspace, cudaStream_t st, int sms, const GatedArgs &ga = {}) {
