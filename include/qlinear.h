@@ -475,7 +475,8 @@ ql_status qlinear_gemm_dx_workspace_bytes(const ql_desc *desc, int64_t M, size_t
  * M >= 1 and every N and K of the format.  On the tcgen05 tensor cores, the
  * dequantisation fused: each dy row is scaled to fp16 against the power-of-two
  * scales that the weight rows get, one rounding an element; the weights are
- * those of qlinear_gated's GEMM form; fp32 accumulation, one rounding to bf16.
+ * those of qlinear_gated's GEMM form (affine ones below 2^126 in magnitude);
+ * fp32 accumulation, one rounding to bf16.
  * A column of dx depends on that column of W alone, so what a group keeps that
  * lies far below its row's largest is what its columns have where it does so in
  * every row.  Results do not depend on timing (split sums are added in a fixed
